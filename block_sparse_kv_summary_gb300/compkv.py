@@ -40,6 +40,17 @@ class compkv_buffers(ctypes.Structure):
                 ("scratch_bytes", c_size_t)]
 
 
+# element types (include/compkv.h)
+COMPKV_BF16 = 0
+COMPKV_F32 = 1
+
+
+class compkv_rope_args(ctypes.Structure):
+    _fields_ = [("qkv", c_void_p), ("qkv_type", c_int), ("qkv_stride", c_int64), ("table", c_void_p),
+                ("table_rows", c_int), ("rot_dim", c_int), ("interleaved", c_int), ("q_weight", c_void_p),
+                ("k_weight", c_void_p), ("eps", ctypes.c_float), ("positions", c_void_p), ("q_type", c_int)]
+
+
 class CompKVError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {message}")
@@ -62,6 +73,15 @@ _SIGNATURES = [
     ("compkv_decode_host", c_int, [c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
     ("compkv_decode_static", c_int, [POINTER(compkv_config), POINTER(compkv_buffers), c_int, c_void_p, c_void_p,
                                      c_void_p, c_void_p, c_void_p, c_void_p]),
+    ("compkv_rope", c_int, [c_void_p, c_int, POINTER(compkv_rope_args), c_void_p, c_void_p, c_void_p, c_void_p]),
+    ("compkv_prefill_qkv", c_int, [c_void_p, c_int, POINTER(compkv_rope_args), POINTER(c_int), POINTER(c_int),
+                                   c_void_p, c_void_p]),
+    ("compkv_fork", c_int, [c_void_p, c_int, c_int, c_int, POINTER(c_int), POINTER(c_int), POINTER(c_int), c_void_p]),
+    ("compkv_compact", c_int, [c_void_p, c_int, c_int, c_int, POINTER(c_int), POINTER(c_int), c_void_p, c_int,
+                               c_void_p]),
+    ("compkv_attend_shared_bytes", c_size_t, [POINTER(compkv_config)]),
+    ("compkv_attend_shared", c_int, [c_void_p, c_int, c_void_p, c_int, POINTER(c_int), POINTER(c_int), c_void_p,
+                                     c_void_p, c_size_t, c_void_p]),
     ("compkv_device_status", c_int, [c_void_p, c_void_p]),
     ("compkv_launch_count", c_int64, [c_void_p]),
     ("compkv_selftest_wait_timeout", c_int, [c_void_p, c_void_p]),
@@ -194,6 +214,42 @@ def compkv_decode_static(cfg, bufs, layer, q, k_new, v_new, out, sel, stream):
                                       stream), "compkv_decode_static")
 
 
+def _ints(x):
+    return None if x is None else (c_int * len(x))(*x)
+
+
+def compkv_rope(ctx, layer, args, q, k_new, v_new, stream):
+    """Norms and rotation of one token per sequence; args: a compkv_rope_args."""
+    _check(lib().compkv_rope(ctx, layer, ctypes.byref(args), q, k_new, v_new, stream), "compkv_rope")
+
+
+def compkv_prefill_qkv(ctx, layer, args, starts, counts, q, stream):
+    """Norms and rotation of packed tokens, written into the cache with their summaries."""
+    _check(lib().compkv_prefill_qkv(ctx, layer, ctypes.byref(args), _ints(starts), _ints(counts), q, stream),
+           "compkv_prefill_qkv")
+
+
+def compkv_fork(ctx, layer0, layers, src, dst, lens, stream):
+    """Copy sequences src[i] to dst[i] (or cut them in place); lens None: whole."""
+    _check(lib().compkv_fork(ctx, layer0, layers, len(src), _ints(src), _ints(dst), _ints(lens), stream),
+           "compkv_fork")
+
+
+def compkv_compact(ctx, layer0, layers, src, dst, keep, keep_blocks, stream):
+    """Move the listed blocks of src[i] to the front of dst[i]; keep: device address."""
+    _check(lib().compkv_compact(ctx, layer0, layers, len(src), _ints(src), _ints(dst), keep, keep_blocks, stream),
+           "compkv_compact")
+
+
+def compkv_attend_shared_bytes(cfg: compkv_config) -> int:
+    return lib().compkv_attend_shared_bytes(ctypes.byref(cfg))
+
+
+def compkv_attend_shared(ctx, layer, q, type, prefix_seq, prefix_len, out, workspace, workspace_bytes, stream):
+    _check(lib().compkv_attend_shared(ctx, layer, q, type, _ints(prefix_seq), _ints(prefix_len), out, workspace,
+                                      workspace_bytes, stream), "compkv_attend_shared")
+
+
 def compkv_device_status(ctx, stream) -> int:
     """Synchronise, read and clear the device status word; returns the status code."""
     return lib().compkv_device_status(ctx, stream)
@@ -209,7 +265,8 @@ def compkv_launch_count(ctx) -> int:
 
 
 KERNEL_FAMILIES = {"prefill": 0, "append": 1, "score": 2, "attend": 4, "decode": 5,
-                   "k_stream": 6, "k_post": 7}
+                   "k_stream": 6, "k_post": 7, "rope": 8, "prefill_qkv": 9, "fork": 10, "compact": 11,
+                   "attend_shared": 12}
 
 
 def compkv_profile_enable(ctx, enable):

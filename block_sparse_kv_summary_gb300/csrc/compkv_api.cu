@@ -389,6 +389,111 @@ compkv_status launch_chain(compkv_ctx* c, int family, const LayerArgs& a, int mo
   return r;
 }
 
+// The arguments common to compkv_rope and compkv_prefill_qkv, checked.
+compkv_status rope_base(const compkv_ctx* c, int layer, const compkv_rope_args* r, const void* q, RopeArgs* out) {
+  COMPKV_TRY(check_call(c, layer));
+  if (!r) return fail(COMPKV_ERR_INVALID_ARG, "rope arguments are NULL");
+  const int d = c->cfg.head_dim, Hkv = c->cfg.num_kv_heads, Hq = Hkv * c->cfg.group_size;
+  if (r->qkv_type != COMPKV_BF16 && r->qkv_type != COMPKV_F32)
+    return fail(COMPKV_ERR_INVALID_ARG, "qkv_type must be COMPKV_BF16 or COMPKV_F32 (got %d)", r->qkv_type);
+  if (r->q_type != COMPKV_BF16 && r->q_type != COMPKV_F32)
+    return fail(COMPKV_ERR_INVALID_ARG, "q_type must be COMPKV_BF16 or COMPKV_F32 (got %d)", r->q_type);
+  COMPKV_TRY(check_ptr(r->qkv, "qkv", 16));
+  COMPKV_TRY(check_ptr(q, "q", 16));
+  COMPKV_TRY(check_ptr(r->table, "table", 16));
+  if (r->q_weight) COMPKV_TRY(check_ptr(r->q_weight, "q_weight", 16));
+  if (r->k_weight) COMPKV_TRY(check_ptr(r->k_weight, "k_weight", 16));
+  if (r->positions) COMPKV_TRY(check_ptr(r->positions, "positions", 4));
+  const int64_t width = (int64_t)(Hq + 2 * Hkv) * d, per16 = r->qkv_type == COMPKV_BF16 ? 8 : 4;
+  if (r->qkv_stride < width || r->qkv_stride % per16)
+    return fail(COMPKV_ERR_INVALID_ARG, "qkv_stride must be at least %lld elements and a multiple of 16 bytes (got %lld)",
+                (long long)width, (long long)r->qkv_stride);
+  if (r->rot_dim < 16 || r->rot_dim > d || r->rot_dim % 16)
+    return fail(COMPKV_ERR_UNSUPPORTED_SHAPE, "rot_dim must be a multiple of 16 in 16..%d (got %d)", d, r->rot_dim);
+  if (r->table_rows < 1) return fail(COMPKV_ERR_INVALID_ARG, "table_rows must be >= 1 (got %d)", r->table_rows);
+  if (!(r->eps >= 0.f)) return fail(COMPKV_ERR_INVALID_ARG, "eps must be >= 0");
+  if (r->interleaved != 0 && r->interleaved != 1)
+    return fail(COMPKV_ERR_INVALID_ARG, "interleaved must be 0 or 1 (got %d)", r->interleaved);
+  RopeArgs a;
+  memset(&a, 0, sizeof(a));
+  const LayerArgs b = base_args(c, layer);
+  a.qkv = r->qkv;
+  a.stride = r->qkv_stride;
+  a.table = r->table;
+  a.q_weight = r->q_weight;
+  a.k_weight = r->k_weight;
+  a.positions = r->positions;
+  a.seq_len = b.seq_len;
+  a.status = b.status;
+  a.q = const_cast<void*>(q);
+  a.k = b.k;
+  a.v = b.v;
+  a.kbar = b.kbar;
+  a.vbar = b.vbar;
+  a.dbar = b.dbar;
+  a.eps = r->eps;
+  a.in_f32 = r->qkv_type == COMPKV_F32;
+  a.q_bf16 = r->q_type == COMPKV_BF16;
+  a.interleaved = r->interleaved;
+  a.table_rows = r->table_rows;
+  a.rot = r->rot_dim;
+  a.B = c->cfg.batch;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.r = c->cfg.r;
+  for (int s = 0; s < a.B; ++s) {
+    a.seq_row0[s] = c->lay.seq_row0[s];
+    a.cap_blocks[s] = c->lay.cap_blocks[s];
+  }
+  *out = a;
+  return COMPKV_OK;
+}
+
+// The arguments common to compkv_fork and compkv_compact, checked: pairs of
+// sequences whose destinations take part in no other pair.
+compkv_status page_base(const compkv_ctx* c, int layer0, int layers, int n, const int* src, const int* dst,
+                        PageArgs* out) {
+  if (!c) return fail(COMPKV_ERR_INVALID_ARG, "context is NULL");
+  if (layer0 < 0 || layers < 1 || layer0 > c->cfg.num_layers - layers)
+    return fail(COMPKV_ERR_INVALID_ARG, "layers [%d, %d + %d) outside [0, %d)", layer0, layer0, layers, c->cfg.num_layers);
+  if (n < 1 || n > c->cfg.batch) return fail(COMPKV_ERR_INVALID_ARG, "pairs must be in 1..%d (got %d)", c->cfg.batch, n);
+  if (!src || !dst) return fail(COMPKV_ERR_INVALID_ARG, "src and dst must not be NULL");
+  int reads[kMaxBatch] = {}, writes[kMaxBatch] = {};
+  for (int i = 0; i < n; ++i) {
+    if (src[i] < 0 || src[i] >= c->cfg.batch || dst[i] < 0 || dst[i] >= c->cfg.batch)
+      return fail(COMPKV_ERR_INVALID_ARG, "pair %d: sequences %d -> %d outside [0, %d)", i, src[i], dst[i], c->cfg.batch);
+    ++reads[src[i]];
+    ++writes[dst[i]];
+  }
+  for (int i = 0; i < n; ++i)
+    if (writes[dst[i]] > 1 || reads[dst[i]] > (src[i] == dst[i] ? 1 : 0))
+      return fail(COMPKV_ERR_INVALID_ARG, "pair %d: sequence %d is written and takes part in another pair", i, dst[i]);
+  PageArgs a;
+  memset(&a, 0, sizeof(a));
+  a.k = reinterpret_cast<__nv_bfloat16*>(c->buf.k);
+  a.v = reinterpret_cast<__nv_bfloat16*>(c->buf.v);
+  a.kbar = c->buf.kbar;
+  a.vbar = c->buf.vbar;
+  a.dbar = c->buf.dbar;
+  a.seq_len = c->buf.seq_len;
+  a.status = reinterpret_cast<int*>(reinterpret_cast<char*>(c->buf.scratch) + c->lay.off_status);
+  a.rows_per_layer = c->lay.rows_per_layer;
+  a.layer0 = layer0;
+  a.layers = layers;
+  a.n = n;
+  a.B = c->cfg.batch;
+  a.Hkv = c->cfg.num_kv_heads;
+  a.d = c->cfg.head_dim;
+  a.r = c->cfg.r;
+  for (int s = 0; s < a.B; ++s) {
+    a.seq_row0[s] = c->lay.seq_row0[s];
+    a.cap_blocks[s] = c->lay.cap_blocks[s];
+  }
+  *out = a;
+  return COMPKV_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -588,6 +693,162 @@ compkv_status compkv_decode_host(compkv_ctx* c, int layer, const float* q_host, 
   }
   COMPKV_TRY(cuda_status(cudaStreamSynchronize(st), "stream synchronize"));
   return COMPKV_OK;
+}
+
+compkv_status compkv_rope(compkv_ctx* c, int layer, const compkv_rope_args* args, void* q, void* k_new, void* v_new,
+                          void* stream) {
+  RopeArgs a;
+  COMPKV_TRY(rope_base(c, layer, args, q, &a));
+  COMPKV_TRY(check_ptr(k_new, "k_new", 16));
+  COMPKV_TRY(check_ptr(v_new, "v_new", 16));
+  a.k_new = reinterpret_cast<__nv_bfloat16*>(k_new);
+  a.v_new = reinterpret_cast<__nv_bfloat16*>(v_new);
+  cudaStream_t st = (cudaStream_t)stream;
+  return launch(c, COMPKV_KERNEL_ROPE, st, "rope launch", [&] { return launch_rope_step(a, st); });
+}
+
+compkv_status compkv_prefill_qkv(compkv_ctx* c, int layer, const compkv_rope_args* args, const int* starts,
+                                 const int* counts, void* q, void* stream) {
+  RopeArgs a;
+  COMPKV_TRY(rope_base(c, layer, args, q, &a));
+  if (!counts) return fail(COMPKV_ERR_INVALID_ARG, "counts is NULL");
+  int64_t tokens = 0, blocks = 0;
+  for (int s = 0; s < a.B; ++s) {
+    const int start = starts ? starts[s] : 0, count = counts[s], cap = a.cap_blocks[s] * kBlock;
+    if (count < 0) return fail(COMPKV_ERR_INVALID_ARG, "counts[%d] = %d is negative", s, count);
+    a.token0[s] = (int)tokens;
+    a.item0[s] = (int)blocks;
+    if (!count) continue;
+    if (start < 0) return fail(COMPKV_ERR_INVALID_ARG, "starts[%d] = %d is negative", s, start);
+    if (start > cap || count > cap - start)
+      return fail(COMPKV_ERR_CAPACITY, "tokens [%d, %d + %d) of sequence %d exceed its capacity %d", start, start, count, s, cap);
+    a.starts[s] = start;
+    a.counts[s] = count;
+    tokens += count;
+    blocks += (start + count - 1) / kBlock - start / kBlock + 1;
+    if (tokens > 0x7fffffff) return fail(COMPKV_ERR_UNSUPPORTED_SHAPE, "more than 2^31 - 1 tokens in one call");
+  }
+  a.item0[a.B] = (int)blocks;
+  if (!blocks) return COMPKV_OK;
+  cudaStream_t st = (cudaStream_t)stream;
+  return launch(c, COMPKV_KERNEL_PREFILL_QKV, st, "prefill launch", [&] { return launch_rope_prefill(a, st); });
+}
+
+compkv_status compkv_fork(compkv_ctx* c, int layer0, int layers, int n, const int* src, const int* dst, const int* lens,
+                          void* stream) {
+  PageArgs a;
+  COMPKV_TRY(page_base(c, layer0, layers, n, src, dst, &a));
+  for (int i = 0; lens && i < n; ++i) {
+    if (lens[i] < -1) return fail(COMPKV_ERR_INVALID_ARG, "lens[%d] = %d is below -1", i, lens[i]);
+    for (int s : {src[i], dst[i]})
+      if (lens[i] > a.cap_blocks[s] * kBlock)
+        return fail(COMPKV_ERR_CAPACITY, "lens[%d] = %d exceeds the capacity %d of sequence %d", i, lens[i],
+                    a.cap_blocks[s] * kBlock, s);
+  }
+  // pairs with one source stand together: its tokens are then read once from DRAM
+  int at = 0;
+  int64_t items = 0;
+  for (int s = 0; s < a.B; ++s) {
+    const int first = at;
+    int most = 0;
+    for (int i = 0; i < n; ++i) {
+      if (src[i] != s) continue;
+      a.src[at] = s;
+      a.dst[at] = dst[i];
+      a.lens[at] = lens ? lens[i] : -1;
+      const int blocks = a.lens[at] < 0 ? a.cap_blocks[s] : (a.lens[at] + kBlock - 1) / kBlock;
+      if (dst[i] != s && blocks > most) most = blocks;
+      ++at;
+    }
+    if (at == first) continue;
+    a.pair0[a.groups] = first;
+    a.item0[a.groups] = items;
+    ++a.groups;
+    items += (int64_t)layers * a.Hkv * fork_chunks(most);
+  }
+  a.pair0[a.groups] = n;
+  a.item0[a.groups] = items;
+  if (items > 0x7fffffff) return fail(COMPKV_ERR_UNSUPPORTED_SHAPE, "the copies need more than 2^31 - 1 work items");
+  cudaStream_t st = (cudaStream_t)stream;
+  return launch(c, COMPKV_KERNEL_FORK, st, "fork launch", [&] { return launch_fork(a, st); });
+}
+
+compkv_status compkv_compact(compkv_ctx* c, int layer0, int layers, int n, const int* src, const int* dst,
+                             const int* keep, int keep_blocks, void* stream) {
+  PageArgs a;
+  COMPKV_TRY(page_base(c, layer0, layers, n, src, dst, &a));
+  COMPKV_TRY(check_ptr(keep, "keep", 4));
+  if (keep_blocks < 1 || keep_blocks > c->lay.max_cap_blocks)
+    return fail(COMPKV_ERR_INVALID_ARG, "keep_blocks must be in 1..%d (got %d)", c->lay.max_cap_blocks, keep_blocks);
+  a.keep = keep;
+  a.keep_blocks = keep_blocks;
+  int in = 0;
+  for (int i = 0; i < n; ++i) {
+    a.src[i] = src[i];
+    a.dst[i] = dst[i];
+    in += src[i] == dst[i];
+  }
+  // the verdicts of the lists stand in the scratch that the decode step's compensation sums use
+  char* sc = reinterpret_cast<char*>(c->buf.scratch);
+  a.verdict = reinterpret_cast<int2*>(sc + c->lay.off_comp);
+  const int64_t room = (int64_t)((c->lay.off_zs - c->lay.off_comp) / sizeof(int2));
+  if ((int64_t)layers * n > room)
+    return fail(COMPKV_ERR_UNSUPPORTED_SHAPE, "%d layers x %d pairs in one call; at most %lld", layers, n, (long long)room);
+  cudaStream_t st = (cudaStream_t)stream;
+  return launch(c, COMPKV_KERNEL_COMPACT, st, "compact launch", [&] { return launch_compact(a, st); },
+                1 + (in > 0) + (in < n));
+}
+
+size_t compkv_attend_shared_bytes(const compkv_config* cfg) {
+  Layout L;
+  if (make_layout(cfg, &L) != COMPKV_OK) return 0;
+  return shared_workspace_bytes(cfg->batch, cfg->num_kv_heads, cfg->group_size, cfg->head_dim);
+}
+
+compkv_status compkv_attend_shared(compkv_ctx* c, int layer, const void* q, int type, const int* prefix_seq,
+                                   const int* prefix_len, void* out, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  COMPKV_TRY(check_call(c, layer));
+  COMPKV_TRY(check_ptr(q, "q", 16));
+  COMPKV_TRY(check_ptr(out, "out", 16));
+  COMPKV_TRY(check_ptr(workspace, "workspace", 256));
+  if (type != COMPKV_BF16 && type != COMPKV_F32)
+    return fail(COMPKV_ERR_INVALID_ARG, "type must be COMPKV_BF16 or COMPKV_F32 (got %d)", type);
+  if (!prefix_seq || !prefix_len) return fail(COMPKV_ERR_INVALID_ARG, "prefix_seq and prefix_len must not be NULL");
+  if (c->kv_host) return fail(COMPKV_ERR_UNSUPPORTED_SHAPE, "compkv_attend_shared needs k and v in device memory");
+  SharedArgs a;
+  memset(&a, 0, sizeof(a));
+  const LayerArgs b = base_args(c, layer);
+  a.k = b.k;
+  a.v = b.v;
+  a.seq_len = b.seq_len;
+  a.q = q;
+  a.out = out;
+  a.ws = reinterpret_cast<float*>(workspace);
+  a.status = b.status;
+  a.q_bf16 = type == COMPKV_BF16;
+  a.B = c->cfg.batch;
+  a.Hkv = c->cfg.num_kv_heads;
+  a.G = c->cfg.group_size;
+  a.d = c->cfg.head_dim;
+  const size_t need = shared_workspace_bytes(a.B, a.Hkv, a.G, a.d);
+  if (workspace_bytes < need)
+    return fail(COMPKV_ERR_INVALID_ARG, "workspace_bytes %zu < required %zu", workspace_bytes, need);
+  for (int s = 0; s < a.B; ++s) {
+    const int p = prefix_seq[s];
+    if (p < -2 || p >= a.B) return fail(COMPKV_ERR_INVALID_ARG, "prefix_seq[%d] = %d not in -2..%d", s, p, a.B - 1);
+    a.seq_row0[s] = c->lay.seq_row0[s];
+    a.cap_blocks[s] = c->lay.cap_blocks[s];
+    a.prefix_seq[s] = p;
+    if (p < 0) continue;
+    if (prefix_len[p] < 0 || prefix_len[p] > c->lay.cap_blocks[p] * kBlock)
+      return fail(COMPKV_ERR_CAPACITY, "prefix_len[%d] = %d outside [0, %d]", p, prefix_len[p],
+                  c->lay.cap_blocks[p] * kBlock);
+    a.prefix_len[p] = prefix_len[p];
+  }
+  cudaStream_t st = (cudaStream_t)stream;
+  return launch(c, COMPKV_KERNEL_ATTEND_SHARED, st, "shared attention launch",
+                [&] { return launch_attend_shared(a, st); }, 2);
 }
 
 compkv_status compkv_device_status(compkv_ctx* c, void* stream) {

@@ -20,6 +20,7 @@ constexpr int kMaxC = 16;         // CTAs of one unit's cluster in the post kern
 // Device status word codes (mirrors compkv_status).
 enum DevErr : int {
   kDevOk = 0,
+  kDevInvalidArg = 1,
   kDevCapacity = 3,
   kDevTimeout = 5,
   kDevBadSelection = 6,
@@ -83,6 +84,79 @@ struct LayerArgs {
   int64_t seq_row0[kMaxBatch];   // first row of (s, head 0) relative to the layer
   int cap_blocks[kMaxBatch];     // capacity of sequence s in blocks
   int lens[kMaxBatch];           // prefill lengths (compkv_prefill only)
+};
+
+// Arguments of the kernels that norm and rotate the projection's heads.
+struct RopeArgs {
+  const void* qkv;             // [tokens] rows of (Hq + 2 Hkv) d bf16 or fp32, `stride` elements apart
+  int64_t stride;
+  const float* table;          // [table_rows][rot]: cos of rot/2 angles, then their sin
+  const float* q_weight;       // [d] or null (no norm)
+  const float* k_weight;
+  const int* positions;        // [tokens] or null
+  int* seq_len;                // [B] of this layer
+  int* status;
+  void* q;                     // [tokens][Hq][d] bf16 or fp32
+  __nv_bfloat16* k_new;        // one token per sequence: [B][Hkv][d]
+  __nv_bfloat16* v_new;
+  __nv_bfloat16* k;            // many tokens: the cache of this layer
+  __nv_bfloat16* v;
+  float* kbar;
+  float* vbar;
+  float* dbar;
+  float eps;
+  int in_f32, q_bf16, interleaved;
+  int table_rows, rot;
+  int B, Hq, Hkv, d, r;
+  // per sequence, for many tokens
+  int64_t seq_row0[kMaxBatch];
+  int cap_blocks[kMaxBatch];
+  int starts[kMaxBatch];       // slot of its first token
+  int counts[kMaxBatch];       // its tokens
+  int token0[kMaxBatch];       // its first token in qkv
+  int item0[kMaxBatch + 1];    // cache blocks that receive tokens, before sequence s
+};
+
+// Arguments of the kernels that copy and compact pages (16-token blocks).
+struct PageArgs {
+  __nv_bfloat16* k;            // the cache from its first row on (all layers)
+  __nv_bfloat16* v;
+  float* kbar;
+  float* vbar;
+  float* dbar;
+  int* seq_len;                // [num_layers][B]
+  int* status;
+  int2* verdict;               // compaction: [layers][n] kept blocks (-1: refused) and tokens
+  const int* keep;             // compaction: [layers][n][Hkv][keep_blocks]
+  int keep_blocks;
+  int64_t rows_per_layer;
+  int layer0, layers, n;       // n pairs
+  int B, Hkv, d, r;
+  int groups;                  // copies: pairs with one source stand together and make a group
+  int64_t seq_row0[kMaxBatch];
+  int cap_blocks[kMaxBatch];
+  int src[kMaxBatch];          // per pair
+  int dst[kMaxBatch];
+  int lens[kMaxBatch];         // tokens to copy; -1: all that the source holds
+  int pair0[kMaxBatch + 1];    // copies: first pair of a group
+  int64_t item0[kMaxBatch + 1];  // work items of the groups (copies) or pairs (compaction) before this one
+};
+
+// Arguments of the attention over a shared prefix and the sequences' own tokens.
+struct SharedArgs {
+  const __nv_bfloat16* k;      // the cache of this layer
+  const __nv_bfloat16* v;
+  const int* seq_len;          // [B] of this layer
+  const void* q;               // [B][Hq][d] fp32, or bf16 where q_bf16
+  void* out;                   // the same type
+  float* ws;                   // workspace
+  int* status;
+  int q_bf16;
+  int B, Hkv, G, d;
+  int64_t seq_row0[kMaxBatch];
+  int cap_blocks[kMaxBatch];
+  int prefix_seq[kMaxBatch];   // the sequence that holds the prefix, -1: none, -2: takes no part
+  int prefix_len[kMaxBatch];   // of a holder: tokens of its prefix
 };
 
 __host__ __device__ inline int pad_g(int G) { return G < 4 ? 4 : G; }

@@ -27,6 +27,17 @@ cudaError_t launch_append(const LayerArgs& a, cudaStream_t st);
 // kernel; the sources may be page-locked host memory.
 cudaError_t launch_stage_in(void* d0, const void* s0, size_t b0, void* d1, const void* s1, size_t b1, void* d2,
                             const void* s2, size_t b2, cudaStream_t st);
+// Norms and rotation of the projection's heads: one token per sequence, or many into the cache.
+cudaError_t launch_rope_step(const RopeArgs& a, cudaStream_t st);
+cudaError_t launch_rope_prefill(const RopeArgs& a, cudaStream_t st);
+// Pages: copies between sequences, and listed blocks to the front of a sequence.
+constexpr int kForkBlocks = 16;  // blocks of one work item of a copy
+inline int fork_chunks(int blocks) { return blocks < 1 ? 1 : (blocks + kForkBlocks - 1) / kForkBlocks; }
+cudaError_t launch_fork(const PageArgs& a, cudaStream_t st);
+cudaError_t launch_compact(const PageArgs& a, cudaStream_t st);
+// Attention over a shared prefix and the sequences' own tokens.
+size_t shared_workspace_bytes(int B, int Hkv, int G, int d);
+cudaError_t launch_attend_shared(const SharedArgs& a, cudaStream_t st);
 // One bounded mbarrier wait that runs out and records kDevTimeout in `status`.
 cudaError_t launch_wait_selftest(int* status, cudaStream_t st);
 

@@ -1,0 +1,296 @@
+// Pages of the cache: the tokens and summaries of a sequence copied to other
+// sequences (or cut short in place), and listed blocks moved to the front of
+// a sequence.  One row of the cache is one 16-token block of a (layer,
+// sequence, head), so a sequence's blocks of one head are one contiguous run
+// in each of the five arrays.
+#include "block_summary.cuh"
+#include "compkv_launch.h"
+
+namespace compkv {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ int64_t first_row(const PageArgs& a, int layer, int s, int h) {
+  return a.rows_per_layer * layer + a.seq_row0[s] + (int64_t)h * a.cap_blocks[s];
+}
+
+// Copies `chunks` 16-byte chunks, kThreads threads, four loads in flight each.
+__device__ __forceinline__ void copy16(void* dst, const void* src, int chunks) {
+  uint4* d = reinterpret_cast<uint4*>(dst);
+  const uint4* s = reinterpret_cast<const uint4*>(src);
+  for (int i = threadIdx.x; i < chunks; i += 4 * kThreads) {
+    uint4 t[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + u * kThreads < chunks) t[u] = s[i + u * kThreads];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + u * kThreads < chunks) d[i + u * kThreads] = t[u];
+  }
+}
+__device__ __forceinline__ void copy4(float* dst, const float* src, int n) {
+  for (int i = threadIdx.x; i < n; i += kThreads) dst[i] = src[i];
+}
+
+// Tokens that pair i of this layer copies; -1 when it is refused.
+__device__ __forceinline__ int pair_len(const PageArgs& a, int layer, int i, int held, bool report) {
+  const int len = a.lens[i] < 0 ? held : a.lens[i];
+  if (len > held || len > a.cap_blocks[a.dst[i]] * kBlock) {
+    if (report) set_error(a.status, len > held ? kDevInvalidArg : kDevCapacity, a.dst[i], -1, 3);
+    return -1;
+  }
+  return len;
+}
+
+// One CTA per (group of pairs with one source, layer, head, 16 blocks).
+template <int D>
+__global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ PageArgs a) {
+  int g = 0;
+  while (g + 1 < a.groups && a.item0[g + 1] <= (int64_t)blockIdx.x) ++g;
+  const int64_t per = (a.item0[g + 1] - a.item0[g]) / (a.layers * a.Hkv);  // chunks of a (layer, head)
+  int64_t x = (int64_t)blockIdx.x - a.item0[g];
+  const int b0 = (int)(x % per) * kForkBlocks;
+  x /= per;
+  const int h = (int)(x % a.Hkv), layer = a.layer0 + (int)(x / a.Hkv);
+  const int s = a.src[a.pair0[g]];
+  const int held = max(0, min(__ldcg(a.seq_len + (int64_t)layer * a.B + s), a.cap_blocks[s] * kBlock));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  for (int i = a.pair0[g]; i < a.pair0[g + 1]; ++i) {
+    const int to = a.dst[i];
+    if (to == s) {  // a cut in place: one CTA for all heads, the length last
+      if (h || b0) continue;
+      const int len = pair_len(a, layer, i, held, threadIdx.x == 0);
+      const int part = len % kBlock;
+      __syncthreads();  // every thread has read the length
+      if (len < 0) continue;
+      if (part && len < held)
+        for (int hh = warp; hh < a.Hkv; hh += kThreads / 32) {
+          const int64_t row = first_row(a, layer, s, hh) + len / kBlock;
+          warp_block_summary<D>(a.k + row * kBlock * D, a.v + row * kBlock * D, part, nullptr, nullptr,
+                                a.kbar + row * D, a.vbar + row * D, a.dbar + row * a.r, a.r, lane);
+        }
+      if (threadIdx.x == 0) a.seq_len[(int64_t)layer * a.B + to] = len;
+      continue;
+    }
+    const bool first = !h && !b0;
+    const int len = pair_len(a, layer, i, held, first && threadIdx.x == 0);
+    if (len < 0) continue;
+    if (first && threadIdx.x == 0) a.seq_len[(int64_t)layer * a.B + to] = len;
+    const int tokens = min(len - b0 * kBlock, kForkBlocks * kBlock);
+    if (tokens <= 0) continue;
+    const int64_t rs = first_row(a, layer, s, h) + b0, rd = first_row(a, layer, to, h) + b0;
+    copy16(a.k + rd * kBlock * D, a.k + rs * kBlock * D, tokens * D / 8);
+    copy16(a.v + rd * kBlock * D, a.v + rs * kBlock * D, tokens * D / 8);
+    // the summary of a block that this cut leaves incomplete is formed from its tokens; others are copied
+    const int part = tokens % kBlock;
+    const bool cut = part && len < held;
+    const int nb = tokens / kBlock + (part && !cut);
+    copy16(a.kbar + rd * D, a.kbar + rs * D, nb * D / 4);
+    copy16(a.vbar + rd * D, a.vbar + rs * D, nb * D / 4);
+    copy4(a.dbar + rd * a.r, a.dbar + rs * a.r, nb * a.r);
+    if (cut && warp == 0)
+      warp_block_summary<D>(a.k + (rs + nb) * kBlock * D, a.v + (rs + nb) * kBlock * D, part, nullptr, nullptr,
+                            a.kbar + (rd + nb) * D, a.vbar + (rd + nb) * D, a.dbar + (rd + nb) * a.r, a.r, lane);
+  }
+}
+
+// One CTA per (layer, pair): are the lists of all heads ascending block
+// indices of the source, equally long, padded by -1, and does the source's
+// last block stand in all of them or in none (it may hold fewer tokens)?
+// Writes the kept blocks and tokens for the kernel that moves, and the length.
+__global__ void __launch_bounds__(kThreads) compact_check_kernel(const __grid_constant__ PageArgs a) {
+  __shared__ int s_count[32], s_last[32], s_bad;
+  const int i = blockIdx.x % a.n, l = blockIdx.x / a.n, layer = a.layer0 + l;
+  const int src = a.src[i], to = a.dst[i];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int held = max(0, min(__ldcg(a.seq_len + (int64_t)layer * a.B + src), a.cap_blocks[src] * kBlock));
+  const int N = ceil_blocks(held);
+  if (threadIdx.x == 0) s_bad = 0;
+  __syncthreads();
+  for (int h = warp; h < a.Hkv; h += kThreads / 32) {
+    const int* list = a.keep + (((int64_t)l * a.n + i) * a.Hkv + h) * a.keep_blocks;
+    int count = 0, last = 0, bad = 0;
+    for (int j = lane; j < a.keep_blocks; j += 32) {
+      const int b = list[j], before = j ? list[j - 1] : -1;
+      if (b >= 0) {
+        ++count;
+        bad |= b >= N || before >= b || (j && before < 0);
+        last |= b == N - 1;
+      } else {
+        bad |= b != -1;
+      }
+    }
+    for (int o = 16; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
+    last = __any_sync(0xffffffffu, last);
+    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&s_bad, 1);
+    if (lane == 0) {
+      s_count[h] = count;
+      s_last[h] = last;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const int count = s_count[0];
+    bool bad = s_bad != 0;
+    for (int h = 1; h < a.Hkv; ++h) bad |= s_count[h] != count || s_last[h] != s_last[0];
+    const bool full = count > a.cap_blocks[to];
+    const int tokens = !count ? 0 : s_last[0] ? (count - 1) * kBlock + held - (N - 1) * kBlock : count * kBlock;
+    if (bad || full) set_error(a.status, bad ? kDevBadSelection : kDevCapacity, src, -1, 4);
+    else a.seq_len[(int64_t)layer * a.B + to] = tokens;
+    a.verdict[(int64_t)l * a.n + i] = bad || full ? make_int2(-1, 0) : make_int2(count, tokens);
+  }
+}
+
+// Out of place: one warp per (layer, pair, head, block).
+template <int D>
+__global__ void __launch_bounds__(kThreads) compact_copy_kernel(const __grid_constant__ PageArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+  const int64_t items = (int64_t)a.layers * a.n * a.Hkv * a.keep_blocks;
+  for (int64_t it = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += warps) {
+    const int j = (int)(it % a.keep_blocks);
+    int64_t x = it / a.keep_blocks;
+    const int h = (int)(x % a.Hkv);
+    x /= a.Hkv;
+    const int i = (int)(x % a.n), layer = a.layer0 + (int)(x / a.n);
+    if (a.src[i] == a.dst[i]) continue;
+    const int2 v = __ldcg(a.verdict + x);
+    if (j >= v.x) continue;
+    const int64_t rs = first_row(a, layer, a.src[i], h) + __ldg(a.keep + it), rd = first_row(a, layer, a.dst[i], h) + j;
+    const int chunks = min(v.y - j * kBlock, kBlock) * D / 8;
+    const uint4* ks = reinterpret_cast<const uint4*>(a.k + rs * kBlock * D);
+    const uint4* vs = reinterpret_cast<const uint4*>(a.v + rs * kBlock * D);
+    uint4* kd = reinterpret_cast<uint4*>(a.k + rd * kBlock * D);
+    uint4* vd = reinterpret_cast<uint4*>(a.v + rd * kBlock * D);
+    constexpr int U = kBlock * D / 8 / 32;
+    uint4 kt[U], vt[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (u * 32 + lane < chunks) {
+        kt[u] = ks[u * 32 + lane];
+        vt[u] = vs[u * 32 + lane];
+      }
+    const int e = lane * (D / 32);
+    float mk[D / 32], mv[D / 32];
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) {
+      mk[u] = a.kbar[rs * D + e + u];
+      mv[u] = a.vbar[rs * D + e + u];
+    }
+    for (int c = lane; c < a.r; c += 32) a.dbar[rd * a.r + c] = a.dbar[rs * a.r + c];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (u * 32 + lane < chunks) {
+        kd[u * 32 + lane] = kt[u];
+        vd[u * 32 + lane] = vt[u];
+      }
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) {
+      a.kbar[rd * D + e + u] = mk[u];
+      a.vbar[rd * D + e + u] = mv[u];
+    }
+  }
+}
+
+// In place.  Block j comes from keep[j] >= j, so blocks have to be moved in
+// ascending order, but the columns of a row are independent of one another: a
+// CTA takes a 512-byte column slice of one array of one (layer, pair, head)
+// and walks the list alone, kInBlocks blocks a turn (all loaded before any is
+// stored; later turns read behind what this one wrote).
+constexpr int kInBlocks = 32;
+template <int D>
+__global__ void __launch_bounds__(kThreads) compact_in_place_kernel(const __grid_constant__ PageArgs a) {
+  constexpr int KS = kBlock * D * 2 / 512;  // slices of K, as many of V, then kbar, vbar, dbar
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = blockIdx.x;
+  const int slice = (int)(x % (2 * KS + 3));
+  x /= 2 * KS + 3;
+  const int h = (int)(x % a.Hkv);
+  x /= a.Hkv;
+  const int i = (int)(x % a.n), layer = a.layer0 + (int)(x / a.n);
+  if (a.src[i] != a.dst[i]) return;
+  const int2 v = __ldcg(a.verdict + x);
+  const int* list = a.keep + (x * a.Hkv + h) * a.keep_blocks;
+  const int64_t r0 = first_row(a, layer, a.src[i], h);
+  // this lane's bytes of a row: `base + row * pitch`, `step` floats or 16-byte chunks
+  const bool tokens = slice < 2 * KS;
+  constexpr int PER = kInBlocks / (kThreads / 32);
+  if (tokens) {
+    const int col = (slice % KS) * 32 + lane;  // 16-byte chunk of the row
+    uint4* base = reinterpret_cast<uint4*>(slice < KS ? a.k : a.v) + r0 * (kBlock * D / 8) + col;
+    for (int j0 = 0; j0 < v.x; j0 += kInBlocks) {
+      uint4 t[PER];
+      bool go[PER];
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        const int j = j0 + u * (kThreads / 32) + warp;
+        const int b = j < v.x ? __ldg(list + j) : j;
+        go[u] = b > j && col < min(v.y - j * kBlock, kBlock) * D / 8;
+        if (go[u]) t[u] = base[(int64_t)b * (kBlock * D / 8)];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < PER; ++u)
+        if (go[u]) base[(int64_t)(j0 + u * (kThreads / 32) + warp) * (kBlock * D / 8)] = t[u];
+    }
+  } else {
+    const int w = slice == 2 * KS + 2 ? a.r : D;
+    float* base = (slice == 2 * KS ? a.kbar : slice == 2 * KS + 1 ? a.vbar : a.dbar) + r0 * w;
+    for (int j0 = 0; j0 < v.x; j0 += kInBlocks) {
+      float t[PER][4];
+      int b[PER];
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        const int j = j0 + u * (kThreads / 32) + warp;
+        b[u] = j < v.x ? __ldg(list + j) : j;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (b[u] > j && c * 32 + lane < w) t[u][c] = base[(int64_t)b[u] * w + c * 32 + lane];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        const int j = j0 + u * (kThreads / 32) + warp;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (b[u] > j && c * 32 + lane < w) base[(int64_t)j * w + c * 32 + lane] = t[u][c];
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_fork(const PageArgs& a, cudaStream_t st) {
+  const unsigned grid = (unsigned)a.item0[a.groups];
+  if (a.d == 128) fork_kernel<128><<<grid, kThreads, 0, st>>>(a);
+  else fork_kernel<64><<<grid, kThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_compact(const PageArgs& a, cudaStream_t st) {
+  compact_check_kernel<<<(unsigned)(a.layers * a.n), kThreads, 0, st>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  int in = 0;
+  for (int i = 0; i < a.n; ++i) in += a.src[i] == a.dst[i];
+  if (in < a.n) {
+    int64_t ctas = ((int64_t)a.layers * a.n * a.Hkv * a.keep_blocks + kThreads / 32 - 1) / (kThreads / 32);
+    if (ctas > 1 << 20) ctas = 1 << 20;
+    if (a.d == 128) compact_copy_kernel<128><<<(unsigned)ctas, kThreads, 0, st>>>(a);
+    else compact_copy_kernel<64><<<(unsigned)ctas, kThreads, 0, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (in) {
+    const unsigned grid = (unsigned)(a.layers * a.n * a.Hkv) * (2 * kBlock * a.d * 2 / 512 + 3);
+    if (a.d == 128) compact_in_place_kernel<128><<<grid, kThreads, 0, st>>>(a);
+    else compact_in_place_kernel<64><<<grid, kThreads, 0, st>>>(a);
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+}  // namespace compkv

@@ -237,6 +237,114 @@ compkv_status compkv_decode_static(const compkv_config *cfg, const compkv_buffer
                                    const float *q, const void *k_new, const void *v_new, float *out,
                                    int *sel, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the decode step: what a server does with the cache before and
+ * between decode steps.  The CompKV page has no counterpart to these calls.
+ * ------------------------------------------------------------------------- */
+
+/* Element types of the calls below. */
+enum { COMPKV_BF16 = 0, COMPKV_F32 = 1 };
+
+/* Norms and position rotation of a projection's heads (compkv_rope and
+ * compkv_prefill_qkv).  Per head x of d coordinates:
+ *     y = w x / sqrt(mean(x^2) + eps)      queries with q_weight, keys with k_weight;
+ *                                          y = x where the weight is NULL
+ *     (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin)
+ * for the pairs of its first rot_dim coordinates: pair i is (i, i + rot_dim/2),
+ * or (2i, 2i + 1) when `interleaved` is 1; the other coordinates stay.  cos
+ * and sin of pair i at position p are table[p][i] and table[p][rot_dim/2 + i].
+ * Values are only copied.  Queries are computed in fp32; keys to some 40 bits
+ * and rounded to bf16 once, because the summaries are those of the stored
+ * keys.  Inputs are finite, with squares that fp32 holds. */
+typedef struct {
+  const void *qkv;        /* device [tokens] rows of (Hq + 2 Hkv) d elements: the query heads,   */
+                          /* the key heads, the value heads; 16-byte aligned                     */
+  int qkv_type;           /* COMPKV_BF16 or COMPKV_F32                                           */
+  int64_t qkv_stride;     /* elements from one token's row to the next; a multiple of 16 bytes   */
+  const float *table;     /* device fp32 [table_rows][rot_dim], 16-byte aligned                  */
+  int table_rows;
+  int rot_dim;            /* a multiple of 16, 16..d                                             */
+  int interleaved;        /* 0 or 1                                                              */
+  const float *q_weight;  /* device fp32 [d], 16-byte aligned, or NULL                           */
+  const float *k_weight;
+  float eps;              /* >= 0                                                                */
+  const int *positions;   /* device int32 [tokens], or NULL: the token's index in its sequence   */
+  int q_type;             /* type of the queries that come out                                   */
+} compkv_rope_args;
+
+/* One token per sequence: the inputs of a decode step from the projection's
+ * output.  qkv holds B tokens, in the order of the sequences; without
+ * `positions` the token of sequence s stands at seq_len[layer][s], where the
+ * next decode step or append puts it.  q: device [B][Hq][d] of q_type
+ * (compkv_decode takes fp32); k_new, v_new: device bf16 [B][Hkv][d].  A
+ * position outside the table raises COMPKV_ERR_INVALID_ARG in the device
+ * status and uses the table's nearest row.  Reads the cache's lengths and
+ * changes nothing of it. */
+compkv_status compkv_rope(compkv_ctx *ctx, int layer, const compkv_rope_args *args, void *q, void *k_new,
+                          void *v_new, void *stream);
+
+/* Many tokens, packed sequence after sequence: counts[s] of sequence s (host
+ * int32 [B]; 0: none, the sequence stays as it is) go to its slots
+ * [starts[s], starts[s] + counts[s]) (host int32 [B]; NULL: from slot 0).  Keys
+ * and values are written into the cache, the summaries of every block that
+ * receives a token are formed, from the tokens that stand in it before
+ * starts[s] too, and seq_len[layer][s] becomes starts[s] + counts[s]; what the
+ * sequence held behind that is dropped.  The slots before starts[s] must hold
+ * tokens.  q: device [tokens][Hq][d] of q_type.  Without `positions` a token's
+ * position is its slot; outside the table as for compkv_rope. */
+compkv_status compkv_prefill_qkv(compkv_ctx *ctx, int layer, const compkv_rope_args *args, const int *starts,
+                                 const int *counts, void *q, void *stream);
+
+/* Copies of sequences.  For pair i < n and every layer in [layer0, layer0 +
+ * layers): the first lens[i] tokens of sequence src[i] (lens[i] = -1 or lens
+ * NULL: all that it holds) and their summaries go to sequence dst[i], whose
+ * length becomes lens[i].  src[i] == dst[i] cuts the sequence to lens[i] tokens
+ * in place (0 frees it).  The summary of a block that loses tokens is formed
+ * again from the tokens that stay; slots behind the last token are left as they
+ * were.  A source may stand in several pairs; a sequence that is written
+ * (dst[i], also where it equals src[i]) stands in one pair only.  src, dst, lens: host
+ * int32 [n], n <= B.  A source that holds fewer than lens[i] tokens
+ * (COMPKV_ERR_INVALID_ARG) or more than the destination has room for
+ * (COMPKV_ERR_CAPACITY) is reported in the device status, and that pair
+ * changes nothing in that layer.  Works in both placements of k and v. */
+compkv_status compkv_fork(compkv_ctx *ctx, int layer0, int layers, int n, const int *src, const int *dst,
+                          const int *lens, void *stream);
+
+/* Listed blocks only.  For pair i < n and every layer in [layer0, layer0 +
+ * layers): block j of every head of sequence dst[i] becomes block
+ * keep[layer - layer0][i][head][j] of sequence src[i], with its summary; in
+ * place where src[i] == dst[i].  keep: device int32 [layers][n][Hkv]
+ * [keep_blocks], ascending block indices padded with -1, the format of a
+ * selection (compkv_score_select).  All heads of a pair keep the same number
+ * of blocks, and all or none of them the source's last one, which may be
+ * incomplete; the length of dst[i] becomes the number of tokens in the kept
+ * blocks (0 where every entry is -1).  The keys keep the rotation of their old
+ * positions: give later tokens their positions explicitly.  Lists that break
+ * these rules (COMPKV_ERR_BAD_SELECTION) or exceed the destination
+ * (COMPKV_ERR_CAPACITY) are reported in the device status, and that pair
+ * changes nothing in that layer.  Sources and destinations as for compkv_fork. */
+compkv_status compkv_compact(compkv_ctx *ctx, int layer0, int layers, int n, const int *src, const int *dst,
+                             const int *keep, int keep_blocks, void *stream);
+
+/* Exact attention of every sequence over a prefix that one sequence of the
+ * batch holds for all, read once, and over its own tokens, under one softmax:
+ *     out = sum_j e^(z_j) v_j / sum_j e^(z_j),   z_j = q . k_j / sqrt(d).
+ * prefix_seq: host int32 [B].  prefix_seq[s] = p >= 0: sequence s attends to the
+ * first prefix_len[p] tokens of sequence p and to its own tokens (for s == p:
+ * those behind its prefix); -1: to its own tokens alone; -2: it takes no part
+ * and its rows of out are left as they were.  prefix_len: host int32 [B], read
+ * for the sequences that hold a prefix.  A holder with fewer tokens than
+ * prefix_len raises COMPKV_ERR_INVALID_ARG in the device status and gives those
+ * that it has.  A row with no token at all is zero.  q and out: device
+ * [B][Hq][d], both of `type`.  With COMPKV_F32 queries and softmax weights
+ * enter the products to 24 bits; with COMPKV_BF16 the weights are rounded to bf16.
+ * workspace: device memory of compkv_attend_shared_bytes(), 256-byte aligned,
+ * that no other call uses meanwhile.  k and v must be in device memory. */
+size_t compkv_attend_shared_bytes(const compkv_config *cfg);
+compkv_status compkv_attend_shared(compkv_ctx *ctx, int layer, const void *q, int type, const int *prefix_seq,
+                                   const int *prefix_len, void *out, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
 /* Synchronise `stream`, read and clear the device status word.  Returns
  * COMPKV_OK or the first device-side error since the last call. */
 compkv_status compkv_device_status(compkv_ctx *ctx, void *stream);
@@ -260,7 +368,8 @@ int64_t compkv_launch_count(const compkv_ctx *ctx);
  * summed device time in milliseconds and the number of launches since the
  * last read (then resets them).  Families COMPKV_KERNEL_PREFILL, _APPEND,
  * _SCORE, _ATTEND and _DECODE time whole API calls (compkv_prefill,
- * compkv_append, compkv_score_select, compkv_attend, compkv_decode).  A
+ * compkv_append, compkv_score_select, compkv_attend, compkv_decode), and so do
+ * _ROPE, _PREFILL_QKV, _FORK, _COMPACT and _ATTEND_SHARED.  A
  * score/select, attend or decode call launches two kernels, each timed on its
  * own (enable = 2) under COMPKV_KERNEL_K_STREAM (append, and the stream over
  * every block summary: zbar, sigma2, the logsumexp parts and the compensation
@@ -276,7 +385,12 @@ enum {
   COMPKV_KERNEL_DECODE = 5,
   COMPKV_KERNEL_K_STREAM = 6,
   COMPKV_KERNEL_K_POST = 7,
-  COMPKV_KERNEL_FAMILIES = 8
+  COMPKV_KERNEL_ROPE = 8,
+  COMPKV_KERNEL_PREFILL_QKV = 9,
+  COMPKV_KERNEL_FORK = 10,
+  COMPKV_KERNEL_COMPACT = 11,
+  COMPKV_KERNEL_ATTEND_SHARED = 12,
+  COMPKV_KERNEL_FAMILIES = 13
 };
 compkv_status compkv_profile_enable(compkv_ctx *ctx, int enable);
 
