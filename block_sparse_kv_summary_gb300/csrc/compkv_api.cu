@@ -136,6 +136,7 @@ struct compkv_ctx {
   compkv_buffers buf;
   Layout lay;
   CUtensorMap tmap_k, tmap_v;  // the whole K and V caches, for the post kernel's block copies
+  CUtensorMap tmap_k128, tmap_v128;  // the same in boxes of 128 tokens, for the attention over a shared prefix
   int tmap_ok = 0;             // the maps were built
   int kv_host = 0;             // K and V in page-locked host memory (no tensor maps)
   int64_t launches = 0;
@@ -192,7 +193,8 @@ int device_stream_ctas(int d, int r, int G) {
 }
 
 // Tensor maps of the whole K and V caches: 2-D (d, tokens) bf16, boxes of
-// 64 x 16 with the 128-byte swizzle (one 16-token block is d / 64 boxes).
+// 64 x 16 (one 16-token block is d / 64 boxes) and of 64 x 128, with the
+// 128-byte swizzle.
 compkv_status make_tensor_maps(compkv_ctx* c) {
   // where K and V live: device memory (tensor maps), or page-locked host memory that the device
   // reaches over the chip-to-chip link (plain 16-byte copies, no tensor maps)
@@ -215,6 +217,8 @@ compkv_status make_tensor_maps(compkv_ctx* c) {
   c->kv_host = host ? 1 : 0;
   memset(&c->tmap_k, 0, sizeof(c->tmap_k));
   memset(&c->tmap_v, 0, sizeof(c->tmap_v));
+  memset(&c->tmap_k128, 0, sizeof(c->tmap_k128));
+  memset(&c->tmap_v128, 0, sizeof(c->tmap_v128));
   c->tmap_ok = 0;
   if (c->kv_host) return COMPKV_OK;
   static std::atomic<void*> encode_fn{nullptr};
@@ -236,11 +240,12 @@ compkv_status make_tensor_maps(compkv_ctx* c) {
                 (unsigned long long)tokens);
   const cuuint64_t dims[2] = {(cuuint64_t)d, tokens};
   const cuuint64_t strides[1] = {(cuuint64_t)d * 2};
-  const cuuint32_t box[2] = {64, kBlock};
+  const cuuint32_t boxes[2][2] = {{64, kBlock}, {64, 128}};
   const cuuint32_t estr[2] = {1, 1};
-  CUtensorMap* maps[2] = {&c->tmap_k, &c->tmap_v};
-  void* bases[2] = {c->buf.k, c->buf.v};
-  for (int i = 0; i < 2; ++i) {
+  CUtensorMap* maps[4] = {&c->tmap_k, &c->tmap_v, &c->tmap_k128, &c->tmap_v128};
+  void* bases[4] = {c->buf.k, c->buf.v, c->buf.k, c->buf.v};
+  for (int i = 0; i < 4; ++i) {
+    const cuuint32_t* box = boxes[i / 2];
     const CUresult r = reinterpret_cast<Encode>(fn)(maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, bases[i], dims,
                                                     strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -542,6 +547,7 @@ compkv_status compkv_init(const compkv_config* cfg, const compkv_buffers* bufs, 
   // the kernels' shared memory limits and cluster size, once for this configuration
   cudaError_t e = prepare_stream(cfg->head_dim, cfg->r, cfg->group_size);
   if (e == cudaSuccess) e = prepare_post(cfg->head_dim, cfg->group_size, L.C, L.bpc_max, L.K);
+  if (e == cudaSuccess) e = prepare_shared(cfg->head_dim);
   if (e != cudaSuccess) {
     delete c;
     return cuda_status(e, "setting the kernels' attributes");
@@ -815,37 +821,73 @@ compkv_status compkv_attend_shared(compkv_ctx* c, int layer, const void* q, int 
   if (type != COMPKV_BF16 && type != COMPKV_F32)
     return fail(COMPKV_ERR_INVALID_ARG, "type must be COMPKV_BF16 or COMPKV_F32 (got %d)", type);
   if (!prefix_seq || !prefix_len) return fail(COMPKV_ERR_INVALID_ARG, "prefix_seq and prefix_len must not be NULL");
-  if (c->kv_host) return fail(COMPKV_ERR_UNSUPPORTED_SHAPE, "compkv_attend_shared needs k and v in device memory");
+  if (c->kv_host || !c->tmap_ok) return fail(COMPKV_ERR_UNSUPPORTED_SHAPE, "compkv_attend_shared needs k and v in device memory");
   SharedArgs a;
   memset(&a, 0, sizeof(a));
   const LayerArgs b = base_args(c, layer);
-  a.k = b.k;
-  a.v = b.v;
   a.seq_len = b.seq_len;
   a.q = q;
   a.out = out;
-  a.ws = reinterpret_cast<float*>(workspace);
   a.status = b.status;
   a.q_bf16 = type == COMPKV_BF16;
   a.B = c->cfg.batch;
   a.Hkv = c->cfg.num_kv_heads;
   a.G = c->cfg.group_size;
   a.d = c->cfg.head_dim;
+  a.P = device_sms() < kMaxSharedCtas ? device_sms() : kMaxSharedCtas;
+  a.layer_row0 = b.layer_row0;
   const size_t need = shared_workspace_bytes(a.B, a.Hkv, a.G, a.d);
   if (workspace_bytes < need)
     return fail(COMPKV_ERR_INVALID_ARG, "workspace_bytes %zu < required %zu", workspace_bytes, need);
+  a.acc = reinterpret_cast<float*>(workspace);
+  a.ml = reinterpret_cast<float2*>(a.acc + shared_rows(a.B, a.Hkv, a.G) * a.d);
   for (int s = 0; s < a.B; ++s) {
     const int p = prefix_seq[s];
     if (p < -2 || p >= a.B) return fail(COMPKV_ERR_INVALID_ARG, "prefix_seq[%d] = %d not in -2..%d", s, p, a.B - 1);
     a.seq_row0[s] = c->lay.seq_row0[s];
     a.cap_blocks[s] = c->lay.cap_blocks[s];
-    a.prefix_seq[s] = p;
+    a.prefix_seq[s] = (signed char)p;
+    a.part[s] = p != -2;
     if (p < 0) continue;
     if (prefix_len[p] < 0 || prefix_len[p] > c->lay.cap_blocks[p] * kBlock)
       return fail(COMPKV_ERR_CAPACITY, "prefix_len[%d] = %d outside [0, %d]", p, prefix_len[p],
                   c->lay.cap_blocks[p] * kBlock);
     a.prefix_len[p] = prefix_len[p];
   }
+  // entries: 128 query rows of the sequences of each prefix, then every sequence's own tokens
+  int members = 0;
+  auto entry = [&](int holder, int rows) {
+    a.holder[a.entries] = (unsigned char)holder;
+    a.rows[a.entries] = (unsigned char)rows;
+    a.row0[a.entries + 1] = a.row0[a.entries] + rows * a.Hkv;
+    ++a.entries;
+  };
+  const int most = 128 / a.G;  // sequences of one entry
+  for (int p = 0; p < a.B; ++p) {
+    int first = members;
+    for (int s = 0; s < a.B; ++s)
+      if (prefix_seq[s] == p) a.member[members++] = (unsigned char)s;
+    for (; first < members; first += most) {
+      const int n = members - first < most ? members - first : most;
+      for (int i = 0; i < n; ++i) {
+        a.prefix_entry[a.member[first + i]] = (unsigned char)a.entries;
+        a.prefix_row[a.member[first + i]] = (unsigned char)(i * a.G);
+      }
+      a.member0[a.entries] = (unsigned char)first;
+      entry(p, n * a.G);
+    }
+  }
+  a.prefixes = a.entries;
+  for (int s = 0; s < a.B; ++s) {
+    if (!a.part[s]) continue;
+    a.tail_entry[s] = (unsigned char)a.entries;
+    entry(s, a.G);
+  }
+  if (!a.entries) return COMPKV_OK;
+  memcpy(a.k16, &c->tmap_k, sizeof(CUtensorMap));
+  memcpy(a.v16, &c->tmap_v, sizeof(CUtensorMap));
+  memcpy(a.k128, &c->tmap_k128, sizeof(CUtensorMap));
+  memcpy(a.v128, &c->tmap_v128, sizeof(CUtensorMap));
   cudaStream_t st = (cudaStream_t)stream;
   return launch(c, COMPKV_KERNEL_ATTEND_SHARED, st, "shared attention launch",
                 [&] { return launch_attend_shared(a, st); }, 2);

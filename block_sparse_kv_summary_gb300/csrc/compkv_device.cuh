@@ -143,20 +143,40 @@ struct PageArgs {
 };
 
 // Arguments of the attention over a shared prefix and the sequences' own tokens.
+// Its work items are entries x KV heads: one entry per 128 query rows of a
+// prefix's sequences, then one per sequence for its own tokens.
+constexpr int kMaxPrefixEntries = kMaxBatch;  // each has a sequence of its own
+constexpr int kMaxSharedEntries = kMaxPrefixEntries + kMaxBatch;
 struct SharedArgs {
-  const __nv_bfloat16* k;      // the cache of this layer
-  const __nv_bfloat16* v;
   const int* seq_len;          // [B] of this layer
   const void* q;               // [B][Hq][d] fp32, or bf16 where q_bf16
   void* out;                   // the same type
-  float* ws;                   // workspace
+  float* acc;                  // workspace: [rows][d] unnormalised outputs of a segment's rows
+  float2* ml;                  // workspace: [rows] maximum (log2 units) and sum of its weights
   int* status;
   int q_bf16;
   int B, Hkv, G, d;
+  int P;                       // CTAs of the attention kernel
+  int prefixes, entries;       // entries of prefixes, and all
+  int64_t layer_row0;          // first row of this layer in the whole cache
   int64_t seq_row0[kMaxBatch];
   int cap_blocks[kMaxBatch];
-  int prefix_seq[kMaxBatch];   // the sequence that holds the prefix, -1: none, -2: takes no part
   int prefix_len[kMaxBatch];   // of a holder: tokens of its prefix
+  signed char part[kMaxBatch];        // of a sequence: 1 takes part
+  signed char prefix_seq[kMaxBatch];  // the sequence that holds its prefix, or < 0
+  unsigned char member[kMaxBatch];    // sequences in the order of their prefixes
+  unsigned char tail_entry[kMaxBatch];    // of a sequence: its own entry, and its rows in a prefix's:
+  unsigned char prefix_entry[kMaxBatch];  // the entry
+  unsigned char prefix_row[kMaxBatch];    // and the first row
+  unsigned char holder[kMaxSharedEntries];   // of an entry: the sequence whose tokens it reads
+  unsigned char member0[kMaxPrefixEntries];  // its first row's place in `member`
+  unsigned char rows[kMaxSharedEntries];     // query rows per head, 1..128
+  int row0[kMaxSharedEntries + 1];           // rows of all heads of the entries before it
+  // tensor maps of the whole K and V caches, boxes of 64 x 16 and of 64 x 128 with the 128-byte swizzle
+  alignas(64) unsigned long long k16[16];
+  alignas(64) unsigned long long v16[16];
+  alignas(64) unsigned long long k128[16];
+  alignas(64) unsigned long long v128[16];
 };
 
 __host__ __device__ inline int pad_g(int G) { return G < 4 ? 4 : G; }

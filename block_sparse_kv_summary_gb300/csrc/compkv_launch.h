@@ -36,7 +36,14 @@ inline int fork_chunks(int blocks) { return blocks < 1 ? 1 : (blocks + kForkBloc
 cudaError_t launch_fork(const PageArgs& a, cudaStream_t st);
 cudaError_t launch_compact(const PageArgs& a, cudaStream_t st);
 // Attention over a shared prefix and the sequences' own tokens.
-size_t shared_workspace_bytes(int B, int Hkv, int G, int d);
+// Workspace rows: every entry's rows of every head once, and up to 128 more per CTA where a segment ends
+// inside an item.
+constexpr int kMaxSharedCtas = 256;
+inline int64_t shared_rows(int B, int Hkv, int G) { return (int64_t)2 * B * Hkv * G + 128 * kMaxSharedCtas; }
+inline size_t shared_workspace_bytes(int B, int Hkv, int G, int d) {
+  return (size_t)shared_rows(B, Hkv, G) * (d + 2) * 4;
+}
+cudaError_t prepare_shared(int d);
 cudaError_t launch_attend_shared(const SharedArgs& a, cudaStream_t st);
 // One bounded mbarrier wait that runs out and records kDevTimeout in `status`.
 cudaError_t launch_wait_selftest(int* status, cudaStream_t st);

@@ -10,10 +10,11 @@
 // A head is held by D/8 lanes, 8 coordinates each: one 16-byte load of bf16.
 //
 // Queries are computed in fp32.  Keys are computed as unevaluated sums of two
-// floats and rounded to bf16 once: the summaries are those of the stored
-// keys, and a key that falls on the wrong side of a rounding border moves its
-// block's mean and variance by a bf16 step, some thousand times more than the
-// fp32 arithmetic of the summary itself loses.
+// floats, so that the fp32 value that is then rounded to bf16 is the nearest
+// one: the summaries are those of the stored keys, and a key that falls on the
+// wrong side of a rounding border moves its block's mean and variance by a
+// bf16 step, some thousand times more than the fp32 arithmetic of the summary
+// itself loses.
 #include "compkv_launch.h"
 
 namespace compkv {
@@ -38,16 +39,6 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   const float lo = __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo));
   const float hi = __fadd_rn(s.hi, lo);
   return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
-}
-
-// bf16 nearest to hi + lo: hi is moved to its odd neighbour on lo's side when
-// it is inexact, so that the rounding of hi alone sees on which side of a tie
-// the sum lies.
-__device__ __forceinline__ __nv_bfloat16 round_bf16(F2 x) {
-  uint32_t u = __float_as_uint(x.hi);
-  if (x.lo != 0.f && (u & 1u) == 0u && (u & 0x7fffffffu) != 0u && (u & 0x7f800000u) != 0x7f800000u)
-    u += ((__float_as_uint(x.lo) ^ u) >> 31) ? 0xffffffffu : 1u;  // towards zero when the signs differ
-  return __float2bfloat16_rn(__uint_as_float(u));
 }
 
 template <typename T>
@@ -139,7 +130,7 @@ __device__ __forceinline__ F2 turn2(F2 u, float c, F2 v, float s) {
   return add2(p, q);
 }
 
-// The same with two floats per value, rounded to bf16.
+// The same with two floats per value, rounded to fp32 and then to bf16.
 template <int D>
 __device__ __forceinline__ void head_bf16(const float* x, const float* w, const float* row, const RopeArgs& a,
                                           Pairing p, __nv_bfloat16* out) {
@@ -191,11 +182,7 @@ __device__ __forceinline__ void head_bf16(const float* x, const float* w, const 
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const F2 t = {__fadd_rn(y[i].hi, y[i].lo), 0.f};
-    const float lo = __fsub_rn(y[i].lo, __fsub_rn(t.hi, y[i].hi));
-    out[i] = round_bf16({t.hi, lo});
-  }
+  for (int i = 0; i < 8; ++i) out[i] = __float2bfloat16_rn(__fadd_rn(y[i].hi, y[i].lo));
 }
 
 __device__ __forceinline__ void weights8(const float* w, int l, float* out) {

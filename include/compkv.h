@@ -253,9 +253,9 @@ enum { COMPKV_BF16 = 0, COMPKV_F32 = 1 };
  * for the pairs of its first rot_dim coordinates: pair i is (i, i + rot_dim/2),
  * or (2i, 2i + 1) when `interleaved` is 1; the other coordinates stay.  cos
  * and sin of pair i at position p are table[p][i] and table[p][rot_dim/2 + i].
- * Values are only copied.  Queries are computed in fp32; keys to some 40 bits
- * and rounded to bf16 once, because the summaries are those of the stored
- * keys.  Inputs are finite, with squares that fp32 holds. */
+ * Values are only copied.  Queries are computed in fp32; keys to some 40 bits,
+ * rounded to fp32 and then to bf16, because the summaries are those of the
+ * stored keys.  Inputs are finite, with squares that fp32 holds. */
 typedef struct {
   const void *qkv;        /* device [tokens] rows of (Hq + 2 Hkv) d elements: the query heads,   */
                           /* the key heads, the value heads; 16-byte aligned                     */
