@@ -854,15 +854,15 @@ compkv_status compkv_attend_shared(compkv_ctx* c, int layer, const void* q, int 
                   c->lay.cap_blocks[p] * kBlock);
     a.prefix_len[p] = prefix_len[p];
   }
-  // entries: 128 query rows of the sequences of each prefix, then every sequence's own tokens
+  // entries: the query rows of each prefix's sequences, 128 or 256 at a time, then every sequence's own tokens
   int members = 0;
   auto entry = [&](int holder, int rows) {
     a.holder[a.entries] = (unsigned char)holder;
-    a.rows[a.entries] = (unsigned char)rows;
+    a.rows[a.entries] = (unsigned short)rows;
     a.row0[a.entries + 1] = a.row0[a.entries] + rows * a.Hkv;
     ++a.entries;
   };
-  const int most = 128 / a.G;  // sequences of one entry
+  const int most = shared_entry_rows(a.q_bf16) / a.G;  // sequences of one entry
   for (int p = 0; p < a.B; ++p) {
     int first = members;
     for (int s = 0; s < a.B; ++s)

@@ -143,8 +143,8 @@ struct PageArgs {
 };
 
 // Arguments of the attention over a shared prefix and the sequences' own tokens.
-// Its work items are entries x KV heads: one entry per 128 query rows of a
-// prefix's sequences, then one per sequence for its own tokens.
+// Its work items are entries x KV heads: one entry per 128 query rows (256 in
+// bf16) of a prefix's sequences, then one per sequence for its own tokens.
 constexpr int kMaxPrefixEntries = kMaxBatch;  // each has a sequence of its own
 constexpr int kMaxSharedEntries = kMaxPrefixEntries + kMaxBatch;
 struct SharedArgs {
@@ -167,10 +167,10 @@ struct SharedArgs {
   unsigned char member[kMaxBatch];    // sequences in the order of their prefixes
   unsigned char tail_entry[kMaxBatch];    // of a sequence: its own entry, and its rows in a prefix's:
   unsigned char prefix_entry[kMaxBatch];  // the entry
-  unsigned char prefix_row[kMaxBatch];    // and the first row
+  unsigned char prefix_row[kMaxBatch];    // and the first row, below 256
   unsigned char holder[kMaxSharedEntries];   // of an entry: the sequence whose tokens it reads
   unsigned char member0[kMaxPrefixEntries];  // its first row's place in `member`
-  unsigned char rows[kMaxSharedEntries];     // query rows per head, 1..128
+  unsigned short rows[kMaxSharedEntries];    // query rows per head, 1..256
   int row0[kMaxSharedEntries + 1];           // rows of all heads of the entries before it
   // tensor maps of the whole K and V caches, boxes of 64 x 16 and of 64 x 128 with the 128-byte swizzle
   alignas(64) unsigned long long k16[16];

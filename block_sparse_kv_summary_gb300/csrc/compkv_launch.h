@@ -36,10 +36,11 @@ inline int fork_chunks(int blocks) { return blocks < 1 ? 1 : (blocks + kForkBloc
 cudaError_t launch_fork(const PageArgs& a, cudaStream_t st);
 cudaError_t launch_compact(const PageArgs& a, cudaStream_t st);
 // Attention over a shared prefix and the sequences' own tokens.
-// Workspace rows: every entry's rows of every head once, and up to 128 more per CTA where a segment ends
-// inside an item.
-constexpr int kMaxSharedCtas = 256;
-inline int64_t shared_rows(int B, int Hkv, int G) { return (int64_t)2 * B * Hkv * G + 128 * kMaxSharedCtas; }
+// Query rows of one entry at most, and the workspace's rows: every entry's rows of every head once, and an
+// entry's more per CTA where a segment ends inside an item.
+constexpr int kMaxSharedCtas = 160;
+inline int shared_entry_rows(bool bf16) { return bf16 ? 256 : 128; }
+inline int64_t shared_rows(int B, int Hkv, int G) { return (int64_t)2 * B * Hkv * G + 256 * kMaxSharedCtas; }
 inline size_t shared_workspace_bytes(int B, int Hkv, int G, int d) {
   return (size_t)shared_rows(B, Hkv, G) * (d + 2) * 4;
 }

@@ -3,14 +3,16 @@
 //   out = sum_j e^(z_j) v_j / sum_j e^(z_j),   z_j = q . k_j / sqrt(d),
 // j over the prefix's tokens and the sequence's own.
 //
-// A prefix is read once for up to 128 query rows (sequences x query heads of a
-// KV head); a sequence's own tokens are one more item with G rows.  Items are
-// walked in tiles of 128 keys.  One persistent CTA per multiprocessor takes an
-// equal run of the tiles of all items, so that a long prefix and few rows
-// still fill the chip; each piece of an item leaves its rows' maximum, sum and
-// unnormalised output, and a second kernel joins the pieces.
+// A prefix is read once for up to 256 query rows (sequences x query heads of a
+// KV head; 128 in fp32); a sequence's own tokens are one more item with G
+// rows.  Items are walked in tiles of 128 keys.  One persistent CTA per
+// multiprocessor takes an equal run of the tiles of all items, so that a long
+// prefix and few rows still fill the chip; each piece of an item leaves its
+// rows' maximum, sum and unnormalised output, and a second kernel joins the
+// pieces.
 //
-// Within a CTA (tcgen05, one tile in flight behind the other):
+// Within a CTA (tcgen05; a step is one K/V tile times 128 rows, one or two
+// steps a tile, one step in flight behind the other):
 //   warp 8   copies K and V tiles by tensor maps into a ring of stages,
 //   warp 9   issues S = Q K^T into one of two TMEM buffers and O += P V,
 //   warps 0-7 load Q, take the running maximum and sum (thread = row and half
@@ -19,10 +21,14 @@
 // (in powers of two): the weights then stay below 2^8, and what the final
 // division by their sum loses by that is nothing.
 //
-// fp32 queries and weights are split into three bf16 parts of 8 bits each and
-// multiplied part by part (K and V are bf16 as they are), so the products hold
-// 24 bits; bf16 queries take one product, and their weights are rounded to
-// bf16, 2^-9 of each on average, as the result is.
+// bf16 queries take one product each, and their weights are rounded to bf16,
+// as the result is.  fp32 queries and weights are split into three bf16 parts
+// of 8 bits each and multiplied part by part (K and V are bf16 as they are),
+// the smallest first: the accumulator truncates what each addition of 16
+// products loses below its last bit, always towards zero, and only the last
+// part's additions meet a large accumulator.  For the same reason O of a tile
+// is added up over the tiles in registers, rounded to nearest: left in TMEM
+// over 32K keys it came out 8e-6 too small.
 #include "compkv_launch.h"
 
 namespace compkv {
@@ -31,7 +37,7 @@ namespace {
 
 constexpr int kTile = 128;                // keys of a tile, and query rows of an item at most
 constexpr int kSoftmaxWarps = 8;
-constexpr int kThreads = 32 * (kSoftmaxWarps + 2);
+constexpr int kThreads = 32 * (kSoftmaxWarps + 4);  // registers are dealt out by groups of four warps
 constexpr int kItemUnits = 1;             // what starting an item costs, in tiles
 constexpr float kRescale = 8.f;           // log2 of the factor that a maximum may rise by before O is scaled
 constexpr size_t kSmemLimit = 232448;
@@ -116,9 +122,9 @@ struct Walk {
   }
 };
 // Workspace row of the first row of a segment of CTA c: segments follow one another by item or by CTA,
-// and each step adds at least the rows of the segment before it.
-__device__ __forceinline__ int64_t segment_row(const SharedArgs& a, int e, int h, int c) {
-  return a.row0[e] + h * a.rows[e] + (int64_t)kTile * c;
+// and each step adds at least the rows of the segment before it (256 at most).
+__device__ __forceinline__ int segment_row(const SharedArgs& a, int e, int h, int c) {
+  return a.row0[e] + h * a.rows[e] + 256 * c;
 }
 
 // ---------------------------------------------------------------- tcgen05
@@ -139,24 +145,38 @@ __device__ __forceinline__ constexpr uint32_t instruction(int n, bool n_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((n_major ? 1u : 0u) << 16) | ((uint32_t)(n / 8) << 17) |
          ((uint32_t)(kTile / 16) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// Issued by the warp's leader; the whole warp computes the operands, which then stand in uniform registers.
+__device__ __forceinline__ uint32_t elect_leader() {
+  uint32_t lead;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(lead));
+  return lead;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+__device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead)
+      : "memory");
 }
+// Registers of this warp from here on; every warp of its group of four says the same.
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -182,11 +202,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float* f) {
 __device__ __forceinline__ void tmem_ld64(uint32_t addr, float* f) {
   uint32_t* r = reinterpret_cast<uint32_t*>(f);
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
       "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%2"
-      "6,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%5"
-      "0,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63"
+      "6,%27,%28,%29,%30,%31"
       "}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,"
+      "%56,%57,%58,%59,%60,%61,%62,%63"
+      "}, [%65];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
@@ -196,7 +219,7 @@ __device__ __forceinline__ void tmem_ld64(uint32_t addr, float* f) {
         "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
         "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
         "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-      : "r"(addr)
+      : "r"(addr), "r"(addr + 32)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
@@ -209,6 +232,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
+      "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16"
+      "};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -218,8 +250,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
 __device__ __forceinline__ uint32_t split2(float& a, float& b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
-  a -= __uint_as_float(u << 16);
-  b -= __uint_as_float(u & 0xffff0000u);
+  const float2 left = __ffma2_rn(make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)),
+                                 make_float2(-1.f, -1.f), make_float2(a, b));
+  a = left.x;
+  b = left.y;
   return u;
 }
 
@@ -227,8 +261,10 @@ __device__ __forceinline__ uint32_t split2(float& a, float& b) {
 template <int D, int PARTS>
 struct Shape {
   static constexpr int kHalf = kTile * 128;             // 64 coordinates of 128 rows, 128 bytes a row
-  static constexpr int kStage = kHalf * (D / 64);       // a K or a V tile
-  static constexpr int kQ = kStage * PARTS;
+  static constexpr int kStage = kHalf * (D / 64);       // a K or a V tile, or 128 rows of Q in one part
+  static constexpr int kSub = PARTS == 1 ? 2 : 1;       // times 128 query rows of an item at most
+  static constexpr int kQ = kStage * PARTS * kSub;
+  static constexpr bool kTileO = PARTS == 3;            // O of one tile at a time; added up in registers
   // TMEM columns: two buffers of 128 scores and, over and behind them, up to three parts of weights; O
   static constexpr int kBuffer = PARTS == 3 ? 192 : 128;
   static constexpr int kO = 2 * kBuffer;
@@ -236,6 +272,7 @@ struct Shape {
 };
 struct Control {
   Plan plan;
+  unsigned char member[kMaxBatch];  // of the arguments: there a warp's lanes would read them one after another
   float row_max[2][2][kTile];  // [tile & 1][half of the keys][row]; sums at the end of a segment
   uint64_t full[8], empty[8], q_full, s_full[2], p_full[2], o_full[2];  // [tile & 1]
   uint32_t tmem;
@@ -270,30 +307,55 @@ __device__ __forceinline__ bool warp_wait(Control* ctl, uint64_t* bar, uint32_t 
   return ok;
 }
 
-// Rows of the segment's queries into shared memory, swizzled, in PARTS parts; by the softmax warps.
+// Rows of the segment's queries into shared memory, swizzled, in PARTS parts; by the softmax warps, with
+// several loads of a thread in flight.
 template <int D, int PARTS>
-__device__ __forceinline__ void load_queries(const SharedArgs& a, const Segment& g, char* q_smem) {
+__device__ __forceinline__ void load_queries(const SharedArgs& a, const Control* ctl, const Segment& g, char* q_smem) {
   constexpr int CH = D / 8;  // 16-byte chunks of 8 coordinates
-  const int rows = a.rows[g.e];
-  for (int i = threadIdx.x; i < rows * CH; i += 32 * kSoftmaxWarps) {
-    const int r = i / CH, c = i % CH;
-    const int s = g.e < a.prefixes ? a.member[a.member0[g.e] + r / a.G] : a.holder[g.e];
-    const int64_t at = (((int64_t)s * a.Hkv + g.h) * a.G + r % a.G) * D + 8 * c;
-    const int to = (c / 8) * Shape<D, PARTS>::kHalf + r * 128 + (((c % 8) ^ (r & 7)) << 4);
-    if (PARTS == 1) {
-      *reinterpret_cast<uint4*>(q_smem + to) = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) + at));
-    } else {
-      const float4* src = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.q) + at);
-      const float4 u = __ldg(src), v = __ldg(src + 1);
-      float x[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+  constexpr int N = PARTS == 1 ? 8 : 4, W = PARTS == 1 ? 1 : 2, T = 32 * kSoftmaxWarps;
+  const int rows = a.rows[g.e], chunks = rows * CH, gs = 31 - __clz(a.G);
+  const bool prefix = g.e < a.prefixes;
+  const unsigned char* member = ctl->member + (prefix ? a.member0[g.e] : 0);
+  const int holder = a.holder[g.e];
+  const char* base = reinterpret_cast<const char*>(a.q) + (int64_t)g.h * a.G * (D * 2 * W);
+  for (int i0 = threadIdx.x; i0 < chunks; i0 += N * T) {
+    uint4 x[N][W];
 #pragma unroll
-      for (int p = 0; p < PARTS; ++p) {
-        uint4 w;
-        w.x = split2(x[0], x[1]);
-        w.y = split2(x[2], x[3]);
-        w.z = split2(x[4], x[5]);
-        w.w = split2(x[6], x[7]);
-        *reinterpret_cast<uint4*>(q_smem + p * Shape<D, PARTS>::kStage + to) = w;
+    for (int u = 0; u < N; ++u) {
+      const int i = min(i0 + u * T, chunks - 1), r = i / CH;  // behind the last chunk: that one again
+      const int s = prefix ? member[r >> gs] : holder;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          base + ((int64_t)(s * a.Hkv * a.G + (r & (a.G - 1))) * D + 8 * (i % CH)) * (2 * W));
+#pragma unroll
+      for (int w = 0; w < W; ++w) x[u][w] = __ldg(src + w);
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int i = i0 + u * T, r = i / CH, c = i % CH;
+      if (i < chunks) {
+        char* to = q_smem + (r / kTile) * (PARTS * Shape<D, PARTS>::kStage) + (c / 8) * Shape<D, PARTS>::kHalf +
+                   (r % kTile) * 128 + (((c % 8) ^ (r & 7)) << 4);
+        if (PARTS == 1) {
+          *reinterpret_cast<uint4*>(to) = x[u][0];
+        } else {
+          float f[8];
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            f[4 * w] = __uint_as_float(x[u][w].x);
+            f[4 * w + 1] = __uint_as_float(x[u][w].y);
+            f[4 * w + 2] = __uint_as_float(x[u][w].z);
+            f[4 * w + 3] = __uint_as_float(x[u][w].w);
+          }
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) {
+            uint4 w;
+            w.x = split2(f[0], f[1]);
+            w.y = split2(f[2], f[3]);
+            w.z = split2(f[4], f[5]);
+            w.w = split2(f[6], f[7]);
+            *reinterpret_cast<uint4*>(to + p * Shape<D, PARTS>::kStage) = w;
+          }
+        }
       }
     }
   }
@@ -333,6 +395,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
     }
     ctl->abort = 0;
     fence_mbar_init();
+  } else if (warp == 3) {
+    ctl->member[lane] = a.member[lane];
+    ctl->member[lane + 32] = a.member[lane + 32];
   }
   fence_before();
   __syncthreads();
@@ -343,118 +408,139 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
   Walk walk(a, ctl->plan, c);
   Segment g;
 
-  if (warp == kSoftmaxWarps) {
-    // ---- copies: K and V of every tile in turn, 16-token boxes where the item ends inside the tile
-    if (lane == 0) {
-      int slot = 0, phase = 0;
-      while (walk.next(a, ctl->plan, g)) {
-        const int s = a.holder[g.e];
-        const int64_t tok = (a.layer_row0 + a.seq_row0[s] + (int64_t)g.h * a.cap_blocks[s]) * kBlock +
-                            entry_first(a, g.e, held_tokens(a, s));
-        for (int t = g.tile0; t < g.tile1; ++t) {
-          const int valid = g.valid(t), y = (int)(tok + (int64_t)t * kTile);
-          for (int kv = 0; kv < 2; ++kv) {
-            if (wait(ctl, &ctl->empty[slot], phase ^ 1, a.status, 51)) {
-              char* dst = ring + slot * S::kStage;
-              if (valid == kTile) {
-                mbar_arrive_expect_tx(&ctl->full[slot], S::kStage);
-#pragma unroll
-                for (int x = 0; x < D / 64; ++x)
-                  tma_box(dst + x * S::kHalf, kv ? a.v128 : a.k128, 64 * x, y, &ctl->full[slot]);
-              } else {
-                const int nb = (valid + kBlock - 1) / kBlock;
-                mbar_arrive_expect_tx(&ctl->full[slot], nb * kBlock * D * 2);
-                for (int b = 0; b < nb; ++b)
+  if (warp >= kSoftmaxWarps) {
+    fewer_registers<72>();  // 128 x 72 + 256 x 216: the 384 x 168 of the launch
+    if (warp == kSoftmaxWarps) {
+      // ---- copies: K and V of every tile in turn, 16-token boxes where the item ends inside the tile
+      if (lane == 0) {
+        int slot = 0, phase = 0;
+        while (walk.next(a, ctl->plan, g)) {
+          const int s = a.holder[g.e];
+          const int64_t tok = (a.layer_row0 + a.seq_row0[s] + (int64_t)g.h * a.cap_blocks[s]) * kBlock +
+                              entry_first(a, g.e, held_tokens(a, s));
+          for (int t = g.tile0; t < g.tile1; ++t) {
+            const int valid = g.valid(t), y = (int)(tok + (int64_t)t * kTile);
+            for (int kv = 0; kv < 2; ++kv) {
+              if (wait(ctl, &ctl->empty[slot], phase ^ 1, a.status, 51)) {
+                char* dst = ring + slot * S::kStage;
+                if (valid == kTile) {
+                  mbar_arrive_expect_tx(&ctl->full[slot], S::kStage);
 #pragma unroll
                   for (int x = 0; x < D / 64; ++x)
-                    tma_box(dst + x * S::kHalf + b * kBlock * 128, kv ? a.v16 : a.k16, 64 * x, y + b * kBlock,
-                            &ctl->full[slot]);
+                    tma_box(dst + x * S::kHalf, kv ? a.v128 : a.k128, 64 * x, y, &ctl->full[slot]);
+                } else {
+                  const int nb = (valid + kBlock - 1) / kBlock;
+                  mbar_arrive_expect_tx(&ctl->full[slot], nb * kBlock * D * 2);
+                  for (int b = 0; b < nb; ++b)
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x)
+                      tma_box(dst + x * S::kHalf + b * kBlock * 128, kv ? a.v16 : a.k16, 64 * x, y + b * kBlock,
+                              &ctl->full[slot]);
+                }
               }
-            }
-            if (++slot == STAGES) {
-              slot = 0;
-              phase ^= 1;
+              if (++slot == STAGES) {
+                slot = 0;
+                phase ^= 1;
+              }
             }
           }
         }
       }
-    }
-  } else if (warp == kSoftmaxWarps + 1) {
-    // ---- products: S of tile n + 1 is issued ahead of O += P V of tile n
-    const uint32_t q_addr = smem_u32(q_smem), ring_addr = smem_u32(ring);
-    int n = 0, segs = 0;       // tiles and segments before this one
-    int slot = 0, phase = 0;   // of the next K tile in the ring
-    int v_slot = 0, v_phase = 0, v_valid = 0;
-    bool pending = false, first = false;  // a tile whose P V is still to come, and whether O starts with it
-    auto issue_pv = [&] {
-      // tile n - 1
-      warp_wait(ctl, &ctl->full[v_slot], v_phase, a.status, 52);
-      const uint32_t v = ring_addr + v_slot * S::kStage;
-      if (v_valid % kBlock) {  // weights behind the last key are zero, but 0 x NaN is not
-        const int upto = (v_valid + kBlock - 1) / kBlock * kBlock;
-        for (int i = lane; i < (upto - v_valid) * (D / 8); i += 32) {
-          const int r = v_valid + i / (D / 8), ch = i % (D / 8);
-          *reinterpret_cast<uint4*>(ring + v_slot * S::kStage + (ch / 8) * S::kHalf + r * 128 + (ch % 8) * 16) =
-              make_uint4(0, 0, 0, 0);
-        }
-        fence_async_smem();
-        __syncwarp();
-      }
-      const bool ok = warp_wait(ctl, &ctl->p_full[(n - 1) & 1], ((n - 1) >> 1) & 1, a.status, 53);
-      fence_after();
-      if (lane == 0 && ok) {
-        const uint32_t p = tmem + ((n - 1) & 1) * S::kBuffer;
-        const int steps = (v_valid + 15) / 16;
-        for (int part = 0; part < PARTS; ++part)
-          for (int k = 0; k < steps; ++k)
-            mma_ts(tmem + S::kO, p + part * 64 + k * 8, operand(v + k * 16 * 128, S::kHalf, 1024),
-                   instruction(D, true), !(first && part == 0 && k == 0));
-        mma_commit(&ctl->empty[v_slot]);
-        mma_commit(&ctl->o_full[(n - 1) & 1]);
-      }
-      pending = false;
-    };
-    while (walk.next(a, ctl->plan, g)) {
-      for (int t = g.tile0; t < g.tile1; ++t) {
-        if (t == g.tile0) {
-          if (pending) issue_pv();
-          warp_wait(ctl, &ctl->q_full, segs & 1, a.status, 54);
-          ++segs;
-        }
-        const bool ok = warp_wait(ctl, &ctl->full[slot], phase, a.status, 55);
-        fence_after();
-        if (lane == 0 && ok) {
-          const uint32_t k = ring_addr + slot * S::kStage;
-#pragma unroll
-          for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              const uint32_t off = (i / 4) * S::kHalf + (i % 4) * 32;
-              mma_ss(tmem + (n & 1) * S::kBuffer, operand(q_addr + part * S::kStage + off, 16, 1024),
-                     operand(k + off, 16, 1024), instruction(kTile, false), part + i > 0);
+    } else if (warp == kSoftmaxWarps + 1) {
+      // ---- products: S of step n is issued ahead of O += P V of step n - 1
+      const uint32_t q_addr = smem_u32(q_smem), ring_addr = smem_u32(ring), lead = elect_leader();
+      int n = 0, segs = 0;      // steps and segments before this one
+      int slot = 0, phase = 0;  // of the next tile in the ring
+      // the step whose P V is still to come
+      bool pending = false, v_first = false, v_last = false;  // O starts with it; it is the tile's last
+      int v_slot = 0, v_phase = 0, v_valid = 0, v_sub = 0;
+      auto issue_pv = [&] {  // of step n - 1
+        const uint32_t v = ring_addr + v_slot * S::kStage;
+        if (v_sub == 0) {
+          warp_wait(ctl, &ctl->full[v_slot], v_phase, a.status, 52);
+          if (v_valid % kBlock) {  // weights behind the last key are zero, but 0 x NaN is not
+            const int upto = (v_valid + kBlock - 1) / kBlock * kBlock;
+            for (int i = lane; i < (upto - v_valid) * (D / 8); i += 32) {
+              const int r = v_valid + i / (D / 8), ch = i % (D / 8);
+              *reinterpret_cast<uint4*>(ring + v_slot * S::kStage + (ch / 8) * S::kHalf + r * 128 + (ch % 8) * 16) =
+                  make_uint4(0, 0, 0, 0);
             }
-          mma_commit(&ctl->empty[slot]);
-          mma_commit(&ctl->s_full[n & 1]);
+            fence_async_smem();
+            __syncwarp();
+          }
         }
+        const bool ok = warp_wait(ctl, &ctl->p_full[(n - 1) & 1], ((n - 1) >> 1) & 1, a.status, 53);
+        fence_after();
+        if (ok) {
+          const uint32_t p = tmem + ((n - 1) & 1) * S::kBuffer, o = tmem + S::kO + v_sub * D;
+          const uint64_t vd = operand(v, S::kHalf, 1024);
+          const bool add = !(v_first || S::kTileO);
+          if (v_valid == kTile) {
+#pragma unroll
+            for (int part = PARTS - 1; part >= 0; --part)
+#pragma unroll
+              for (int k = 0; k < kTile / 16; ++k)
+                mma_ts(o, p + part * 64 + k * 8, vd + k * (16 * 128 / 16), instruction(D, true),
+                       part < PARTS - 1 || k > 0 || add, lead);
+          } else {
+            for (int part = PARTS - 1; part >= 0; --part)
+              for (int k = 0; k < (v_valid + 15) / 16; ++k)
+                mma_ts(o, p + part * 64 + k * 8, vd + k * (16 * 128 / 16), instruction(D, true),
+                       part < PARTS - 1 || k > 0 || add, lead);
+          }
+          if (v_last) mma_commit(&ctl->empty[v_slot], lead);
+          mma_commit(&ctl->o_full[(n - 1) & 1], lead);
+        }
+        pending = false;
+      };
+      while (walk.next(a, ctl->plan, g)) {
+        const int subs = (a.rows[g.e] + kTile - 1) / kTile;
         if (pending) issue_pv();
-        if (++slot == STAGES) {
-          slot = 0;
-          phase ^= 1;
+        warp_wait(ctl, &ctl->q_full, segs & 1, a.status, 54);
+        ++segs;
+        for (int t = g.tile0; t < g.tile1; ++t) {
+          const bool ok = warp_wait(ctl, &ctl->full[slot], phase, a.status, 55);
+          const uint32_t k = ring_addr + slot * S::kStage;
+          const int k_slot = slot;
+          if (++slot == STAGES) {
+            slot = 0;
+            phase ^= 1;
+          }
+          for (int sub = 0; sub < subs; ++sub) {
+            fence_after();
+            if (ok) {
+              const uint64_t qd = operand(q_addr + sub * (PARTS * S::kStage), 16, 1024), kd = operand(k, 16, 1024);
+#pragma unroll
+              for (int part = PARTS - 1; part >= 0; --part)
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                  const uint32_t off = (i / 4) * S::kHalf + (i % 4) * 32;
+                  mma_ss(tmem + (n & 1) * S::kBuffer, qd + (part * S::kStage + off) / 16, kd + off / 16,
+                         instruction(kTile, false), part < PARTS - 1 || i > 0, lead);
+                }
+              if (sub == subs - 1) mma_commit(&ctl->empty[k_slot], lead);
+              mma_commit(&ctl->s_full[n & 1], lead);
+            }
+            if (pending) issue_pv();
+            v_slot = slot;
+            v_phase = phase;
+            v_valid = g.valid(t);
+            v_first = t == g.tile0;
+            v_sub = sub;
+            v_last = sub == subs - 1;
+            pending = true;
+            ++n;
+          }
+          if (++slot == STAGES) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
-        v_slot = slot;
-        v_phase = phase;
-        v_valid = g.valid(t);
-        first = t == g.tile0;
-        pending = true;
-        if (++slot == STAGES) {
-          slot = 0;
-          phase ^= 1;
-        }
-        ++n;
       }
+      if (pending) issue_pv();
     }
-    if (pending) issue_pv();
   } else {
+    more_registers<216>();
     // ---- softmax: thread = row (its TMEM lane) and half of the keys
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -462,109 +548,150 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
     int n = 0;
     bool more = walk.next(a, ctl->plan, g);
     if (more) {
-      load_queries<D, PARTS>(a, g, q_smem);
+      load_queries<D, PARTS>(a, ctl, g, q_smem);
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->q_full);
     }
     while (more) {
       const Segment cur = g;
-      const int rows = a.rows[cur.e];
-      const bool live = (warp & 3) * 32 < rows;  // the same for both warps of these rows
-      float m = -INFINITY, l = 0.f;              // maximum that the weights refer to, and their sum over this half
-      for (int t = cur.tile0; t < cur.tile1; ++t, ++n) {
-        warp_wait(ctl, &ctl->s_full[n & 1], (n >> 1) & 1, a.status, 56);
-        fence_after();
-        if (live) {
-          const uint32_t buf = tmem + lanes + (n & 1) * S::kBuffer;
-          float s[64];
-          tmem_ld64(buf + half * 64, s);
-          const int valid = cur.valid(t) - half * 64;  // keys of this half
-          if (valid < 64) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (i >= valid) s[i] = -INFINITY;
-          }
-          float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-          for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-          const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-          ctl->row_max[n & 1][half][row] = mine;
-          fence_before();
-          asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");  // both halves have read S, too
+      const int rows = a.rows[cur.e], subs = (rows + kTile - 1) / kTile;
+      float m2[2] = {-INFINITY, -INFINITY}, l2[2] = {0.f, 0.f};  // per 128 rows: reference of the weights, their sum here
+      float acc[S::kTileO ? D / 2 : 1] = {};                     // kTileO: O so far, in units of the reference
+      for (int t = cur.tile0; t < cur.tile1; ++t) {
+        for (int sub = 0; sub < subs; ++sub, ++n) {
+          warp_wait(ctl, &ctl->s_full[n & 1], (n >> 1) & 1, a.status, 56);
           fence_after();
-          const float top = fmaxf(mine, ctl->row_max[n & 1][half ^ 1][row]);
-          const bool raise = row < rows && top > m + kRescale;  // holds for a segment's first tile: m = -inf
-          if (__any_sync(0xffffffffu, raise)) {
-            const float next = raise ? top : m;
-            if (t > cur.tile0) {
-              // O of the tiles before is complete, and the next product waits for p_full
+          if (sub * kTile + (warp & 3) * 32 < rows) {  // the same for both warps of these rows
+            const uint32_t buf = tmem + lanes + (n & 1) * S::kBuffer;
+            const uint32_t o_at = tmem + lanes + S::kO + sub * D + half * (D / 2);
+            float s[64];
+            tmem_ld64(buf + half * 64, s);
+            const int valid = cur.valid(t) - half * 64;  // keys of this half
+            if (valid < 64) {
+#pragma unroll
+              for (int i = 0; i < 64; ++i)
+                if (i >= valid) s[i] = -INFINITY;
+            }
+            float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+            const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+            ctl->row_max[n & 1][half][row] = mine;
+            fence_before();
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");  // both halves have read S, too
+            fence_after();
+            const float top = fmaxf(mine, ctl->row_max[n & 1][half ^ 1][row]);
+            float m = sub ? m2[1] : m2[0], l = sub ? l2[1] : l2[0], f = 1.f;
+            // holds for a segment's first tile: m = -inf
+            const bool raise = __any_sync(0xffffffffu, sub * kTile + row < rows && top > m + kRescale);
+            if (raise) {
+              const float next = top > m + kRescale ? top : m;
+              f = m == next ? 1.f : exp2_approx(m - next);
+              m = next;
+              l *= f;
+              if (!S::kTileO && t > cur.tile0) {
+                // O of the tile before is complete (with two steps a tile: S was issued behind its product),
+                // and the next product into it waits for p_full
+                if (subs == 1) warp_wait(ctl, &ctl->o_full[(n - 1) & 1], ((n - 1) >> 1) & 1, a.status, 57);
+                fence_after();
+#pragma unroll
+                for (int x = 0; x < D / 64; ++x) {
+                  float o[32];
+                  tmem_ld32(o_at + 32 * x, o);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) o[i] *= f;
+                  tmem_st32(o_at + 32 * x, reinterpret_cast<const uint32_t*>(o));
+                }
+              }
+            }
+            const float ref = m == -INFINITY ? 0.f : m;
+            float2 sum[2] = {};
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float2 x = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), make_float2(scale, scale), make_float2(-ref, -ref));
+              s[2 * i] = exp2_approx(x.x);
+              s[2 * i + 1] = exp2_approx(x.y);
+              sum[i & 1] = __fadd2_rn(sum[i & 1], make_float2(s[2 * i], s[2 * i + 1]));
+            }
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            if (sub) {
+              m2[1] = m;
+              l2[1] = l;
+            } else {
+              m2[0] = m;
+              l2[0] = l;
+            }
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part) {
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = split2(s[32 * x + 2 * i], s[32 * x + 2 * i + 1]);
+                tmem_st16(buf + part * 64 + half * 32 + 16 * x, w);
+              }
+            }
+            if (S::kTileO && t > cur.tile0) {
+              // O of the tile before, in the reference of its weights; the next product waits for p_full
               warp_wait(ctl, &ctl->o_full[(n - 1) & 1], ((n - 1) >> 1) & 1, a.status, 57);
               fence_after();
-              const float f = m == next ? 1.f : exp2_approx(m - next);
 #pragma unroll
               for (int x = 0; x < D / 64; ++x) {
                 float o[32];
-                tmem_ld32(tmem + lanes + S::kO + half * (D / 2) + 32 * x, o);
+                tmem_ld32(o_at + 32 * x, o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] *= f;
-                tmem_st32(tmem + lanes + S::kO + half * (D / 2) + 32 * x, reinterpret_cast<const uint32_t*>(o));
+                for (int i = 0; i < 32; ++i) acc[(32 * x + i) % (S::kTileO ? D / 2 : 1)] += o[i];
               }
-              l *= f;
+              if (raise) {
+#pragma unroll
+                for (int i = 0; i < D / 2; ++i) acc[i % (S::kTileO ? D / 2 : 1)] *= f;
+              }
             }
-            m = next;
+            wait_st();
+            fence_before();
           }
-          const float ref = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            s[i] = exp2_approx(fmaf(s[i], scale, -ref));
-            sum[i & 3] += s[i];
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-#pragma unroll
-          for (int part = 0; part < PARTS; ++part) {
-            uint32_t w[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = split2(s[2 * i], s[2 * i + 1]);
-            tmem_st32(buf + part * 64 + half * 32, w);
-          }
-          wait_st();
-          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->p_full[n & 1]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->p_full[n & 1]);
       }
       // every S of this segment has been computed: the next one's queries may overwrite these
       more = walk.next(a, ctl->plan, g);
       if (more) {
-        load_queries<D, PARTS>(a, g, q_smem);
+        load_queries<D, PARTS>(a, ctl, g, q_smem);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->q_full);
       }
       warp_wait(ctl, &ctl->o_full[(n - 1) & 1], ((n - 1) >> 1) & 1, a.status, 58);
       fence_after();
-      if (live) {
-        if (half) ctl->row_max[n & 1][0][row] = l;
+      for (int sub = 0; sub < subs; ++sub) {
+        const int r = sub * kTile + row;
+        if (sub * kTile + (warp & 3) * 32 >= rows) break;
+        float l = sub ? l2[1] : l2[0];
+        if (half) ctl->row_max[sub][0][row] = l;
         asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
-        if (!half) l += ctl->row_max[n & 1][0][row];
-        const int64_t at = segment_row(a, cur.e, cur.h, c) + row;
+        if (!half) l += ctl->row_max[sub][0][row];
+        const int64_t at = segment_row(a, cur.e, cur.h, c) + r;
         float* dst = a.acc + at * D + half * (D / 2);
 #pragma unroll
         for (int x = 0; x < D / 64; ++x) {
           float o[32];
-          tmem_ld32(tmem + lanes + S::kO + half * (D / 2) + 32 * x, o);
-          if (row < rows) {
+          tmem_ld32(tmem + lanes + S::kO + sub * D + half * (D / 2) + 32 * x, o);
+          if (S::kTileO) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] += acc[(32 * x + i) % (S::kTileO ? D / 2 : 1)];
+          }
+          if (r < rows) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               reinterpret_cast<float4*>(dst + 32 * x)[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
         }
-        if (!half && row < rows) a.ml[at] = make_float2(m, l);
+        if (!half && r < rows) a.ml[at] = make_float2(sub ? m2[1] : m2[0], l);
         asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");  // the sums have been read
-        fence_before();
       }
+      fence_before();
     }
   }
   __syncwarp();
@@ -580,7 +707,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
 }
 
 // ---------------------------------------------------------------- joining
-// One warp per (sequence, query head): the pieces of its prefix and of its own tokens.
+// One warp per (sequence, query head): the pieces of its prefix and of its own
+// tokens, 32 at a time: a lane's piece gives its maximum and sum, then the
+// warp adds up their outputs, eight loads in flight.
 template <int D>
 __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ SharedArgs a) {
   __shared__ Plan plan;
@@ -593,33 +722,64 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
   const int item = blockIdx.x * 8 + (threadIdx.x >> 5), s = item / Hq, hq = item % Hq, h = hq / a.G;
   if (item >= a.B * Hq || !a.part[s]) return;
   const int total = plan.cum[a.entries];
-  float m = -INFINITY, l = 0.f, o[V] = {};
+  int count[2] = {0, 0}, c0[2] = {0, 0}, row[2] = {0, 0};
+#pragma unroll
   for (int side = 0; side < 2; ++side) {
     if (side == 0 && a.prefix_seq[s] < 0) continue;
     const int e = side ? a.tail_entry[s] : a.prefix_entry[s];
-    const int r = hq % a.G + (side ? 0 : a.prefix_row[s]);
     const int units = entry_units(a, plan, e);
     if (!units) continue;
-    const int64_t u0 = plan.cum[e] + h * units + kItemUnits, u1 = plan.cum[e] + (h + 1) * units - 1;  // first and last tile
-    const int c1 = (int)(((u1 + 1) * a.P - 1) / total);
-    for (int c = (int)(((u0 + 1) * a.P - 1) / total); c <= c1; ++c) {
-      if (cta_unit(c, a.P, total) == cta_unit(c + 1, a.P, total)) continue;
-      const int64_t at = segment_row(a, e, h, c) + r;
-      const float2 w = __ldcg(a.ml + at);
-      const float top = fmaxf(m, w.x);
-      const float f = m == top ? 1.f : exp2_approx(m - top), f2 = w.x == top ? 1.f : exp2_approx(w.x - top);
-      l = l * f + w.y * f2;
+    // the CTAs that hold its first and its last tile
+    const int64_t u0 = plan.cum[e] + h * units + kItemUnits, u1 = plan.cum[e] + (h + 1) * units - 1;
+    c0[side] = (int)(((u0 + 1) * a.P - 1) / total);
+    count[side] = (int)(((u1 + 1) * a.P - 1) / total) - c0[side] + 1;
+    row[side] = segment_row(a, e, h, 0) + hq % a.G + (side ? 0 : a.prefix_row[s]);
+  }
+  float m = -INFINITY, l = 0.f, o[V] = {};
+  for (int x0 = 0; x0 < count[0] + count[1]; x0 += 32) {
+    const int x = x0 + lane, side = x >= count[0];
+    const int c = (side ? c0[1] - count[0] : c0[0]) + x;
+    const int at = (side ? row[1] : row[0]) + 256 * c;
+    // a CTA without units holds no piece
+    const bool some = x < count[0] + count[1] && cta_unit(c, a.P, total) < cta_unit(c + 1, a.P, total);
+    const float2 w = some ? __ldcg(a.ml + at) : make_float2(-INFINITY, 0.f);
+    const float top = fmaxf(m, warp_max(w.x));
+    const float f0 = m == top ? 1.f : exp2_approx(m - top), f = !some ? 0.f : w.x == top ? 1.f : exp2_approx(w.x - top);
+    l = l * f0 + warp_sum(w.y * f);
+    m = top;
 #pragma unroll
-      for (int i = 0; i < V; ++i) o[i] = o[i] * f + __ldcg(a.acc + at * D + i * 32 + lane) * f2;
-      m = top;
+    for (int i = 0; i < V; ++i) o[i] *= f0;
+    const unsigned have = __ballot_sync(0xffffffffu, some);
+    const int n = min(32, count[0] + count[1] - x0);
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) {
+      const float fj = __shfl_sync(0xffffffffu, f, j);
+      const float* src = a.acc + (int64_t)__shfl_sync(0xffffffffu, at, j) * D + lane * V;
+      float y[V] = {};
+      if (have >> j & 1) {
+        if (V == 4) {
+          const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
+          y[0] = t.x; y[1] = t.y; y[V - 2] = t.z; y[V - 1] = t.w;
+        } else {
+          const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
+          y[0] = t.x; y[1] = t.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = fmaf(y[i], fj, o[i]);
     }
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const float y = l > 0.f ? o[i] / l : l == 0.f ? 0.f : l;  // without a token: zero; NaN stays
-    const int64_t at = (int64_t)item * D + i * 32 + lane;
-    if (a.q_bf16) reinterpret_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
-    else reinterpret_cast<float*>(a.out)[at] = y;
+  for (int i = 0; i < V; ++i) o[i] = l > 0.f ? o[i] / l : l == 0.f ? 0.f : l;  // without a token: zero; NaN stays
+  const int64_t at = (int64_t)item * D + lane * V;
+  if (a.q_bf16) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2)
+      *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at + i) = __floats2bfloat162_rn(o[i], o[i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2)
+      *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + at + i) = make_float2(o[i], o[i + 1]);
   }
 }
 
