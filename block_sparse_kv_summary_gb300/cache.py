@@ -6,8 +6,6 @@ library.  Nothing here computes any part of the decode step.
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import compkv as C
@@ -16,11 +14,10 @@ BLOCK = 16
 
 
 def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 _TYPES = {torch.bfloat16: C.COMPKV_BF16, torch.float32: C.COMPKV_F32}
-_HERE = contextlib.nullcontext()
 
 
 class CompKVCache:
@@ -162,16 +159,19 @@ class CompKVCache:
         return out
 
     # ------------------------------------------------------------------ around the decode step
-    def _on(self):
-        """The cache's device as the current one (nothing to do where it is already)."""
-        return _HERE if torch.cuda.current_device() == self.device.index else torch.cuda.device(self.device)
+    # (these calls take microseconds, so their checks are written out for speed)
+    def _call(self, fn, *args):
+        """A library call with the cache's device as the current one."""
+        if torch._C._cuda_getDevice() == self.device.index:
+            fn(self.ctx, *args, _stream(self.device))
+        else:
+            with torch.cuda.device(self.device):
+                fn(self.ctx, *args, _stream(self.device))
 
-    def _rows_of(self, t, name, shape, dtypes):
-        """A tensor of the given shape whose last dimensions are contiguous; its rows may stand apart."""
-        if (t.device != self.device or t.dtype not in dtypes or tuple(t.shape) != tuple(shape)
-                or t.stride(-1) != 1 or (t.shape[0] > 1 and t.stride(0) < t.shape[1])):
-            raise ValueError(f"{name}: expected rows {tuple(shape)} of {' or '.join(map(str, dtypes))} on {self.device}, "
-                             f"got {t.dtype} {tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
+    def _is(self, t, name, dtype, shape):
+        """Address of a contiguous tensor of this type and shape."""
+        if t.dtype is not dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
+            self._t(t, name, dtype, shape)
         return t.data_ptr()
 
     def _rope_args(self, qkv, tokens, table, q_weight, k_weight, eps, positions, interleaved, q_dtype):
@@ -180,14 +180,18 @@ class CompKVCache:
             raise ValueError(f"q_dtype must be torch.float32 or torch.bfloat16, got {q_dtype}")
         if table.dim() != 2:
             raise ValueError(f"table must be [positions, rot_dim], got {tuple(table.shape)}")
-        at = self._rows_of(qkv, "qkv", (tokens, width), tuple(_TYPES))
-        stride = qkv.stride(0) if tokens > 1 else width
+        stride = qkv.stride()
+        if (qkv.dtype not in _TYPES or qkv.shape != (tokens, width) or qkv.device != self.device
+                or stride[1] != 1 or (tokens > 1 and stride[0] < width)):
+            raise ValueError(f"qkv: expected rows {(tokens, width)} of {' or '.join(map(str, _TYPES))} on {self.device}, "
+                             f"got {qkv.dtype} {tuple(qkv.shape)} with strides {stride} on {qkv.device}")
+        d = (self.d,)
         return C.compkv_rope_args(
-            at, _TYPES[qkv.dtype], stride, self._t(table, "table", torch.float32, table.shape), table.shape[0],
-            table.shape[1], 1 if interleaved else 0,
-            0 if q_weight is None else self._t(q_weight, "q_weight", torch.float32, (self.d,)),
-            0 if k_weight is None else self._t(k_weight, "k_weight", torch.float32, (self.d,)), eps,
-            0 if positions is None else self._t(positions, "positions", torch.int32, (tokens,)), _TYPES[q_dtype])
+            qkv.data_ptr(), _TYPES[qkv.dtype], stride[0] if tokens > 1 else width,
+            self._is(table, "table", torch.float32, table.shape), table.shape[0], table.shape[1], 1 if interleaved else 0,
+            None if q_weight is None else self._is(q_weight, "q_weight", torch.float32, d),
+            None if k_weight is None else self._is(k_weight, "k_weight", torch.float32, d), eps,
+            None if positions is None else self._is(positions, "positions", torch.int32, (tokens,)), _TYPES[q_dtype])
 
     def rope(self, layer, qkv, table, *, q_weight=None, k_weight=None, eps=1e-6, positions=None, interleaved=False,
              q_dtype=torch.float32, q=None, k_new=None, v_new=None):
@@ -198,12 +202,20 @@ class CompKVCache:
         sequences' lengths).  See include/compkv.h."""
         a = self._rope_args(qkv, self.batch, table, q_weight, k_weight, eps, positions, interleaved, q_dtype)
         dev = self.device
-        q = torch.empty((self.batch, self.Hkv * self.G, self.d), dtype=q_dtype, device=dev) if q is None else q
-        k_new = torch.empty((self.batch, self.Hkv, self.d), dtype=torch.bfloat16, device=dev) if k_new is None else k_new
-        v_new = torch.empty((self.batch, self.Hkv, self.d), dtype=torch.bfloat16, device=dev) if v_new is None else v_new
-        qp = self._t(q, "q", q_dtype, (self.batch, self.Hkv * self.G, self.d))
-        with self._on():
-            C.compkv_rope(self.ctx, layer, a, qp, self._kv(k_new, "k_new"), self._kv(v_new, "v_new"), _stream(dev))
+        qs, ks = (self.batch, self.Hkv * self.G, self.d), (self.batch, self.Hkv, self.d)
+        if q is None:
+            q = torch.empty(qs, dtype=q_dtype, device=dev)
+        else:
+            self._is(q, "q", q_dtype, qs)
+        if k_new is None:
+            k_new = torch.empty(ks, dtype=torch.bfloat16, device=dev)
+        else:
+            self._is(k_new, "k_new", torch.bfloat16, ks)
+        if v_new is None:
+            v_new = torch.empty(ks, dtype=torch.bfloat16, device=dev)
+        else:
+            self._is(v_new, "v_new", torch.bfloat16, ks)
+        self._call(C.compkv_rope, layer, a, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr())
         return q, k_new, v_new
 
     def prefill_qkv(self, layer, qkv, counts, table, *, starts=None, q_weight=None, k_weight=None, eps=1e-6,
@@ -212,23 +224,25 @@ class CompKVCache:
 
         qkv: [tokens, (Hq + 2 Hkv) d], the counts[s] tokens of every sequence one after another; they go to the
         slots from starts[s] (0) on.  positions: int32 [tokens] or None (the slots)."""
-        counts = [int(x) for x in counts]
-        starts = None if starts is None else [int(x) for x in starts]
+        counts, starts = C.ints(counts), C.ints(starts)
         if len(counts) != self.batch or (starts is not None and len(starts) != self.batch):
             raise ValueError(f"counts and starts need {self.batch} entries")
         tokens = sum(counts)
-        q = torch.empty((tokens, self.Hkv * self.G, self.d), dtype=q_dtype, device=self.device) if q is None else q
+        if min(counts) < 0:
+            raise ValueError(f"counts must not be negative, got {counts.tolist()}")
+        shape = (tokens, self.Hkv * self.G, self.d)
         a = self._rope_args(qkv, tokens, table, q_weight, k_weight, eps, positions, interleaved, q_dtype)
-        qp = self._t(q, "q", q_dtype, (tokens, self.Hkv * self.G, self.d))
-        if not tokens and min(counts) >= 0:
-            return q
-        with self._on():
-            C.compkv_prefill_qkv(self.ctx, layer, a, starts, counts, qp, _stream(self.device))
+        if q is None:
+            q = torch.empty(shape, dtype=q_dtype, device=self.device)
+        else:
+            self._is(q, "q", q_dtype, shape)
+        if tokens:
+            self._call(C.compkv_prefill_qkv, layer, a, starts, counts, q.data_ptr())
         return q
 
     def _pairs(self, src, dst, layers):
-        src = [int(x) for x in src]
-        dst = src if dst is None else [int(x) for x in dst]
+        src = C.ints(src)
+        dst = src if dst is None else C.ints(dst)
         if len(src) != len(dst):
             raise ValueError(f"src and dst must have one entry per pair, got {len(src)} and {len(dst)}")
         layer0, n = (0, self.num_layers) if layers is None else (int(layers[0]), int(layers[1]) - int(layers[0]))
@@ -238,11 +252,10 @@ class CompKVCache:
         """Copy the first lens[i] tokens (None or -1: all) of sequence src[i] to dst[i], summaries included, in
         the layers [layers[0], layers[1]) (None: every layer); src[i] == dst[i] cuts it in place."""
         src, dst, layer0, n = self._pairs(src, dst, layers)
-        lens = None if lens is None else [int(x) for x in lens]
+        lens = C.ints(lens)
         if lens is not None and len(lens) != len(src):
             raise ValueError(f"lens must have one entry per pair, got {len(lens)} for {len(src)}")
-        with self._on():
-            C.compkv_fork(self.ctx, layer0, n, src, dst, lens, _stream(self.device))
+        self._call(C.compkv_fork, layer0, n, src, dst, lens)
 
     def truncate(self, seqs, lens, layers=None):
         """Cut sequences to lens[i] tokens in place (0 frees them)."""
@@ -255,9 +268,8 @@ class CompKVCache:
         src, dst, layer0, n = self._pairs(range(self.batch) if src is None else src, dst, layers)
         if keep.dim() != 4:
             raise ValueError(f"keep must be [layers, pairs, Hkv, blocks], got {tuple(keep.shape)}")
-        kp = self._t(keep, "keep", torch.int32, (n, len(src), self.Hkv, keep.shape[3]))
-        with self._on():
-            C.compkv_compact(self.ctx, layer0, n, src, dst, kp, keep.shape[3], _stream(self.device))
+        kp = self._is(keep, "keep", torch.int32, (n, len(src), self.Hkv, keep.shape[3]))
+        self._call(C.compkv_compact, layer0, n, src, dst, kp, keep.shape[3])
 
     def shared_workspace(self):
         """The workspace of attend_shared, allocated on first use and kept."""
@@ -271,18 +283,20 @@ class CompKVCache:
         """Exact attention over a prefix that sequence prefix_seq[s] holds for sequence s (its first
         prefix_len[prefix_seq[s]] tokens) and over the sequence's own tokens; -1: no prefix, -2: no part.
         q: [B, Hq, d] fp32 or bf16; out has its type."""
-        prefix_seq, prefix_len = [int(x) for x in prefix_seq], [int(x) for x in prefix_len]
+        prefix_seq, prefix_len = C.ints(prefix_seq), C.ints(prefix_len)
         if len(prefix_seq) != self.batch or len(prefix_len) != self.batch:
             raise ValueError(f"prefix_seq and prefix_len need {self.batch} entries")
-        if q.dtype not in _TYPES:
-            raise ValueError(f"q must be torch.float32 or torch.bfloat16, got {q.dtype}")
-        shape = (self.batch, self.Hkv * self.G, self.d)
-        out = torch.empty(shape, dtype=q.dtype, device=self.device) if out is None else out
+        dtype, shape = q.dtype, (self.batch, self.Hkv * self.G, self.d)
+        if dtype not in _TYPES:
+            raise ValueError(f"q must be torch.float32 or torch.bfloat16, got {dtype}")
+        qp = self._is(q, "q", dtype, shape)
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=self.device)
+        else:
+            self._is(out, "out", dtype, shape)
         ws = self.shared_workspace()
-        with self._on():
-            C.compkv_attend_shared(self.ctx, layer, self._t(q, "q", q.dtype, shape), _TYPES[q.dtype], prefix_seq,
-                                   prefix_len, self._t(out, "out", q.dtype, shape), ws.data_ptr(), ws.numel(),
-                                   _stream(self.device))
+        self._call(C.compkv_attend_shared, layer, qp, _TYPES[dtype], prefix_seq, prefix_len, out.data_ptr(),
+                   ws.data_ptr(), ws.numel())
         return out
 
     def device_status(self) -> int:

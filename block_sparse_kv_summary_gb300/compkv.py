@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from ctypes import POINTER, c_char_p, c_int, c_int64, c_size_t, c_void_p
 
 from ._build import HEADER, LIB
@@ -74,14 +75,12 @@ _SIGNATURES = [
     ("compkv_decode_static", c_int, [POINTER(compkv_config), POINTER(compkv_buffers), c_int, c_void_p, c_void_p,
                                      c_void_p, c_void_p, c_void_p, c_void_p]),
     ("compkv_rope", c_int, [c_void_p, c_int, POINTER(compkv_rope_args), c_void_p, c_void_p, c_void_p, c_void_p]),
-    ("compkv_prefill_qkv", c_int, [c_void_p, c_int, POINTER(compkv_rope_args), POINTER(c_int), POINTER(c_int),
-                                   c_void_p, c_void_p]),
-    ("compkv_fork", c_int, [c_void_p, c_int, c_int, c_int, POINTER(c_int), POINTER(c_int), POINTER(c_int), c_void_p]),
-    ("compkv_compact", c_int, [c_void_p, c_int, c_int, c_int, POINTER(c_int), POINTER(c_int), c_void_p, c_int,
-                               c_void_p]),
+    ("compkv_prefill_qkv", c_int, [c_void_p, c_int, POINTER(compkv_rope_args), c_void_p, c_void_p, c_void_p, c_void_p]),
+    ("compkv_fork", c_int, [c_void_p, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p]),
+    ("compkv_compact", c_int, [c_void_p, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_int, c_void_p]),
     ("compkv_attend_shared_bytes", c_size_t, [POINTER(compkv_config)]),
-    ("compkv_attend_shared", c_int, [c_void_p, c_int, c_void_p, c_int, POINTER(c_int), POINTER(c_int), c_void_p,
-                                     c_void_p, c_size_t, c_void_p]),
+    ("compkv_attend_shared", c_int, [c_void_p, c_int, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
+                                     c_void_p]),
     ("compkv_device_status", c_int, [c_void_p, c_void_p]),
     ("compkv_launch_count", c_int64, [c_void_p]),
     ("compkv_selftest_wait_timeout", c_int, [c_void_p, c_void_p]),
@@ -214,30 +213,38 @@ def compkv_decode_static(cfg, bufs, layer, q, k_new, v_new, out, sel, stream):
                                       stream), "compkv_decode_static")
 
 
-def _ints(x):
-    return None if x is None else (c_int * len(x))(*x)
+def ints(x):
+    """Host int32 array of a list's integers (None: NULL); what the calls below take for one."""
+    return None if x is None else x if isinstance(x, array) else array("i", x)
+
+
+def _at(x):
+    return None if x is None else x.buffer_info()[0]
 
 
 def compkv_rope(ctx, layer, args, q, k_new, v_new, stream):
     """Norms and rotation of one token per sequence; args: a compkv_rope_args."""
-    _check(lib().compkv_rope(ctx, layer, ctypes.byref(args), q, k_new, v_new, stream), "compkv_rope")
+    st = lib().compkv_rope(ctx, layer, args, q, k_new, v_new, stream)
+    if st != COMPKV_OK:
+        _check(st, "compkv_rope")
 
 
 def compkv_prefill_qkv(ctx, layer, args, starts, counts, q, stream):
     """Norms and rotation of packed tokens, written into the cache with their summaries."""
-    _check(lib().compkv_prefill_qkv(ctx, layer, ctypes.byref(args), _ints(starts), _ints(counts), q, stream),
-           "compkv_prefill_qkv")
+    starts, counts = ints(starts), ints(counts)
+    _check(lib().compkv_prefill_qkv(ctx, layer, args, _at(starts), _at(counts), q, stream), "compkv_prefill_qkv")
 
 
 def compkv_fork(ctx, layer0, layers, src, dst, lens, stream):
     """Copy sequences src[i] to dst[i] (or cut them in place); lens None: whole."""
-    _check(lib().compkv_fork(ctx, layer0, layers, len(src), _ints(src), _ints(dst), _ints(lens), stream),
-           "compkv_fork")
+    src, dst, lens = ints(src), ints(dst), ints(lens)
+    _check(lib().compkv_fork(ctx, layer0, layers, len(src), _at(src), _at(dst), _at(lens), stream), "compkv_fork")
 
 
 def compkv_compact(ctx, layer0, layers, src, dst, keep, keep_blocks, stream):
     """Move the listed blocks of src[i] to the front of dst[i]; keep: device address."""
-    _check(lib().compkv_compact(ctx, layer0, layers, len(src), _ints(src), _ints(dst), keep, keep_blocks, stream),
+    src, dst = ints(src), ints(dst)
+    _check(lib().compkv_compact(ctx, layer0, layers, len(src), _at(src), _at(dst), keep, keep_blocks, stream),
            "compkv_compact")
 
 
@@ -246,7 +253,8 @@ def compkv_attend_shared_bytes(cfg: compkv_config) -> int:
 
 
 def compkv_attend_shared(ctx, layer, q, type, prefix_seq, prefix_len, out, workspace, workspace_bytes, stream):
-    _check(lib().compkv_attend_shared(ctx, layer, q, type, _ints(prefix_seq), _ints(prefix_len), out, workspace,
+    prefix_seq, prefix_len = ints(prefix_seq), ints(prefix_len)
+    _check(lib().compkv_attend_shared(ctx, layer, q, type, _at(prefix_seq), _at(prefix_len), out, workspace,
                                       workspace_bytes, stream), "compkv_attend_shared")
 
 

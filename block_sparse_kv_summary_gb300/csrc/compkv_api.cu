@@ -105,7 +105,7 @@ compkv_status make_layout(const compkv_config* c, Layout* L) {
     off = round256(off + bytes);
   };
   region(&L->off_status, 16);
-  region(&L->off_arrive, 16);
+  region(&L->off_arrive, 16);  // LayerArgs::arrive, and in its second half SharedArgs::arrivals
   region(&L->off_rec, (size_t)L->rec_cap * G * 4 * sizeof(float));
   region(&L->off_comp, (size_t)L->rec_cap * G * d * sizeof(float));
   region(&L->off_zs, (size_t)row * Gp * sizeof(float));
@@ -394,6 +394,10 @@ compkv_status launch_chain(compkv_ctx* c, int family, const LayerArgs& a, int mo
   return r;
 }
 
+int* status_word(const compkv_ctx* c) {
+  return reinterpret_cast<int*>(reinterpret_cast<char*>(c->buf.scratch) + c->lay.off_status);
+}
+
 // The arguments common to compkv_rope and compkv_prefill_qkv, checked.
 compkv_status rope_base(const compkv_ctx* c, int layer, const compkv_rope_args* r, const void* q, RopeArgs* out) {
   COMPKV_TRY(check_call(c, layer));
@@ -419,23 +423,23 @@ compkv_status rope_base(const compkv_ctx* c, int layer, const compkv_rope_args* 
   if (!(r->eps >= 0.f)) return fail(COMPKV_ERR_INVALID_ARG, "eps must be >= 0");
   if (r->interleaved != 0 && r->interleaved != 1)
     return fail(COMPKV_ERR_INVALID_ARG, "interleaved must be 0 or 1 (got %d)", r->interleaved);
-  RopeArgs a;
-  memset(&a, 0, sizeof(a));
-  const LayerArgs b = base_args(c, layer);
+  RopeArgs& a = *out;
+  const int64_t rows = c->lay.rows_per_layer * (int64_t)layer;
   a.qkv = r->qkv;
   a.stride = r->qkv_stride;
   a.table = r->table;
   a.q_weight = r->q_weight;
   a.k_weight = r->k_weight;
   a.positions = r->positions;
-  a.seq_len = b.seq_len;
-  a.status = b.status;
+  a.seq_len = c->buf.seq_len + (int64_t)layer * c->cfg.batch;
+  a.status = status_word(c);
   a.q = const_cast<void*>(q);
-  a.k = b.k;
-  a.v = b.v;
-  a.kbar = b.kbar;
-  a.vbar = b.vbar;
-  a.dbar = b.dbar;
+  a.k_new = a.v_new = nullptr;
+  a.k = reinterpret_cast<__nv_bfloat16*>(c->buf.k) + rows * kBlock * d;
+  a.v = reinterpret_cast<__nv_bfloat16*>(c->buf.v) + rows * kBlock * d;
+  a.kbar = c->buf.kbar + rows * d;
+  a.vbar = c->buf.vbar + rows * d;
+  a.dbar = c->buf.dbar + rows * c->cfg.r;
   a.eps = r->eps;
   a.in_f32 = r->qkv_type == COMPKV_F32;
   a.q_bf16 = r->q_type == COMPKV_BF16;
@@ -447,11 +451,6 @@ compkv_status rope_base(const compkv_ctx* c, int layer, const compkv_rope_args* 
   a.Hkv = Hkv;
   a.d = d;
   a.r = c->cfg.r;
-  for (int s = 0; s < a.B; ++s) {
-    a.seq_row0[s] = c->lay.seq_row0[s];
-    a.cap_blocks[s] = c->lay.cap_blocks[s];
-  }
-  *out = a;
   return COMPKV_OK;
 }
 
@@ -482,7 +481,7 @@ compkv_status page_base(const compkv_ctx* c, int layer0, int layers, int n, cons
   a.vbar = c->buf.vbar;
   a.dbar = c->buf.dbar;
   a.seq_len = c->buf.seq_len;
-  a.status = reinterpret_cast<int*>(reinterpret_cast<char*>(c->buf.scratch) + c->lay.off_status);
+  a.status = status_word(c);
   a.rows_per_layer = c->lay.rows_per_layer;
   a.layer0 = layer0;
   a.layers = layers;
@@ -715,29 +714,33 @@ compkv_status compkv_rope(compkv_ctx* c, int layer, const compkv_rope_args* args
 
 compkv_status compkv_prefill_qkv(compkv_ctx* c, int layer, const compkv_rope_args* args, const int* starts,
                                  const int* counts, void* q, void* stream) {
-  RopeArgs a;
+  RopePrefillArgs p;
+  RopeArgs& a = p.rope;
   COMPKV_TRY(rope_base(c, layer, args, q, &a));
   if (!counts) return fail(COMPKV_ERR_INVALID_ARG, "counts is NULL");
   int64_t tokens = 0, blocks = 0;
   for (int s = 0; s < a.B; ++s) {
-    const int start = starts ? starts[s] : 0, count = counts[s], cap = a.cap_blocks[s] * kBlock;
+    const int start = starts ? starts[s] : 0, count = counts[s], cap = c->lay.cap_blocks[s] * kBlock;
+    p.seq_row0[s] = c->lay.seq_row0[s];
+    p.cap_blocks[s] = c->lay.cap_blocks[s];
+    p.starts[s] = p.counts[s] = 0;
     if (count < 0) return fail(COMPKV_ERR_INVALID_ARG, "counts[%d] = %d is negative", s, count);
-    a.token0[s] = (int)tokens;
-    a.item0[s] = (int)blocks;
+    p.token0[s] = (int)tokens;
+    p.item0[s] = (int)blocks;
     if (!count) continue;
     if (start < 0) return fail(COMPKV_ERR_INVALID_ARG, "starts[%d] = %d is negative", s, start);
     if (start > cap || count > cap - start)
       return fail(COMPKV_ERR_CAPACITY, "tokens [%d, %d + %d) of sequence %d exceed its capacity %d", start, start, count, s, cap);
-    a.starts[s] = start;
-    a.counts[s] = count;
+    p.starts[s] = start;
+    p.counts[s] = count;
     tokens += count;
     blocks += (start + count - 1) / kBlock - start / kBlock + 1;
     if (tokens > 0x7fffffff) return fail(COMPKV_ERR_UNSUPPORTED_SHAPE, "more than 2^31 - 1 tokens in one call");
   }
-  a.item0[a.B] = (int)blocks;
+  p.item0[a.B] = (int)blocks;
   if (!blocks) return COMPKV_OK;
   cudaStream_t st = (cudaStream_t)stream;
-  return launch(c, COMPKV_KERNEL_PREFILL_QKV, st, "prefill launch", [&] { return launch_rope_prefill(a, st); });
+  return launch(c, COMPKV_KERNEL_PREFILL_QKV, st, "prefill launch", [&] { return launch_rope_prefill(p, st); });
 }
 
 compkv_status compkv_fork(compkv_ctx* c, int layer0, int layers, int n, const int* src, const int* dst, const int* lens,
@@ -823,24 +826,24 @@ compkv_status compkv_attend_shared(compkv_ctx* c, int layer, const void* q, int 
   if (!prefix_seq || !prefix_len) return fail(COMPKV_ERR_INVALID_ARG, "prefix_seq and prefix_len must not be NULL");
   if (c->kv_host || !c->tmap_ok) return fail(COMPKV_ERR_UNSUPPORTED_SHAPE, "compkv_attend_shared needs k and v in device memory");
   SharedArgs a;
-  memset(&a, 0, sizeof(a));
-  const LayerArgs b = base_args(c, layer);
-  a.seq_len = b.seq_len;
+  a.seq_len = c->buf.seq_len + (int64_t)layer * c->cfg.batch;
   a.q = q;
   a.out = out;
-  a.status = b.status;
+  a.status = status_word(c);
   a.q_bf16 = type == COMPKV_BF16;
   a.B = c->cfg.batch;
   a.Hkv = c->cfg.num_kv_heads;
   a.G = c->cfg.group_size;
   a.d = c->cfg.head_dim;
   a.P = device_sms() < kMaxSharedCtas ? device_sms() : kMaxSharedCtas;
-  a.layer_row0 = b.layer_row0;
+  a.layer_row0 = c->lay.rows_per_layer * (int64_t)layer;
   const size_t need = shared_workspace_bytes(a.B, a.Hkv, a.G, a.d);
   if (workspace_bytes < need)
     return fail(COMPKV_ERR_INVALID_ARG, "workspace_bytes %zu < required %zu", workspace_bytes, need);
   a.acc = reinterpret_cast<float*>(workspace);
+  a.arrivals = reinterpret_cast<unsigned long long*>(reinterpret_cast<char*>(c->buf.scratch) + c->lay.off_arrive + 8);
   a.ml = reinterpret_cast<float2*>(a.acc + shared_rows(a.B, a.Hkv, a.G) * a.d);
+  int members[kMaxBatch] = {};  // of a holder
   for (int s = 0; s < a.B; ++s) {
     const int p = prefix_seq[s];
     if (p < -2 || p >= a.B) return fail(COMPKV_ERR_INVALID_ARG, "prefix_seq[%d] = %d not in -2..%d", s, p, a.B - 1);
@@ -853,9 +856,11 @@ compkv_status compkv_attend_shared(compkv_ctx* c, int layer, const void* q, int 
       return fail(COMPKV_ERR_CAPACITY, "prefix_len[%d] = %d outside [0, %d]", p, prefix_len[p],
                   c->lay.cap_blocks[p] * kBlock);
     a.prefix_len[p] = prefix_len[p];
+    ++members[p];
   }
   // entries: the query rows of each prefix's sequences, 128 or 256 at a time, then every sequence's own tokens
-  int members = 0;
+  a.entries = 0;
+  a.row0[0] = 0;
   auto entry = [&](int holder, int rows) {
     a.holder[a.entries] = (unsigned char)holder;
     a.rows[a.entries] = (unsigned short)rows;
@@ -863,19 +868,23 @@ compkv_status compkv_attend_shared(compkv_ctx* c, int layer, const void* q, int 
     ++a.entries;
   };
   const int most = shared_entry_rows(a.q_bf16) / a.G;  // sequences of one entry
+  int first_entry[kMaxBatch], at[kMaxBatch], all = 0;  // of a holder; its next member's place
   for (int p = 0; p < a.B; ++p) {
-    int first = members;
-    for (int s = 0; s < a.B; ++s)
-      if (prefix_seq[s] == p) a.member[members++] = (unsigned char)s;
-    for (; first < members; first += most) {
-      const int n = members - first < most ? members - first : most;
-      for (int i = 0; i < n; ++i) {
-        a.prefix_entry[a.member[first + i]] = (unsigned char)a.entries;
-        a.prefix_row[a.member[first + i]] = (unsigned char)(i * a.G);
-      }
-      a.member0[a.entries] = (unsigned char)first;
-      entry(p, n * a.G);
+    first_entry[p] = a.entries;
+    at[p] = all;
+    for (int i = 0; i < members[p]; i += most) {
+      a.member0[a.entries] = (unsigned char)(all + i);
+      entry(p, (members[p] - i < most ? members[p] - i : most) * a.G);
     }
+    all += members[p];
+  }
+  for (int s = 0; s < a.B; ++s) {
+    const int p = a.prefix_seq[s];
+    if (p < 0) continue;
+    const int i = at[p]++, e0 = first_entry[p], of = i - a.member0[e0];
+    a.member[i] = (unsigned char)s;
+    a.prefix_entry[s] = (unsigned char)(e0 + of / most);
+    a.prefix_row[s] = (unsigned char)(of % most * a.G);
   }
   a.prefixes = a.entries;
   for (int s = 0; s < a.B; ++s) {
@@ -890,7 +899,7 @@ compkv_status compkv_attend_shared(compkv_ctx* c, int layer, const void* q, int 
   memcpy(a.v128, &c->tmap_v128, sizeof(CUtensorMap));
   cudaStream_t st = (cudaStream_t)stream;
   return launch(c, COMPKV_KERNEL_ATTEND_SHARED, st, "shared attention launch",
-                [&] { return launch_attend_shared(a, st); }, 2);
+                [&] { return launch_attend_shared(a, st); });
 }
 
 compkv_status compkv_device_status(compkv_ctx* c, void* stream) {

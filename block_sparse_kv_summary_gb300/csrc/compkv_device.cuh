@@ -108,7 +108,9 @@ struct RopeArgs {
   int in_f32, q_bf16, interleaved;
   int table_rows, rot;
   int B, Hq, Hkv, d, r;
-  // per sequence, for many tokens
+};
+struct RopePrefillArgs {       // many tokens, per sequence
+  RopeArgs rope;
   int64_t seq_row0[kMaxBatch];
   int cap_blocks[kMaxBatch];
   int starts[kMaxBatch];       // slot of its first token
@@ -152,7 +154,8 @@ struct SharedArgs {
   const void* q;               // [B][Hq][d] fp32, or bf16 where q_bf16
   void* out;                   // the same type
   float* acc;                  // workspace: [rows][d] unnormalised outputs of a segment's rows
-  float2* ml;                  // workspace: [rows] maximum (log2 units) and sum of its weights
+  float2* ml;                  // workspace: [rows] reference of its weights (log2 units) and their sum
+  unsigned long long* arrivals;  // CTAs that have left their pieces, over all calls of the context
   int* status;
   int q_bf16;
   int B, Hkv, G, d;

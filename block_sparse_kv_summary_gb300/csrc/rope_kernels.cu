@@ -266,17 +266,18 @@ __device__ __forceinline__ float token_sum(float x) {
 // also read the block's earlier tokens from the cache and form its summary
 // (two passes over registers: mean, then squared deviations from it).
 template <int D, typename T>
-__global__ void __launch_bounds__(256) rope_prefill_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(256) rope_prefill_kernel(const __grid_constant__ RopePrefillArgs g) {
+  const RopeArgs& a = g.rope;
   constexpr int LPH = D / 8, TPW = 32 / LPH, IT = kBlock / TPW;
   const int lane = threadIdx.x & 31, l = lane & (LPH - 1), sub = lane / LPH;
   int s = 0;
-  while (s + 1 < a.B && a.item0[s + 1] <= (int)blockIdx.x) ++s;
-  const int b = a.starts[s] / kBlock + ((int)blockIdx.x - a.item0[s]);
-  const int lo = max(a.starts[s] - b * kBlock, 0);                             // slots of this block that receive tokens:
-  const int hi = min(a.starts[s] + a.counts[s] - b * kBlock, kBlock);          // [lo, hi)
-  const int64_t tok0 = (int64_t)a.token0[s] + b * kBlock - a.starts[s];        // token of slot 0
+  while (s + 1 < a.B && g.item0[s + 1] <= (int)blockIdx.x) ++s;
+  const int b = g.starts[s] / kBlock + ((int)blockIdx.x - g.item0[s]);
+  const int lo = max(g.starts[s] - b * kBlock, 0);                             // slots of this block that receive tokens:
+  const int hi = min(g.starts[s] + g.counts[s] - b * kBlock, kBlock);          // [lo, hi)
+  const int64_t tok0 = (int64_t)g.token0[s] + b * kBlock - g.starts[s];        // token of slot 0
   const Pairing p = pairing<LPH>(lane, a.rot, a.interleaved);
-  if (blockIdx.x == a.item0[s] && threadIdx.x == 0) a.seq_len[s] = a.starts[s] + a.counts[s];
+  if (blockIdx.x == g.item0[s] && threadIdx.x == 0) a.seq_len[s] = g.starts[s] + g.counts[s];
 
   const float* row[IT];
 #pragma unroll
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(256) rope_prefill_kernel(const __grid_constant
       continue;
     }
     const bool is_k = h < a.Hq + a.Hkv;
-    const int64_t r = a.seq_row0[s] + (int64_t)(is_k ? h - a.Hq : h - a.Hq - a.Hkv) * a.cap_blocks[s] + b;
+    const int64_t r = g.seq_row0[s] + (int64_t)(is_k ? h - a.Hq : h - a.Hq - a.Hkv) * g.cap_blocks[s] + b;
     __nv_bfloat16* dst = (is_k ? a.k : a.v) + r * kBlock * D + 8 * l;
     if (is_k) weights8(a.k_weight, l, w);
     float t[IT][8], sum[8] = {};
@@ -363,9 +364,9 @@ __global__ void __launch_bounds__(256) rope_prefill_kernel(const __grid_constant
     const int gs = D / a.r;  // coordinates of a variance group: a power of two
     float* db = a.dbar + r * a.r;
     if (gs >= 8) {
-      float g = ((var[0] + var[1]) + (var[2] + var[3])) + ((var[4] + var[5]) + (var[6] + var[7]));
-      for (int o = gs / 16; o > 0; o >>= 1) g += __shfl_xor_sync(0xffffffffu, g, o);
-      if (sub == 0 && l % (gs / 8) == 0) db[l / (gs / 8)] = g / (float)gs;
+      float sum8 = ((var[0] + var[1]) + (var[2] + var[3])) + ((var[4] + var[5]) + (var[6] + var[7]));
+      for (int o = gs / 16; o > 0; o >>= 1) sum8 += __shfl_xor_sync(0xffffffffu, sum8, o);
+      if (sub == 0 && l % (gs / 8) == 0) db[l / (gs / 8)] = sum8 / (float)gs;
     } else if (sub == 0) {
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
@@ -398,15 +399,16 @@ cudaError_t launch_rope_step(const RopeArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_rope_prefill(const RopeArgs& a, cudaStream_t st) {
-  const unsigned grid = (unsigned)a.item0[a.B];
+cudaError_t launch_rope_prefill(const RopePrefillArgs& g, cudaStream_t st) {
+  const RopeArgs& a = g.rope;
+  const unsigned grid = (unsigned)g.item0[a.B];
   if (!grid) return cudaSuccess;
   if (a.d == 128) {
-    if (a.in_f32) rope_prefill_kernel<128, float><<<grid, 256, 0, st>>>(a);
-    else rope_prefill_kernel<128, __nv_bfloat16><<<grid, 256, 0, st>>>(a);
+    if (a.in_f32) rope_prefill_kernel<128, float><<<grid, 256, 0, st>>>(g);
+    else rope_prefill_kernel<128, __nv_bfloat16><<<grid, 256, 0, st>>>(g);
   } else {
-    if (a.in_f32) rope_prefill_kernel<64, float><<<grid, 256, 0, st>>>(a);
-    else rope_prefill_kernel<64, __nv_bfloat16><<<grid, 256, 0, st>>>(a);
+    if (a.in_f32) rope_prefill_kernel<64, float><<<grid, 256, 0, st>>>(g);
+    else rope_prefill_kernel<64, __nv_bfloat16><<<grid, 256, 0, st>>>(g);
   }
   return cudaGetLastError();
 }

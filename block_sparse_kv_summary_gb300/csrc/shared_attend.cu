@@ -15,11 +15,13 @@
 // steps a tile, one step in flight behind the other):
 //   warp 8   copies K and V tiles by tensor maps into a ring of stages,
 //   warp 9   issues S = Q K^T into one of two TMEM buffers and O += P V,
-//   warps 0-7 load Q, take the running maximum and sum (thread = row and half
-//            of the keys), and write the weights P over S in TMEM.
-// O stays in TMEM and is scaled only when a row's maximum rose by more than 8
-// (in powers of two): the weights then stay below 2^8, and what the final
-// division by their sum loses by that is nothing.
+//   warps 0-7 load Q, take the weights and their sum (thread = row and half of
+//            the keys), and write the weights P over S in TMEM.
+// Weights are e^(z - reference).  The reference is the row's maximum in the
+// piece's first tile and stays while the weights of a tile add up to less than
+// 2^30: floating point loses nothing by a common factor, and the join divides
+// it out.  Only where they do not is the tile's maximum taken, O scaled and
+// the tile done again, so that no other tile pays for a maximum.
 //
 // bf16 queries take one product each, and their weights are rounded to bf16,
 // as the result is.  fp32 queries and weights are split into three bf16 parts
@@ -38,13 +40,12 @@ namespace {
 constexpr int kTile = 128;                // keys of a tile, and query rows of an item at most
 constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = 32 * (kSoftmaxWarps + 4);  // registers are dealt out by groups of four warps
-constexpr int kItemUnits = 1;             // what starting an item costs, in tiles
-constexpr float kRescale = 8.f;           // log2 of the factor that a maximum may rise by before O is scaled
+constexpr float kMostWeight = 1073741824.f;  // 2^30: what a tile's weights of a row may add up to
 constexpr size_t kSmemLimit = 232448;
 
 // ---------------------------------------------------------------- the plan
-// Entry e has tiles + kItemUnits units per head (0 without tokens); CTA c of P
-// takes the units [c T / P, (c + 1) T / P) of the T units of all entries and
+// Entry e has item_units() + tiles units per head (0 without tokens); CTA c of
+// P takes the units [c T / P, (c + 1) T / P) of the T units of all entries and
 // heads, in order.
 struct Plan {
   int cum[kMaxSharedEntries + 1];         // units of all heads of the entries before e
@@ -63,6 +64,10 @@ __device__ __forceinline__ int entry_first(const SharedArgs& a, int e, int held)
   return e >= a.prefixes && a.prefix_seq[s] == s ? min(a.prefix_len[s], held) : 0;
 }
 
+// What an item costs besides its tiles, in tiles (1.5 us): loading its queries and leaving its outputs take
+// 2 us for a few rows and 9 us for 256.
+__device__ __forceinline__ int item_units(const SharedArgs& a, int e) { return 1 + a.rows[e] / 64; }
+
 // By one warp; the caller synchronises.
 __device__ void build_plan(const SharedArgs& a, Plan& p, int lane) {
   int base = 0;
@@ -74,7 +79,7 @@ __device__ void build_plan(const SharedArgs& a, Plan& p, int lane) {
       const int len = e < a.prefixes ? min(held, a.prefix_len[s]) : held - entry_first(a, e, held);
       if (e < a.prefixes && held < a.prefix_len[s]) set_error(a.status, kDevInvalidArg, s, -1, 5);
       p.last[e] = (unsigned char)((len + kTile - 1) % kTile + 1);
-      u = len ? ((len + kTile - 1) / kTile + kItemUnits) * a.Hkv : 0;
+      u = len ? ((len + kTile - 1) / kTile + item_units(a, e)) * a.Hkv : 0;
     }
     int x = u;
 #pragma unroll
@@ -110,11 +115,11 @@ struct Walk {
       const int per = entry_units(a, p, e), at = u - p.cum[e];
       g.e = e;
       g.h = at / per;
-      const int x = at - g.h * per, n = min(per - x, end - u);
+      const int x = at - g.h * per, n = min(per - x, end - u), start = item_units(a, e);
       u += n;
-      g.tile0 = max(x - kItemUnits, 0);
-      g.tile1 = x + n - kItemUnits;
-      g.tiles = per - kItemUnits;
+      g.tile0 = max(x - start, 0);
+      g.tile1 = x + n - start;
+      g.tiles = per - start;
       g.last = p.last[e];
       if (g.tile1 > g.tile0) return true;
     }
@@ -273,7 +278,7 @@ struct Shape {
 struct Control {
   Plan plan;
   unsigned char member[kMaxBatch];  // of the arguments: there a warp's lanes would read them one after another
-  float row_max[2][2][kTile];  // [tile & 1][half of the keys][row]; sums at the end of a segment
+  float row_max[2][kTile];  // [half of the keys][row]; sums at the end of a segment
   uint64_t full[8], empty[8], q_full, s_full[2], p_full[2], o_full[2];  // [tile & 1]
   uint32_t tmem;
   int abort;
@@ -307,57 +312,217 @@ __device__ __forceinline__ bool warp_wait(Control* ctl, uint64_t* bar, uint32_t 
   return ok;
 }
 
-// Rows of the segment's queries into shared memory, swizzled, in PARTS parts; by the softmax warps, with
-// several loads of a thread in flight.
+// Scores behind the last key.
+__device__ __forceinline__ void mask(float* s, int valid) {
+  if (valid < 64) {
+#pragma unroll
+    for (int i = 0; i < 64; ++i)
+      if (i >= valid) s[i] = -INFINITY;
+  }
+}
+// Weights 2^(scale s - m) in the place of 64 scores (m = -inf, before a piece's first tile: as if 0); their sum.
+__device__ __forceinline__ float weights(float* s, float scale, float m) {
+  const float ref = m == -INFINITY ? 0.f : m;
+  float2 sum[2] = {};
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float2 x = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), make_float2(scale, scale), make_float2(-ref, -ref));
+    s[2 * i] = exp2_approx(x.x);
+    s[2 * i + 1] = exp2_approx(x.y);
+    sum[i & 1] = __fadd2_rn(sum[i & 1], make_float2(s[2 * i], s[2 * i + 1]));
+  }
+  return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+}
+// Whether `p` holds for a lane of the two warps that meet at barrier `id`.
+__device__ __forceinline__ bool pair_any(int id, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %2, 0;\n\tbarrier.cta.red.or.pred b, %1, 64, a;\n\t"
+      "selp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)p)
+      : "memory");
+  return r != 0;
+}
+
+// A whole 32-byte sector: lanes write rows of their own, and half sectors would reach L2 one by one.
+__device__ __forceinline__ void store_sector(float* p, const float* x) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]),
+               "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+               : "memory");
+}
+
+// Rows of the segment's queries into shared memory, swizzled, in PARTS parts; by
+// the softmax warps.  A thread keeps its 16-byte column and goes down the
+// rows.  Written for few instructions (they are fetched cold here) and with all
+// loads in flight.
 template <int D, int PARTS>
 __device__ __forceinline__ void load_queries(const SharedArgs& a, const Control* ctl, const Segment& g, char* q_smem) {
-  constexpr int CH = D / 8;  // 16-byte chunks of 8 coordinates
-  constexpr int N = PARTS == 1 ? 8 : 4, W = PARTS == 1 ? 1 : 2, T = 32 * kSoftmaxWarps;
-  const int rows = a.rows[g.e], chunks = rows * CH, gs = 31 - __clz(a.G);
+  constexpr int CH = D / 8, STEP = 32 * kSoftmaxWarps / CH;  // chunks of 8 coordinates in a row; rows of a turn
+  const int rows = a.rows[g.e], gs = 31 - __clz(a.G), c = threadIdx.x % CH;
   const bool prefix = g.e < a.prefixes;
   const unsigned char* member = ctl->member + (prefix ? a.member0[g.e] : 0);
-  const int holder = a.holder[g.e];
-  const char* base = reinterpret_cast<const char*>(a.q) + (int64_t)g.h * a.G * (D * 2 * W);
-  for (int i0 = threadIdx.x; i0 < chunks; i0 += N * T) {
-    uint4 x[N][W];
-#pragma unroll
-    for (int u = 0; u < N; ++u) {
-      const int i = min(i0 + u * T, chunks - 1), r = i / CH;  // behind the last chunk: that one again
-      const int s = prefix ? member[r >> gs] : holder;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          base + ((int64_t)(s * a.Hkv * a.G + (r & (a.G - 1))) * D + 8 * (i % CH)) * (2 * W));
-#pragma unroll
-      for (int w = 0; w < W; ++w) x[u][w] = __ldg(src + w);
+  const int holder = a.holder[g.e], Hq = a.Hkv * a.G;
+  int r = threadIdx.x / CH;
+  char* to = q_smem + (c / 8) * Shape<D, PARTS>::kHalf + r * 128 + (((c % 8) ^ (r & 7)) << 4);  // STEP is a multiple of 8
+  auto source = [&](int r) {
+    const int s = prefix ? member[r >> gs] : holder;
+    return ((int64_t)s * Hq + g.h * a.G + (r & (a.G - 1))) * D + 8 * c;
+  };
+  if constexpr (PARTS == 1) {
+    for (; r < rows; r += STEP) {
+      cp_async16(to, reinterpret_cast<const __nv_bfloat16*>(a.q) + source(r));
+      to += STEP * 128;
+      if (r % kTile + STEP >= kTile) to += Shape<D, PARTS>::kStage - kTile * 128;  // the next 128 rows
     }
+    cp_async_wait_all();
+  } else {
+    // the 8 floats come into the places of the first two parts, and the thread that fetched them splits them
+    for (int i = r; i < rows; i += STEP) {
+      const float* src = reinterpret_cast<const float*>(a.q) + source(i);
+      char* at = to + (i - r) * 128;
+      cp_async16(at, src);
+      cp_async16(at + Shape<D, PARTS>::kStage, src + 4);
+    }
+    cp_async_wait_all();
+#pragma unroll 1
+    for (; r < rows; r += STEP, to += STEP * 128) {
+      float4 u = *reinterpret_cast<const float4*>(to), v = *reinterpret_cast<const float4*>(to + Shape<D, PARTS>::kStage);
 #pragma unroll
-    for (int u = 0; u < N; ++u) {
-      const int i = i0 + u * T, r = i / CH, c = i % CH;
-      if (i < chunks) {
-        char* to = q_smem + (r / kTile) * (PARTS * Shape<D, PARTS>::kStage) + (c / 8) * Shape<D, PARTS>::kHalf +
-                   (r % kTile) * 128 + (((c % 8) ^ (r & 7)) << 4);
-        if (PARTS == 1) {
-          *reinterpret_cast<uint4*>(to) = x[u][0];
+      for (int p = 0; p < PARTS; ++p)
+        *reinterpret_cast<uint4*>(to + p * Shape<D, PARTS>::kStage) =
+            make_uint4(split2(u.x, u.y), split2(u.z, u.w), split2(v.x, v.y), split2(v.z, v.w));
+    }
+  }
+}
+
+// Waits until every CTA of the grid has come here (the CTA's warps have: all
+// that it wrote to the workspace is done).  The count runs on from call to
+// call, a multiple of the CTAs between calls.
+__device__ __forceinline__ bool all_arrived(const SharedArgs& a, Control* ctl) {
+  if (threadIdx.x == 0) {
+    __threadfence();
+    const unsigned long long ticket = atomicAdd(a.arrivals, 1ull), goal = (ticket / a.P + 1) * a.P;
+    auto count = [&] {
+      unsigned long long v;
+      asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(a.arrivals) : "memory");
+      return v;
+    };
+    bool ok = count() >= goal;
+    const unsigned long long t0 = global_ns();
+    for (uint32_t i = 1; !ok && i < kWaitPolls; ++i) {
+      ok = count() >= goal;
+      if ((i & 31) == 0 && global_ns() - t0 > kWaitNs) break;
+    }
+    if (!ok) {
+      set_error(a.status, kDevTimeout, -1, -1, 59);
+      ctl->abort = 1;
+    }
+  }
+  __syncthreads();
+  return ctl->abort == 0;
+}
+
+// One query row by `share` warps of a CTA: the pieces of its prefix and of its
+// own tokens, 32 at a time: a lane's piece gives its reference and sum, then
+// the warp adds up their outputs, several loads in flight.  Warp `part` takes
+// every share-th piece; with share > 1 the CTA's warps come here together, and
+// the first of each row adds up what the others leave in `left`.
+template <int D>
+__device__ __forceinline__ void join_row(const SharedArgs& a, const Plan& plan, int item, int part, int share,
+                                         float* left, int lane) {
+  constexpr int V = D / 32;
+  const int Hq = a.Hkv * a.G;
+  const bool mine = item < a.B * Hq && a.part[item / Hq];
+  if (!mine) item = 0;
+  const int s = item / Hq, hq = item % Hq, h = hq / a.G;
+  const int total = plan.cum[a.entries];
+  int count[2] = {0, 0}, c0[2] = {0, 0}, row[2] = {0, 0};
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {
+    if (side == 0 && a.prefix_seq[s] < 0) continue;
+    const int e = side ? a.tail_entry[s] : a.prefix_entry[s];
+    const int units = entry_units(a, plan, e);
+    if (!units) continue;
+    // the CTAs that hold its first and its last tile
+    const int64_t u0 = plan.cum[e] + h * units + item_units(a, e), u1 = plan.cum[e] + (h + 1) * units - 1;
+    const int first = (int)(((u0 + 1) * a.P - 1) / total), last = (int)(((u1 + 1) * a.P - 1) / total);
+    const int r = segment_row(a, e, h, 0) + hq % a.G + (side ? 0 : a.prefix_row[s]);
+    c0[0] = side ? c0[0] : first;
+    count[0] = side ? count[0] : last - first + 1;
+    row[0] = side ? row[0] : r;
+    c0[1] = first;
+    count[1] = side ? last - first + 1 : 0;
+    row[1] = r;
+  }
+  float m = -INFINITY, l = 0.f, o[V] = {};
+  const int pieces = mine ? count[0] + count[1] : 0;
+#pragma unroll 1
+  for (int x0 = part; x0 < pieces; x0 += 32 * share) {
+    const int x = x0 + lane * share, side = x >= count[0];
+    const int c = (side ? c0[1] - count[0] : c0[0]) + x;
+    const int at = (side ? row[1] : row[0]) + 256 * c;
+    // a CTA without units holds no piece
+    const bool some = x < pieces && cta_unit(c, a.P, total) < cta_unit(c + 1, a.P, total);
+    const float2 w = some ? __ldcg(a.ml + at) : make_float2(-INFINITY, 0.f);
+    const float top = fmaxf(m, warp_max(w.x));
+    const float f0 = m == top ? 1.f : exp2_approx(m - top), f = !some ? 0.f : w.x == top ? 1.f : exp2_approx(w.x - top);
+    l = l * f0 + warp_sum(w.y * f);
+    m = top;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] *= f0;
+    const unsigned have = __ballot_sync(0xffffffffu, some);
+    const int n = min(32, (pieces - x0 + share - 1) / share);
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) {
+      const float fj = __shfl_sync(0xffffffffu, f, j);
+      const float* src = a.acc + (int64_t)__shfl_sync(0xffffffffu, at, j) * D + lane * V;
+      float y[V] = {};
+      if (have >> j & 1) {
+        if (V == 4) {
+          const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
+          y[0] = t.x; y[1] = t.y; y[V - 2] = t.z; y[V - 1] = t.w;
         } else {
-          float f[8];
-#pragma unroll
-          for (int w = 0; w < W; ++w) {
-            f[4 * w] = __uint_as_float(x[u][w].x);
-            f[4 * w + 1] = __uint_as_float(x[u][w].y);
-            f[4 * w + 2] = __uint_as_float(x[u][w].z);
-            f[4 * w + 3] = __uint_as_float(x[u][w].w);
-          }
-#pragma unroll
-          for (int p = 0; p < PARTS; ++p) {
-            uint4 w;
-            w.x = split2(f[0], f[1]);
-            w.y = split2(f[2], f[3]);
-            w.z = split2(f[4], f[5]);
-            w.w = split2(f[6], f[7]);
-            *reinterpret_cast<uint4*>(to + p * Shape<D, PARTS>::kStage) = w;
-          }
+          const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
+          y[0] = t.x; y[1] = t.y;
         }
       }
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = fmaf(y[i], fj, o[i]);
     }
+  }
+  if (share > 1) {  // [warp][D + 2]
+    float* own = left + (threadIdx.x >> 5) * (D + 2);
+#pragma unroll
+    for (int i = 0; i < V; ++i) own[lane * V + i] = o[i];
+    if (lane == 0) {
+      own[D] = m;
+      own[D + 1] = l;
+    }
+    __syncthreads();
+    for (int w = 1; w < share && part == 0; ++w) {
+      const float* x = own + w * (D + 2);
+      const float top = fmaxf(m, x[D]);
+      const float f0 = m == top ? 1.f : exp2_approx(m - top), f = x[D] == top ? 1.f : exp2_approx(x[D] - top);
+      l = l * f0 + x[D + 1] * f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = o[i] * f0 + x[lane * V + i] * f;
+      m = top;
+    }
+    __syncthreads();
+  }
+  if (!mine || part) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i) o[i] = l > 0.f ? o[i] / l : l == 0.f ? 0.f : l;  // without a token: zero; NaN stays
+  const int64_t at = (int64_t)item * D + lane * V;
+  if (a.q_bf16) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2)
+      *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at + i) = __floats2bfloat162_rn(o[i], o[i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2)
+      *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + at + i) = make_float2(o[i], o[i + 1]);
   }
 }
 
@@ -402,7 +567,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
   fence_before();
   __syncthreads();
   fence_after();
-  pdl_trigger();
   const uint32_t tmem = ctl->tmem;
   const int c = blockIdx.x;
   Walk walk(a, ctl->plan, c);
@@ -568,28 +732,29 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             float s[64];
             tmem_ld64(buf + half * 64, s);
             const int valid = cur.valid(t) - half * 64;  // keys of this half
-            if (valid < 64) {
-#pragma unroll
-              for (int i = 0; i < 64; ++i)
-                if (i >= valid) s[i] = -INFINITY;
-            }
-            float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-            for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-            const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-            ctl->row_max[n & 1][half][row] = mine;
-            fence_before();
-            asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");  // both halves have read S, too
-            fence_after();
-            const float top = fmaxf(mine, ctl->row_max[n & 1][half ^ 1][row]);
+            mask(s, valid);
             float m = sub ? m2[1] : m2[0], l = sub ? l2[1] : l2[0], f = 1.f;
-            // holds for a segment's first tile: m = -inf
-            const bool raise = __any_sync(0xffffffffu, sub * kTile + row < rows && top > m + kRescale);
+            float sum = weights(s, scale, m);
+            // both halves have read S when they have passed, and P may take its place
+            fence_before();
+            bool raise = pair_any(1 + (warp & 3), sub * kTile + row < rows && (t == cur.tile0 || !(sum < kMostWeight)));
+            fence_after();
             if (raise) {
-              const float next = top > m + kRescale ? top : m;
-              f = m == next ? 1.f : exp2_approx(m - next);
-              m = next;
-              l *= f;
+              tmem_ld64(buf + half * 64, s);
+              mask(s, valid);
+              float top = s[0];
+#pragma unroll
+              for (int i = 1; i < 64; ++i) top = fmaxf(top, s[i]);
+              ctl->row_max[half][row] = top * scale;
+              fence_before();
+              asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
+              fence_after();
+              top = fmaxf(fmaxf(top * scale, ctl->row_max[half ^ 1][row]), m);
+              if (top == -INFINITY) top = 0.f;
+              f = exp2_approx(m - top);  // 0 in the first tile: m = -inf
+              m = top;
+              l = t == cur.tile0 ? 0.f : l * f;
+              sum = weights(s, scale, m);
               if (!S::kTileO && t > cur.tile0) {
                 // O of the tile before is complete (with two steps a tile: S was issued behind its product),
                 // and the next product into it waits for p_full
@@ -604,17 +769,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                   tmem_st32(o_at + 32 * x, reinterpret_cast<const uint32_t*>(o));
                 }
               }
+              asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");  // the maxima have been read
             }
-            const float ref = m == -INFINITY ? 0.f : m;
-            float2 sum[2] = {};
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float2 x = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), make_float2(scale, scale), make_float2(-ref, -ref));
-              s[2 * i] = exp2_approx(x.x);
-              s[2 * i + 1] = exp2_approx(x.y);
-              sum[i & 1] = __fadd2_rn(sum[i & 1], make_float2(s[2 * i], s[2 * i + 1]));
-            }
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            l += sum;
             if (sub) {
               m2[1] = m;
               l2[1] = l;
@@ -669,9 +826,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         const int r = sub * kTile + row;
         if (sub * kTile + (warp & 3) * 32 >= rows) break;
         float l = sub ? l2[1] : l2[0];
-        if (half) ctl->row_max[sub][0][row] = l;
+        if (half) ctl->row_max[0][row] = l;
         asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
-        if (!half) l += ctl->row_max[sub][0][row];
+        if (!half) l += ctl->row_max[0][row];
         const int64_t at = segment_row(a, cur.e, cur.h, c) + r;
         float* dst = a.acc + at * D + half * (D / 2);
 #pragma unroll
@@ -684,8 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
           }
           if (r < rows) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              reinterpret_cast<float4*>(dst + 32 * x)[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int i = 0; i < 4; ++i) store_sector(dst + 32 * x + 8 * i, o + 8 * i);
           }
         }
         if (!half && r < rows) a.ml[at] = make_float2(sub ? m2[1] : m2[0], l);
@@ -704,100 +860,28 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
   fence_after();
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kColumns) : "memory");
-}
-
-// ---------------------------------------------------------------- joining
-// One warp per (sequence, query head): the pieces of its prefix and of its own
-// tokens, 32 at a time: a lane's piece gives its maximum and sum, then the
-// warp adds up their outputs, eight loads in flight.
-template <int D>
-__global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ SharedArgs a) {
-  __shared__ Plan plan;
-  constexpr int V = D / 32;
-  const int lane = threadIdx.x & 31;
-  if (threadIdx.x < 32) build_plan(a, plan, lane);
-  __syncthreads();
-  pdl_wait();
-  const int Hq = a.Hkv * a.G;
-  const int item = blockIdx.x * 8 + (threadIdx.x >> 5), s = item / Hq, hq = item % Hq, h = hq / a.G;
-  if (item >= a.B * Hq || !a.part[s]) return;
-  const int total = plan.cum[a.entries];
-  int count[2] = {0, 0}, c0[2] = {0, 0}, row[2] = {0, 0};
-#pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    if (side == 0 && a.prefix_seq[s] < 0) continue;
-    const int e = side ? a.tail_entry[s] : a.prefix_entry[s];
-    const int units = entry_units(a, plan, e);
-    if (!units) continue;
-    // the CTAs that hold its first and its last tile
-    const int64_t u0 = plan.cum[e] + h * units + kItemUnits, u1 = plan.cum[e] + (h + 1) * units - 1;
-    c0[side] = (int)(((u0 + 1) * a.P - 1) / total);
-    count[side] = (int)(((u1 + 1) * a.P - 1) / total) - c0[side] + 1;
-    row[side] = segment_row(a, e, h, 0) + hq % a.G + (side ? 0 : a.prefix_row[s]);
-  }
-  float m = -INFINITY, l = 0.f, o[V] = {};
-  for (int x0 = 0; x0 < count[0] + count[1]; x0 += 32) {
-    const int x = x0 + lane, side = x >= count[0];
-    const int c = (side ? c0[1] - count[0] : c0[0]) + x;
-    const int at = (side ? row[1] : row[0]) + 256 * c;
-    // a CTA without units holds no piece
-    const bool some = x < count[0] + count[1] && cta_unit(c, a.P, total) < cta_unit(c + 1, a.P, total);
-    const float2 w = some ? __ldcg(a.ml + at) : make_float2(-INFINITY, 0.f);
-    const float top = fmaxf(m, warp_max(w.x));
-    const float f0 = m == top ? 1.f : exp2_approx(m - top), f = !some ? 0.f : w.x == top ? 1.f : exp2_approx(w.x - top);
-    l = l * f0 + warp_sum(w.y * f);
-    m = top;
-#pragma unroll
-    for (int i = 0; i < V; ++i) o[i] *= f0;
-    const unsigned have = __ballot_sync(0xffffffffu, some);
-    const int n = min(32, count[0] + count[1] - x0);
-#pragma unroll 8
-    for (int j = 0; j < n; ++j) {
-      const float fj = __shfl_sync(0xffffffffu, f, j);
-      const float* src = a.acc + (int64_t)__shfl_sync(0xffffffffu, at, j) * D + lane * V;
-      float y[V] = {};
-      if (have >> j & 1) {
-        if (V == 4) {
-          const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
-          y[0] = t.x; y[1] = t.y; y[V - 2] = t.z; y[V - 1] = t.w;
-        } else {
-          const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
-          y[0] = t.x; y[1] = t.y;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < V; ++i) o[i] = fmaf(y[i], fj, o[i]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i) o[i] = l > 0.f ? o[i] / l : l == 0.f ? 0.f : l;  // without a token: zero; NaN stays
-  const int64_t at = (int64_t)item * D + lane * V;
-  if (a.q_bf16) {
-#pragma unroll
-    for (int i = 0; i < V; i += 2)
-      *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at + i) = __floats2bfloat162_rn(o[i], o[i + 1]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; i += 2)
-      *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + at + i) = make_float2(o[i], o[i + 1]);
-  }
+  if (!all_arrived(a, ctl)) return;
+  // rows are dealt to the CTAs; few rows leave several warps for each
+  constexpr int kWarps = kThreads / 32;
+  const int rows = a.B * a.Hkv * a.G, share = rows * 12 <= a.P * kWarps ? 12 : rows * 4 <= a.P * kWarps ? 4 : 1;
+  static_assert(kWarps == 12, "warps of a row");
+  for (int r0 = blockIdx.x * (kWarps / share); r0 < rows; r0 += a.P * (kWarps / share))
+    join_row<D>(a, ctl->plan, r0 + warp / share, warp % share, share, reinterpret_cast<float*>(ring), lane);
 }
 
 template <int D, int PARTS>
 cudaError_t launch(const SharedArgs& a, cudaStream_t st) {
-  shared_attend_kernel<D, PARTS><<<a.P, kThreads, smem_bytes<D, PARTS>(), st>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = (a.B * a.Hkv * a.G + 7) / 8;
-  cfg.blockDim = 256;
+  cfg.gridDim = a.P;
+  cfg.blockDim = kThreads;
+  cfg.dynamicSmemBytes = smem_bytes<D, PARTS>();
   cfg.stream = st;
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[0].id = cudaLaunchAttributeCooperative;  // its CTAs wait for one another
+  at[0].val.cooperative = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared_join_kernel<D>, a);
+  return cudaLaunchKernelEx(&cfg, shared_attend_kernel<D, PARTS>, a);
 }
 
 }  // namespace
