@@ -161,20 +161,21 @@ struct SharedArgs {
   int B, Hkv, G, d;
   int P;                       // CTAs of the attention kernel
   int prefixes, entries;       // entries of prefixes, and all
-  int64_t layer_row0;          // first row of this layer in the whole cache
-  int64_t seq_row0[kMaxBatch];
-  int cap_blocks[kMaxBatch];
-  int prefix_len[kMaxBatch];   // of a holder: tokens of its prefix
-  signed char part[kMaxBatch];        // of a sequence: 1 takes part
-  signed char prefix_seq[kMaxBatch];  // the sequence that holds its prefix, or < 0
-  unsigned char member[kMaxBatch];    // sequences in the order of their prefixes
-  unsigned char tail_entry[kMaxBatch];    // of a sequence: its own entry, and its rows in a prefix's:
-  unsigned char prefix_entry[kMaxBatch];  // the entry
-  unsigned char prefix_row[kMaxBatch];    // and the first row, below 256
-  unsigned char holder[kMaxSharedEntries];   // of an entry: the sequence whose tokens it reads
+  // per sequence
+  signed char part[kMaxBatch];           // it takes part
+  unsigned char member[kMaxBatch];       // sequences in the order of their prefixes
+  unsigned char own_entry[kMaxBatch];    // its own tokens' entry
+  short prefix_entry[kMaxBatch];         // its prefix's entry (-1: none), and its first row there
+  unsigned char prefix_row[kMaxBatch];
+  // per entry
+  unsigned char holder[kMaxSharedEntries];   // the sequence whose tokens it reads
   unsigned char member0[kMaxPrefixEntries];  // its first row's place in `member`
   unsigned short rows[kMaxSharedEntries];    // query rows per head, 1..256
   int row0[kMaxSharedEntries + 1];           // rows of all heads of the entries before it
+  int cap[kMaxSharedEntries];                // the holder's capacity: slots from head to head
+  int skip[kMaxSharedEntries];               // the holder's tokens in front of it
+  int most[kMaxSharedEntries];               // its tokens at most, those in front counted
+  int token0[kMaxSharedEntries];             // its first token of head 0 in the whole cache
   // tensor maps of the whole K and V caches, boxes of 64 x 16 and of 64 x 128 with the 128-byte swizzle
   alignas(64) unsigned long long k16[16];
   alignas(64) unsigned long long v16[16];

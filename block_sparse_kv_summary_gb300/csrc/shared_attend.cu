@@ -14,7 +14,8 @@
 // Within a CTA (tcgen05; a step is one K/V tile times 128 rows, one or two
 // steps a tile, one step in flight behind the other):
 //   warp 8   copies K and V tiles by tensor maps into a ring of stages,
-//   warp 9   issues S = Q K^T into one of two TMEM buffers and O += P V,
+//   warp 9   issues S = Q K^T into one of two TMEM buffers,
+//   warp 10  issues O += P V,
 //   warps 0-7 load Q, take the weights and their sum (thread = row and half of
 //            the keys), and write the weights P over S in TMEM.
 // Weights are e^(z - reference).  The reference is the row's maximum in the
@@ -44,30 +45,21 @@ constexpr float kMostWeight = 1073741824.f;  // 2^30: what a tile's weights of a
 constexpr size_t kSmemLimit = 232448;
 
 // ---------------------------------------------------------------- the plan
-// Entry e has item_units() + tiles units per head (0 without tokens); CTA c of
-// P takes the units [c T / P, (c + 1) T / P) of the T units of all entries and
-// heads, in order.
+// Work is dealt in units of half a microsecond: a tile costs two of them, or
+// three with more than 128 rows (measured 1.0 and 1.7 us); an item costs some
+// more, for its queries and its outputs (measured 2 us for a few rows and 7 us
+// for 256).  CTA c of P takes the units [c T / P, (c + 1) T / P) of the T
+// units of all entries and heads, in order, and the tiles that begin there.
 struct Plan {
   int cum[kMaxSharedEntries + 1];         // units of all heads of the entries before e
   unsigned char last[kMaxSharedEntries];  // keys of its last tile
 };
 
-__device__ __forceinline__ int held_tokens(const SharedArgs& a, int s) {
-  return max(0, min(__ldcg(a.seq_len + s), a.cap_blocks[s] * kBlock));
-}
+__device__ __forceinline__ int tile_units(const SharedArgs& a, int e) { return a.rows[e] > kTile ? 3 : 2; }
+__device__ __forceinline__ int item_units(const SharedArgs& a, int e) { return 4 + a.rows[e] / 32; }
 __device__ __forceinline__ int entry_units(const SharedArgs& a, const Plan& p, int e) {  // per head
   return (p.cum[e + 1] - p.cum[e]) / a.Hkv;
 }
-// First token of an entry in its sequence: a holder's own tokens begin behind its prefix.
-__device__ __forceinline__ int entry_first(const SharedArgs& a, int e, int held) {
-  const int s = a.holder[e];
-  return e >= a.prefixes && a.prefix_seq[s] == s ? min(a.prefix_len[s], held) : 0;
-}
-
-// What an item costs besides its tiles, in tiles (1.5 us): loading its queries and leaving its outputs take
-// 2 us for a few rows and 9 us for 256.
-__device__ __forceinline__ int item_units(const SharedArgs& a, int e) { return 1 + a.rows[e] / 64; }
-
 // By one warp; the caller synchronises.
 __device__ void build_plan(const SharedArgs& a, Plan& p, int lane) {
   int base = 0;
@@ -75,11 +67,11 @@ __device__ void build_plan(const SharedArgs& a, Plan& p, int lane) {
     const int e = e0 + lane;
     int u = 0;
     if (e < a.entries) {
-      const int s = a.holder[e], held = held_tokens(a, s);
-      const int len = e < a.prefixes ? min(held, a.prefix_len[s]) : held - entry_first(a, e, held);
-      if (e < a.prefixes && held < a.prefix_len[s]) set_error(a.status, kDevInvalidArg, s, -1, 5);
+      const int held = max(0, min(__ldcg(a.seq_len + a.holder[e]), a.cap[e])), most = a.most[e];
+      const int len = max(0, min(held, most) - a.skip[e]);
+      if (e < a.prefixes && held < most) set_error(a.status, kDevInvalidArg, a.holder[e], -1, 5);
       p.last[e] = (unsigned char)((len + kTile - 1) % kTile + 1);
-      u = len ? ((len + kTile - 1) / kTile + item_units(a, e)) * a.Hkv : 0;
+      u = len ? ((len + kTile - 1) / kTile * tile_units(a, e) + item_units(a, e)) * a.Hkv : 0;
     }
     int x = u;
 #pragma unroll
@@ -94,6 +86,15 @@ __device__ void build_plan(const SharedArgs& a, Plan& p, int lane) {
 }
 
 __device__ __forceinline__ int cta_unit(int c, int P, int total) { return (int)((int64_t)total * c / P); }
+
+// The tiles [from, to) of an item that begin in the units [x, y) of the item.
+struct Tiles {
+  int from, to;
+};
+__device__ __forceinline__ Tiles tiles_between(const SharedArgs& a, int e, int x, int y) {
+  const int w = tile_units(a, e), start = item_units(a, e);
+  return {max(x - start + w - 1, 0) / w, max(y - start + w - 1, 0) / w};
+}
 
 // Walks the segments (pieces of items) of one CTA; every role walks alike.
 struct Segment {
@@ -115,11 +116,12 @@ struct Walk {
       const int per = entry_units(a, p, e), at = u - p.cum[e];
       g.e = e;
       g.h = at / per;
-      const int x = at - g.h * per, n = min(per - x, end - u), start = item_units(a, e);
+      const int x = at - g.h * per, n = min(per - x, end - u);
+      const Tiles t = tiles_between(a, e, x, x + n);
       u += n;
-      g.tile0 = max(x - start, 0);
-      g.tile1 = x + n - start;
-      g.tiles = per - start;
+      g.tile0 = t.from;
+      g.tile1 = t.to;
+      g.tiles = (per - item_units(a, e)) / tile_units(a, e);
       g.last = p.last[e];
       if (g.tile1 > g.tile0) return true;
     }
@@ -177,6 +179,9 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t lead) {
       "r"(lead)
       : "memory");
 }
+// A value that all lanes hold, in a form that the compiler knows to be uniform: operands of tcgen05 stand in
+// uniform registers, and moving each there anew costs as much as the product.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 // Registers of this warp from here on; every warp of its group of four says the same.
 template <int N>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -437,23 +442,18 @@ __device__ __forceinline__ void join_row(const SharedArgs& a, const Plan& plan, 
   if (!mine) item = 0;
   const int s = item / Hq, hq = item % Hq, h = hq / a.G;
   const int total = plan.cum[a.entries];
-  int count[2] = {0, 0}, c0[2] = {0, 0}, row[2] = {0, 0};
+  int count[2] = {0, 0}, c0[2] = {0, 0}, row[2] = {0, 0}, entry[2] = {0, 0}, begin[2] = {0, 0};
 #pragma unroll 1
   for (int side = 0; side < 2; ++side) {
-    if (side == 0 && a.prefix_seq[s] < 0) continue;
-    const int e = side ? a.tail_entry[s] : a.prefix_entry[s];
-    const int units = entry_units(a, plan, e);
+    if (side == 0 && a.prefix_entry[s] < 0) continue;
+    const int e = side ? a.own_entry[s] : a.prefix_entry[s];
+    const int units = entry_units(a, plan, e), b = plan.cum[e] + h * units;
     if (!units) continue;
-    // the CTAs that hold its first and its last tile
-    const int64_t u0 = plan.cum[e] + h * units + item_units(a, e), u1 = plan.cum[e] + (h + 1) * units - 1;
-    const int first = (int)(((u0 + 1) * a.P - 1) / total), last = (int)(((u1 + 1) * a.P - 1) / total);
+    // the CTAs that hold its first and its last unit
+    const int first = (int)(((int64_t)(b + 1) * a.P - 1) / total), last = (int)(((int64_t)(b + units) * a.P - 1) / total);
     const int r = segment_row(a, e, h, 0) + hq % a.G + (side ? 0 : a.prefix_row[s]);
-    c0[0] = side ? c0[0] : first;
-    count[0] = side ? count[0] : last - first + 1;
-    row[0] = side ? row[0] : r;
-    c0[1] = first;
-    count[1] = side ? last - first + 1 : 0;
-    row[1] = r;
+    if (!side) count[0] = last - first + 1, c0[0] = first, row[0] = r, entry[0] = e, begin[0] = b;
+    else count[1] = last - first + 1, c0[1] = first, row[1] = r, entry[1] = e, begin[1] = b;
   }
   float m = -INFINITY, l = 0.f, o[V] = {};
   const int pieces = mine ? count[0] + count[1] : 0;
@@ -462,8 +462,10 @@ __device__ __forceinline__ void join_row(const SharedArgs& a, const Plan& plan, 
     const int x = x0 + lane * share, side = x >= count[0];
     const int c = (side ? c0[1] - count[0] : c0[0]) + x;
     const int at = (side ? row[1] : row[0]) + 256 * c;
-    // a CTA without units holds no piece
-    const bool some = x < pieces && cta_unit(c, a.P, total) < cta_unit(c + 1, a.P, total);
+    // a CTA in which no tile begins holds no piece
+    const int b = side ? begin[1] : begin[0], e = side ? entry[1] : entry[0], units = entry_units(a, plan, e);
+    const Tiles t = tiles_between(a, e, max(cta_unit(c, a.P, total) - b, 0), min(cta_unit(c + 1, a.P, total) - b, units));
+    const bool some = x < pieces && t.from < t.to;
     const float2 w = some ? __ldcg(a.ml + at) : make_float2(-INFINITY, 0.f);
     const float top = fmaxf(m, warp_max(w.x));
     const float f0 = m == top ? 1.f : exp2_approx(m - top), f = !some ? 0.f : w.x == top ? 1.f : exp2_approx(w.x - top);
@@ -579,11 +581,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
       if (lane == 0) {
         int slot = 0, phase = 0;
         while (walk.next(a, ctl->plan, g)) {
-          const int s = a.holder[g.e];
-          const int64_t tok = (a.layer_row0 + a.seq_row0[s] + (int64_t)g.h * a.cap_blocks[s]) * kBlock +
-                              entry_first(a, g.e, held_tokens(a, s));
+          const int tok = a.token0[g.e] + g.h * a.cap[g.e];
           for (int t = g.tile0; t < g.tile1; ++t) {
-            const int valid = g.valid(t), y = (int)(tok + (int64_t)t * kTile);
+            const int valid = g.valid(t), y = tok + t * kTile;
             for (int kv = 0; kv < 2; ++kv) {
               if (wait(ctl, &ctl->empty[slot], phase ^ 1, a.status, 51)) {
                 char* dst = ring + slot * S::kStage;
@@ -611,97 +611,92 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         }
       }
     } else if (warp == kSoftmaxWarps + 1) {
-      // ---- products: S of step n is issued ahead of O += P V of step n - 1
+      // ---- S = Q K^T of every step, into the buffer whose weights the step before last has used up
       const uint32_t q_addr = smem_u32(q_smem), ring_addr = smem_u32(ring), lead = elect_leader();
       int n = 0, segs = 0;      // steps and segments before this one
-      int slot = 0, phase = 0;  // of the next tile in the ring
-      // the step whose P V is still to come
-      bool pending = false, v_first = false, v_last = false;  // O starts with it; it is the tile's last
-      int v_slot = 0, v_phase = 0, v_valid = 0, v_sub = 0;
-      auto issue_pv = [&] {  // of step n - 1
-        const uint32_t v = ring_addr + v_slot * S::kStage;
-        if (v_sub == 0) {
-          warp_wait(ctl, &ctl->full[v_slot], v_phase, a.status, 52);
-          if (v_valid % kBlock) {  // weights behind the last key are zero, but 0 x NaN is not
-            const int upto = (v_valid + kBlock - 1) / kBlock * kBlock;
-            for (int i = lane; i < (upto - v_valid) * (D / 8); i += 32) {
-              const int r = v_valid + i / (D / 8), ch = i % (D / 8);
-              *reinterpret_cast<uint4*>(ring + v_slot * S::kStage + (ch / 8) * S::kHalf + r * 128 + (ch % 8) * 16) =
-                  make_uint4(0, 0, 0, 0);
-            }
-            fence_async_smem();
-            __syncwarp();
-          }
-        }
-        const bool ok = warp_wait(ctl, &ctl->p_full[(n - 1) & 1], ((n - 1) >> 1) & 1, a.status, 53);
-        fence_after();
-        if (ok) {
-          const uint32_t p = tmem + ((n - 1) & 1) * S::kBuffer, o = tmem + S::kO + v_sub * D;
-          const uint64_t vd = operand(v, S::kHalf, 1024);
-          const bool add = !(v_first || S::kTileO);
-          if (v_valid == kTile) {
-#pragma unroll
-            for (int part = PARTS - 1; part >= 0; --part)
-#pragma unroll
-              for (int k = 0; k < kTile / 16; ++k)
-                mma_ts(o, p + part * 64 + k * 8, vd + k * (16 * 128 / 16), instruction(D, true),
-                       part < PARTS - 1 || k > 0 || add, lead);
-          } else {
-            for (int part = PARTS - 1; part >= 0; --part)
-              for (int k = 0; k < (v_valid + 15) / 16; ++k)
-                mma_ts(o, p + part * 64 + k * 8, vd + k * (16 * 128 / 16), instruction(D, true),
-                       part < PARTS - 1 || k > 0 || add, lead);
-          }
-          if (v_last) mma_commit(&ctl->empty[v_slot], lead);
-          mma_commit(&ctl->o_full[(n - 1) & 1], lead);
-        }
-        pending = false;
-      };
+      int slot = 0, phase = 0;  // of the tile in the ring
       while (walk.next(a, ctl->plan, g)) {
         const int subs = (a.rows[g.e] + kTile - 1) / kTile;
-        if (pending) issue_pv();
         warp_wait(ctl, &ctl->q_full, segs & 1, a.status, 54);
         ++segs;
         for (int t = g.tile0; t < g.tile1; ++t) {
-          const bool ok = warp_wait(ctl, &ctl->full[slot], phase, a.status, 55);
-          const uint32_t k = ring_addr + slot * S::kStage;
-          const int k_slot = slot;
-          if (++slot == STAGES) {
-            slot = 0;
-            phase ^= 1;
-          }
-          for (int sub = 0; sub < subs; ++sub) {
+          bool ok = warp_wait(ctl, &ctl->full[slot], phase, a.status, 55);
+          const uint64_t kd = operand(uniform(ring_addr + slot * S::kStage), 16, 1024);
+          for (int sub = 0; sub < subs; ++sub, ++n) {
+            const uint64_t qd = operand(uniform(q_addr + sub * (PARTS * S::kStage)), 16, 1024);
+            const uint32_t d = uniform(tmem + (n & 1) * S::kBuffer);
+            if (n >= 2) ok &= warp_wait(ctl, &ctl->o_full[n & 1], ((n >> 1) - 1) & 1, a.status, 53);
             fence_after();
             if (ok) {
-              const uint64_t qd = operand(q_addr + sub * (PARTS * S::kStage), 16, 1024), kd = operand(k, 16, 1024);
 #pragma unroll
               for (int part = PARTS - 1; part >= 0; --part)
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                   const uint32_t off = (i / 4) * S::kHalf + (i % 4) * 32;
-                  mma_ss(tmem + (n & 1) * S::kBuffer, qd + (part * S::kStage + off) / 16, kd + off / 16,
-                         instruction(kTile, false), part < PARTS - 1 || i > 0, lead);
+                  mma_ss(d, qd + (part * S::kStage + off) / 16, kd + off / 16, instruction(kTile, false),
+                         part < PARTS - 1 || i > 0, lead);
                 }
-              if (sub == subs - 1) mma_commit(&ctl->empty[k_slot], lead);
               mma_commit(&ctl->s_full[n & 1], lead);
+              if (sub == subs - 1) mma_commit(&ctl->empty[slot], lead);
             }
-            if (pending) issue_pv();
-            v_slot = slot;
-            v_phase = phase;
-            v_valid = g.valid(t);
-            v_first = t == g.tile0;
-            v_sub = sub;
-            v_last = sub == subs - 1;
-            pending = true;
-            ++n;
           }
-          if (++slot == STAGES) {
-            slot = 0;
+          slot += 2;
+          if (slot >= STAGES) {
+            slot -= STAGES;
             phase ^= 1;
           }
         }
       }
-      if (pending) issue_pv();
+    } else if (warp == kSoftmaxWarps + 2) {
+      // ---- O += P V of every step; a warp of its own, so that waiting for weights holds up no scores
+      const uint32_t ring_addr = smem_u32(ring), lead = elect_leader();
+      int n = 0, slot = 1, phase = 0;
+      while (walk.next(a, ctl->plan, g)) {
+        const int subs = (a.rows[g.e] + kTile - 1) / kTile;
+        for (int t = g.tile0; t < g.tile1; ++t) {
+          bool ok = warp_wait(ctl, &ctl->full[slot], phase, a.status, 52);
+          const int valid = g.valid(t);
+          if (valid % kBlock) {  // weights behind the last key are zero, but 0 x NaN is not
+            const int upto = (valid + kBlock - 1) / kBlock * kBlock;
+            for (int i = lane; i < (upto - valid) * (D / 8); i += 32) {
+              const int r = valid + i / (D / 8), ch = i % (D / 8);
+              *reinterpret_cast<uint4*>(ring + slot * S::kStage + (ch / 8) * S::kHalf + r * 128 + (ch % 8) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            fence_async_smem();
+            __syncwarp();
+          }
+          const uint64_t vd = operand(uniform(ring_addr + slot * S::kStage), S::kHalf, 1024);
+          for (int sub = 0; sub < subs; ++sub, ++n) {
+            const uint32_t p = uniform(tmem + (n & 1) * S::kBuffer), o = uniform(tmem + S::kO + sub * D);
+            const bool add = !(t == g.tile0 || S::kTileO);
+            ok &= warp_wait(ctl, &ctl->p_full[n & 1], (n >> 1) & 1, a.status, 53);
+            fence_after();
+            if (ok) {
+              if (valid == kTile) {
+#pragma unroll
+                for (int part = PARTS - 1; part >= 0; --part)
+#pragma unroll
+                  for (int k = 0; k < kTile / 16; ++k)
+                    mma_ts(o, p + part * 64 + k * 8, vd + k * (16 * 128 / 16), instruction(D, true),
+                           part < PARTS - 1 || k > 0 || add, lead);
+              } else {
+                for (int part = PARTS - 1; part >= 0; --part)
+                  for (int k = 0; k < (valid + 15) / 16; ++k)
+                    mma_ts(o, p + part * 64 + k * 8, vd + k * (16 * 128 / 16), instruction(D, true),
+                           part < PARTS - 1 || k > 0 || add, lead);
+              }
+              mma_commit(&ctl->o_full[n & 1], lead);
+              if (sub == subs - 1) mma_commit(&ctl->empty[slot], lead);
+            }
+          }
+          slot += 2;
+          if (slot >= STAGES) {
+            slot -= STAGES;
+            phase ^= 1;
+          }
+        }
+      }
     }
   } else {
     more_registers<216>();
