@@ -262,7 +262,6 @@ LayerArgs base_args(const compkv_ctx* c, int layer) {
   static_assert(sizeof(a.tmap_k) == sizeof(CUtensorMap), "tensor map size");
   memcpy(a.tmap_k, &c->tmap_k, sizeof(CUtensorMap));
   memcpy(a.tmap_v, &c->tmap_v, sizeof(CUtensorMap));
-  a.layer_row0 = c->lay.rows_per_layer * (int64_t)layer;
   a.kv_host = c->kv_host;
   a.tmap_ok = c->tmap_ok;
   const int d = c->cfg.head_dim, r = c->cfg.r, G = c->cfg.group_size;
@@ -740,7 +739,7 @@ compkv_status compkv_prefill_qkv(compkv_ctx* c, int layer, const compkv_rope_arg
   p.item0[a.B] = (int)blocks;
   if (!blocks) return COMPKV_OK;
   cudaStream_t st = (cudaStream_t)stream;
-  return launch(c, COMPKV_KERNEL_PREFILL_QKV, st, "prefill launch", [&] { return launch_rope_prefill(p, st); });
+  return launch(c, COMPKV_KERNEL_PREFILL_QKV, st, "prefill launch", [&] { return launch_rope_prefill(p, device_sms(), st); });
 }
 
 compkv_status compkv_fork(compkv_ctx* c, int layer0, int layers, int n, const int* src, const int* dst, const int* lens,
@@ -836,7 +835,6 @@ compkv_status compkv_attend_shared(compkv_ctx* c, int layer, const void* q, int 
   a.G = c->cfg.group_size;
   a.d = c->cfg.head_dim;
   a.P = device_sms() < kMaxSharedCtas ? device_sms() : kMaxSharedCtas;
-  a.layer_row0 = c->lay.rows_per_layer * (int64_t)layer;
   const size_t need = shared_workspace_bytes(a.B, a.Hkv, a.G, a.d);
   if (workspace_bytes < need)
     return fail(COMPKV_ERR_INVALID_ARG, "workspace_bytes %zu < required %zu", workspace_bytes, need);
@@ -847,25 +845,27 @@ compkv_status compkv_attend_shared(compkv_ctx* c, int layer, const void* q, int 
   for (int s = 0; s < a.B; ++s) {
     const int p = prefix_seq[s];
     if (p < -2 || p >= a.B) return fail(COMPKV_ERR_INVALID_ARG, "prefix_seq[%d] = %d not in -2..%d", s, p, a.B - 1);
-    a.seq_row0[s] = c->lay.seq_row0[s];
-    a.cap_blocks[s] = c->lay.cap_blocks[s];
-    a.prefix_seq[s] = (signed char)p;
     a.part[s] = p != -2;
+    a.prefix_entry[s] = -1;
     if (p < 0) continue;
     if (prefix_len[p] < 0 || prefix_len[p] > c->lay.cap_blocks[p] * kBlock)
       return fail(COMPKV_ERR_CAPACITY, "prefix_len[%d] = %d outside [0, %d]", p, prefix_len[p],
                   c->lay.cap_blocks[p] * kBlock);
-    a.prefix_len[p] = prefix_len[p];
     ++members[p];
   }
   // entries: the query rows of each prefix's sequences, 128 or 256 at a time, then every sequence's own tokens
   a.entries = 0;
   a.row0[0] = 0;
-  auto entry = [&](int holder, int rows) {
-    a.holder[a.entries] = (unsigned char)holder;
-    a.rows[a.entries] = (unsigned short)rows;
-    a.row0[a.entries + 1] = a.row0[a.entries] + rows * a.Hkv;
-    ++a.entries;
+  auto entry = [&](int holder, int rows, int skip, int most) {
+    const int e = a.entries++, cap = c->lay.cap_blocks[holder] * kBlock;
+    a.holder[e] = (unsigned char)holder;
+    a.rows[e] = (unsigned short)rows;
+    a.row0[e + 1] = a.row0[e] + rows * a.Hkv;
+    a.cap[e] = cap;
+    a.skip[e] = skip;
+    a.most[e] = most;
+    // below 2^31 tokens (make_tensor_maps)
+    a.token0[e] = (int)((c->lay.rows_per_layer * layer + c->lay.seq_row0[holder]) * kBlock) + skip;
   };
   const int most = shared_entry_rows(a.q_bf16) / a.G;  // sequences of one entry
   int first_entry[kMaxBatch], at[kMaxBatch], all = 0;  // of a holder; its next member's place
@@ -874,23 +874,23 @@ compkv_status compkv_attend_shared(compkv_ctx* c, int layer, const void* q, int 
     at[p] = all;
     for (int i = 0; i < members[p]; i += most) {
       a.member0[a.entries] = (unsigned char)(all + i);
-      entry(p, (members[p] - i < most ? members[p] - i : most) * a.G);
+      entry(p, (members[p] - i < most ? members[p] - i : most) * a.G, 0, prefix_len[p]);
     }
     all += members[p];
   }
   for (int s = 0; s < a.B; ++s) {
-    const int p = a.prefix_seq[s];
+    const int p = prefix_seq[s];
     if (p < 0) continue;
     const int i = at[p]++, e0 = first_entry[p], of = i - a.member0[e0];
     a.member[i] = (unsigned char)s;
-    a.prefix_entry[s] = (unsigned char)(e0 + of / most);
+    a.prefix_entry[s] = (short)(e0 + of / most);
     a.prefix_row[s] = (unsigned char)(of % most * a.G);
   }
   a.prefixes = a.entries;
   for (int s = 0; s < a.B; ++s) {
     if (!a.part[s]) continue;
-    a.tail_entry[s] = (unsigned char)a.entries;
-    entry(s, a.G);
+    a.own_entry[s] = (unsigned char)a.entries;
+    entry(s, a.G, prefix_seq[s] == s ? prefix_len[s] : 0, c->lay.cap_blocks[s] * kBlock);
   }
   if (!a.entries) return COMPKV_OK;
   memcpy(a.k16, &c->tmap_k, sizeof(CUtensorMap));

@@ -29,7 +29,7 @@ cudaError_t launch_stage_in(void* d0, const void* s0, size_t b0, void* d1, const
                             const void* s2, size_t b2, cudaStream_t st);
 // Norms and rotation of the projection's heads: one token per sequence, or many into the cache.
 cudaError_t launch_rope_step(const RopeArgs& a, cudaStream_t st);
-cudaError_t launch_rope_prefill(const RopePrefillArgs& a, cudaStream_t st);
+cudaError_t launch_rope_prefill(const RopePrefillArgs& a, int sms, cudaStream_t st);
 // Pages: copies between sequences, and listed blocks to the front of a sequence.
 constexpr int kForkBlocks = 16;  // blocks of one work item of a copy
 inline int fork_chunks(int blocks) { return blocks < 1 ? 1 : (blocks + kForkBlocks - 1) / kForkBlocks; }

@@ -130,33 +130,41 @@ __device__ __forceinline__ F2 turn2(F2 u, float c, F2 v, float s) {
   return add2(p, q);
 }
 
+// 1 / sqrt(mean(x^2) + eps) of the head whose coordinates these lanes hold, in two floats: one step of Newton's
+// iteration on rsqrtf with its residual 1 - m r^2 in two floats.
+template <int D>
+__device__ __forceinline__ F2 inverse_norm(const float* x, float eps) {
+  F2 s = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s = add2(s, two_prod(x[i], x[i]));
+#pragma unroll
+  for (int o = D / 16; o > 0; o >>= 1)
+    s = add2(s, {__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)});
+  s.hi *= 1.f / D;  // exact: D is a power of two
+  s.lo *= 1.f / D;
+  const F2 m = add2(s, {eps, 0.f});
+  const float r0 = rsqrtf(m.hi);
+  const F2 h = two_prod(m.hi, r0);
+  const float e = __fmaf_rn(-h.hi, r0, 1.f) - (h.lo + m.lo * r0) * r0;
+  return {r0, isfinite(r0) ? 0.5f * r0 * e : 0.f};
+}
+// x w r
+__device__ __forceinline__ F2 scaled(float x, float w, F2 r) {
+  const F2 t = two_prod(x, w);
+  F2 y = two_prod(t.hi, r.hi);
+  y.lo = __fmaf_rn(t.hi, r.lo, __fmaf_rn(t.lo, r.hi, y.lo));
+  return y;
+}
+
 // The same with two floats per value, rounded to fp32 and then to bf16.
 template <int D>
 __device__ __forceinline__ void head_bf16(const float* x, const float* w, const float* row, const RopeArgs& a,
                                           Pairing p, __nv_bfloat16* out) {
-  constexpr int LPH = D / 8;
   F2 y[8];
   if (w) {
-    F2 s = {0.f, 0.f};
+    const F2 r = inverse_norm<D>(x, a.eps);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = add2(s, two_prod(x[i], x[i]));
-#pragma unroll
-    for (int o = LPH / 2; o > 0; o >>= 1)
-      s = add2(s, {__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)});
-    s.hi *= 1.f / D;  // exact: D is a power of two
-    s.lo *= 1.f / D;
-    const F2 m = add2(s, {a.eps, 0.f});
-    // r = r0 + r1, one step of Newton's iteration on r0 with the residual 1 - m r0^2 in two floats
-    const float r0 = rsqrtf(m.hi);
-    const F2 h = two_prod(m.hi, r0);
-    const float e = __fmaf_rn(-h.hi, r0, 1.f) - (h.lo + m.lo * r0) * r0;
-    const float r1 = isfinite(r0) ? 0.5f * r0 * e : 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const F2 t = two_prod(x[i], w[i]);
-      y[i] = two_prod(t.hi, r0);
-      y[i].lo = __fmaf_rn(t.hi, r1, __fmaf_rn(t.lo, r0, y[i].lo));
-    }
+    for (int i = 0; i < 8; ++i) y[i] = scaled(x[i], w[i], r);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = {x[i], 0.f};
@@ -253,133 +261,288 @@ __global__ void __launch_bounds__(128) rope_step_kernel(const __grid_constant__ 
   }
 }
 
-// Sum over the lanes that hold the same coordinates of different tokens.
-template <int LPH>
-__device__ __forceinline__ float token_sum(float x) {
+// Many tokens: a lane's part of one token's rotation, the same for all heads.
+//   y_i = x_i cos_i + o_i sin_i,  o_i the other coordinate of the pair, the sign in sin_i
+template <int D>
+struct Turn {
+  float c[8], s[8];
+  int partner;   // the lane that holds the o_i; interleaved pairs are in the lane itself
+  bool inside;   // interleaved
+  __device__ __forceinline__ Turn(const RopeArgs& a, const float* row, int lane) {
+    const Pairing p = pairing<D / 8>(lane, a.rot, a.interleaved);
+    partner = p.partner;
+    inside = a.interleaved;
+    if (!p.rotated) {
 #pragma unroll
-  for (int o = LPH; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-
-// Many tokens.  One CTA per 16-token cache block that receives tokens, one
-// warp per head and turn: 32 / (D/8) tokens at a time.  Key and value warps
-// also read the block's earlier tokens from the cache and form its summary
-// (two passes over registers: mean, then squared deviations from it).
-template <int D, typename T>
-__global__ void __launch_bounds__(256) rope_prefill_kernel(const __grid_constant__ RopePrefillArgs g) {
-  const RopeArgs& a = g.rope;
-  constexpr int LPH = D / 8, TPW = 32 / LPH, IT = kBlock / TPW;
-  const int lane = threadIdx.x & 31, l = lane & (LPH - 1), sub = lane / LPH;
-  int s = 0;
-  while (s + 1 < a.B && g.item0[s + 1] <= (int)blockIdx.x) ++s;
-  const int b = g.starts[s] / kBlock + ((int)blockIdx.x - g.item0[s]);
-  const int lo = max(g.starts[s] - b * kBlock, 0);                             // slots of this block that receive tokens:
-  const int hi = min(g.starts[s] + g.counts[s] - b * kBlock, kBlock);          // [lo, hi)
-  const int64_t tok0 = (int64_t)g.token0[s] + b * kBlock - g.starts[s];        // token of slot 0
-  const Pairing p = pairing<LPH>(lane, a.rot, a.interleaved);
-  if (blockIdx.x == g.item0[s] && threadIdx.x == 0) a.seq_len[s] = g.starts[s] + g.counts[s];
-
-  const float* row[IT];
+      for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
+    } else if (inside) {
+      const float4 u = __ldg(reinterpret_cast<const float4*>(row + p.col));
+      const float4 v = __ldg(reinterpret_cast<const float4*>(row + a.rot / 2 + p.col));
+      const float cc[4] = {u.x, u.y, u.z, u.w}, ss[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    const int j = i * TPW + sub;
-    const bool live = j >= lo && j < hi;
-    const int pos = !live ? 0 : a.positions ? __ldg(a.positions + tok0 + j) : b * kBlock + j;
-    row[i] = table_row(a, pos, s, live && threadIdx.x < 32 && l == 0);
+      for (int i = 0; i < 4; ++i) {
+        c[2 * i] = c[2 * i + 1] = cc[i];
+        s[2 * i] = -ss[i];
+        s[2 * i + 1] = ss[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 u = __ldg(reinterpret_cast<const float4*>(row + p.col) + i);
+        const float4 v = __ldg(reinterpret_cast<const float4*>(row + a.rot / 2 + p.col) + i);
+        const float sign = p.first ? -1.f : 1.f;
+        c[4 * i] = u.x, c[4 * i + 1] = u.y, c[4 * i + 2] = u.z, c[4 * i + 3] = u.w;
+        s[4 * i] = sign * v.x, s[4 * i + 1] = sign * v.y, s[4 * i + 2] = sign * v.z, s[4 * i + 3] = sign * v.w;
+      }
+    }
   }
-  const int heads = a.Hq + 2 * a.Hkv;
-  for (int h = threadIdx.x >> 5; h < heads; h += blockDim.x >> 5) {
-    const T* src = reinterpret_cast<const T*>(a.qkv) + tok0 * a.stride + h * D + 8 * l;
-    float w[8];
-    if (h < a.Hq) {
-      weights8(a.q_weight, l, w);
+  // Weights of this lane's coordinates and of their partners.
+  __device__ __forceinline__ void weights(const float* w, int lane, float* own, float* other) const {
+    weights8(w, lane & (D / 8 - 1), own);
+    if (inside) {
 #pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        const int j = i * TPW + sub;
-        const bool live = j >= lo && j < hi;
-        float x[8] = {};
-        if (live) load8<T>(src + j * a.stride, x);
-        head_f32<D>(x, a.q_weight ? w : nullptr, row[i], a, p);
-        if (live) store_q(a, ((tok0 + j) * a.Hq + h) * D + 8 * l, x);
-      }
-      continue;
+      for (int i = 0; i < 8; ++i) other[i] = own[i ^ 1];
+    } else {
+      weights8(w, partner & (D / 8 - 1), other);
     }
-    const bool is_k = h < a.Hq + a.Hkv;
-    const int64_t r = g.seq_row0[s] + (int64_t)(is_k ? h - a.Hq : h - a.Hq - a.Hkv) * g.cap_blocks[s] + b;
-    __nv_bfloat16* dst = (is_k ? a.k : a.v) + r * kBlock * D + 8 * l;
-    if (is_k) weights8(a.k_weight, l, w);
-    float t[IT][8], sum[8] = {};
+  }
+};
+
+// 8 coordinates as they come.
+template <typename T>
+struct Raw {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p, bool live) {
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int j = i * TPW + sub;
-      const bool live = j >= lo && j < hi;
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (j < lo) u = __ldcg(reinterpret_cast<const uint4*>(dst + j * D));
-      float x[8] = {};
-      if (live) load8<T>(src + j * a.stride, x);
-      __nv_bfloat16 z[8];
-      if (is_k) {
-        head_bf16<D>(x, a.k_weight ? w : nullptr, row[i], a, p, z);
-      } else {
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+      v[i] = live ? __ldcs(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ Raw from(int lane) const {
+    Raw r;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) z[c] = __float2bfloat16_rn(x[c]);
-      }
-      if (live) {
-        u = pack8(z);
-        __stcs(reinterpret_cast<uint4*>(dst + j * D), u);
-      }
-      const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        t[i][2 * c] = __uint_as_float(v[c] << 16);
-        t[i][2 * c + 1] = __uint_as_float(v[c] & 0xffff0000u);
-      }
-      if (j < hi) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c) sum[c] += t[i][c];
-      }
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      r.v[i].x = __shfl_sync(0xffffffffu, v[i].x, lane);
+      r.v[i].y = __shfl_sync(0xffffffffu, v[i].y, lane);
+      r.v[i].z = __shfl_sync(0xffffffffu, v[i].z, lane);
+      r.v[i].w = __shfl_sync(0xffffffffu, v[i].w, lane);
     }
-    const float n = (float)hi;
+    return r;
+  }
+  __device__ __forceinline__ void floats(float* x) const {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) sum[c] = token_sum<LPH>(sum[c]) / n;
-    float* bar = (is_k ? a.kbar : a.vbar) + r * D + 8 * l;
-    if (sub == 0) {
-      reinterpret_cast<float4*>(bar)[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
-      reinterpret_cast<float4*>(bar)[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
-    }
-    if (!is_k) continue;
-    float var[8] = {};
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      if (i * TPW + sub < hi) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const float dlt = t[i][c] - sum[c];
-          var[c] = fmaf(dlt, dlt, var[c]);
+      for (int k = 0; k < 4; ++k) {
+        if (sizeof(T) == 2) {
+          x[2 * k] = __uint_as_float(w[k] << 16);
+          x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        } else {
+          x[4 * i + k] = __uint_as_float(w[k]);
         }
       }
     }
+  }
+};
+
+// The lane's coordinates and their partners'.
+template <int D, typename T>
+__device__ __forceinline__ void pairs(const Raw<T>& raw, const Turn<D>& t, float* x, float* o) {
+  raw.floats(x);
+  if (t.inside) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) var[c] = token_sum<LPH>(var[c]) / n;
-    const int gs = D / a.r;  // coordinates of a variance group: a power of two
-    float* db = a.dbar + r * a.r;
-    if (gs >= 8) {
-      float sum8 = ((var[0] + var[1]) + (var[2] + var[3])) + ((var[4] + var[5]) + (var[6] + var[7]));
-      for (int o = gs / 16; o > 0; o >>= 1) sum8 += __shfl_xor_sync(0xffffffffu, sum8, o);
-      if (sub == 0 && l % (gs / 8) == 0) db[l / (gs / 8)] = sum8 / (float)gs;
-    } else if (sub == 0) {
+    for (int i = 0; i < 8; ++i) o[i] = x[i ^ 1];
+  } else {
+    raw.from(t.partner).floats(o);  // the values as they came: half the exchanges of the normed ones
+  }
+}
+
+// Summary of a block from its tokens in shared memory, by one warp: mean of
+// the first n tokens and, for keys, the grouped mean of the population
+// variances, both in two passes over registers and in the order of
+// warp_block_summary, with the same results.
+template <int D>
+__device__ __forceinline__ void tile_summary(const __nv_bfloat16* tile, int n, float* bar, float* dbar, int r, int lane) {
+  constexpr int V = D / 32;
+  float t[kBlock][V], mean[V] = {};
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        // partial sums in place: var[c] of the first coordinate of a group gathers the group
-        if (gs >= 2 && (c & 1) == 0) var[c] += var[c + 1];
+  for (int j = 0; j < kBlock; ++j) {
+    if (j < n) {
+      if (V == 4) {
+        const uint2 u = *reinterpret_cast<const uint2*>(tile + j * D + lane * V);
+        t[j][0] = __uint_as_float(u.x << 16);
+        t[j][1] = __uint_as_float(u.x & 0xffff0000u);
+        t[j][V - 2] = __uint_as_float(u.y << 16);
+        t[j][V - 1] = __uint_as_float(u.y & 0xffff0000u);
+      } else {
+        const uint32_t u = *reinterpret_cast<const uint32_t*>(tile + j * D + lane * V);
+        t[j][0] = __uint_as_float(u << 16);
+        t[j][1] = __uint_as_float(u & 0xffff0000u);
       }
 #pragma unroll
-      for (int c = 0; c < 8; c += 4)
-        if (gs >= 4) var[c] += var[c + 2];
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        if (c % gs == 0) db[(8 * l + c) / gs] = var[c] / (float)gs;
+      for (int i = 0; i < V; ++i) mean[i] += t[j][i];
     }
+  }
+  const float fn = (float)n;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    mean[i] = mean[i] / fn;
+    bar[lane * V + i] = mean[i];
+  }
+  if (!dbar) return;
+  float var[V] = {};
+#pragma unroll
+  for (int j = 0; j < kBlock; ++j)
+    if (j < n) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float dlt = t[j][i] - mean[i];
+        var[i] = fmaf(dlt, dlt, var[i]);
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < V; ++i) var[i] = var[i] / fn;
+  const int gs = D / r;
+  if (gs >= V) {
+    const int lpg = gs / V;
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) x += var[i];
+    for (int o = lpg >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if ((lane & (lpg - 1)) == 0) dbar[lane / lpg] = x / (float)gs;
+  } else if (gs == 2) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) dbar[(lane * V + i) / 2] = (var[i] + var[i + 1]) / 2.f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) dbar[lane * V + i] = var[i];
+  }
+}
+
+// One CTA per 16-token cache block that receives tokens and `hc` KV heads with
+// their query heads.  A warp has 32 / (D/8) tokens and goes through the heads,
+// kBatch of them in flight, so that a token's angles are read once and stay in
+// registers; the stored keys and values also go to shared memory, the block's
+// earlier tokens with them, and from there the warps form the summaries.
+// Bound by DRAM: 32K tokens x 48 heads of 128 move 0.84 GB.
+constexpr int kBatch = 4;
+template <int D, typename T>
+__global__ void __launch_bounds__(256) rope_prefill_kernel(const __grid_constant__ RopePrefillArgs g, int hc) {
+  const RopeArgs& a = g.rope;
+  constexpr int LPH = D / 8, TPW = 32 / LPH, WT = kBlock / TPW, TEAMS = 8 / WT;
+  extern __shared__ __align__(16) __nv_bfloat16 tiles[];  // [K, V][hc][16][D]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (LPH - 1);
+  int s = 0;
+  while (s + 1 < a.B && g.item0[s + 1] <= (int)blockIdx.x) ++s;
+  const int b = g.starts[s] / kBlock + ((int)blockIdx.x - g.item0[s]);
+  const int lo = max(g.starts[s] - b * kBlock, 0);                     // slots of this block that receive tokens:
+  const int hi = min(g.starts[s] + g.counts[s] - b * kBlock, kBlock);  // [lo, hi)
+  const int kv0 = blockIdx.y * hc, kvn = min(hc, a.Hkv - kv0);
+  if ((int)blockIdx.x == g.item0[s] && blockIdx.y == 0 && threadIdx.x == 0) a.seq_len[s] = g.starts[s] + g.counts[s];
+
+  const int j = warp % WT * TPW + lane / LPH;  // this lane's token
+  const bool live = j >= lo && j < hi;
+  const int64_t tok = (int64_t)g.token0[s] + b * kBlock - g.starts[s] + j;
+  const int pos = !live ? 0 : a.positions ? __ldg(a.positions + tok) : b * kBlock + j;
+  const Turn<D> turn(a, table_row(a, pos, s, live && blockIdx.y == 0 && warp < WT && l == 0), lane);
+
+  // the CTA's heads: kvn G query heads, kvn key heads, kvn value heads; a team of warps takes every TEAMS-th
+  const int G = a.Hq / a.Hkv, nq = kvn * G, heads = nq + 2 * kvn, team = warp / WT;
+  const T* src = reinterpret_cast<const T*>(a.qkv) + tok * a.stride + 8 * l;
+  auto column = [&](int i) {
+    return i < nq ? kv0 * G + i : i < nq + kvn ? a.Hq + kv0 + i - nq : a.Hq + a.Hkv + kv0 + i - nq - kvn;
+  };
+  Raw<T> next[kBatch];
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    const int i = team + u * TEAMS;
+    next[u].load(src + column(i) * D, live && i < heads);
+  }
+  float w[8], wo[8];
+  const float* weight = a.q_weight;
+  if (weight) turn.weights(weight, lane, w, wo);
+  bool keys = false;
+  for (int i0 = team; i0 < heads; i0 += kBatch * TEAMS) {
+    Raw<T> raw[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) raw[u] = next[u];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + (kBatch + u) * TEAMS;
+      next[u].load(src + column(i) * D, live && i < heads);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * TEAMS;
+      if (i >= heads) break;
+      if (i < nq) {
+        float x[8], o[8];
+        pairs<D, T>(raw[u], turn, x, o);
+        if (weight) {
+          float m = 0.f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) m = fmaf(x[k], x[k], m);
+#pragma unroll
+          for (int k = LPH / 2; k > 0; k >>= 1) m += __shfl_xor_sync(0xffffffffu, m, k);
+          const float r = rsqrtf(m * (1.f / D) + a.eps);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            x[k] = x[k] * r * w[k];
+            o[k] = o[k] * r * wo[k];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = fmaf(x[k], turn.c[k], o[k] * turn.s[k]);
+        if (live) store_q(a, (tok * a.Hq + kv0 * G + i) * D + 8 * l, x);
+        continue;
+      }
+      const bool is_k = i < nq + kvn;
+      const int h = i - nq - (is_k ? 0 : kvn);
+      const int64_t r = g.seq_row0[s] + (int64_t)(kv0 + h) * g.cap_blocks[s] + b;
+      uint4* dst = reinterpret_cast<uint4*>((is_k ? a.k : a.v) + (r * kBlock + j) * D + 8 * l);
+      uint4 y = make_uint4(0, 0, 0, 0);
+      if (j < lo) y = __ldcg(dst);
+      if (is_k) {
+        if (!keys) {
+          keys = true;
+          weight = a.k_weight;
+          if (weight) turn.weights(weight, lane, w, wo);
+        }
+        float x[8], o[8];
+        pairs<D, T>(raw[u], turn, x, o);
+        F2 r2 = {1.f, 0.f};
+        if (weight) r2 = inverse_norm<D>(x, a.eps);
+        __nv_bfloat16 z[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const F2 p = weight ? scaled(x[k], w[k], r2) : F2{x[k], 0.f}, q = weight ? scaled(o[k], wo[k], r2) : F2{o[k], 0.f};
+          const F2 t = turn2(p, turn.c[k], q, turn.s[k]);
+          z[k] = __float2bfloat16_rn(__fadd_rn(t.hi, t.lo));
+        }
+        if (live) y = pack8(z);
+      } else if (live) {
+        if (sizeof(T) == 2) {
+          y = raw[u].v[0];
+        } else {
+          float x[8];
+          __nv_bfloat16 z[8];
+          raw[u].floats(x);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) z[k] = __float2bfloat16_rn(x[k]);
+          y = pack8(z);
+        }
+      }
+      if (live) *dst = y;
+      *reinterpret_cast<uint4*>(tiles + (((is_k ? 0 : hc) + h) * kBlock + j) * D + 8 * l) = y;
+    }
+  }
+  __syncthreads();
+  for (int i = warp; i < 2 * kvn; i += 8) {
+    const bool is_k = i < kvn;
+    const int h = is_k ? i : i - kvn;
+    const int64_t r = g.seq_row0[s] + (int64_t)(kv0 + h) * g.cap_blocks[s] + b;
+    tile_summary<D>(tiles + ((is_k ? 0 : hc) + h) * kBlock * D, hi, (is_k ? a.kbar : a.vbar) + r * D,
+                    is_k ? a.dbar + r * a.r : nullptr, a.r, lane);
   }
 }
 
@@ -399,16 +562,22 @@ cudaError_t launch_rope_step(const RopeArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_rope_prefill(const RopePrefillArgs& g, cudaStream_t st) {
+cudaError_t launch_rope_prefill(const RopePrefillArgs& g, int sms, cudaStream_t st) {
   const RopeArgs& a = g.rope;
-  const unsigned grid = (unsigned)g.item0[a.B];
-  if (!grid) return cudaSuccess;
+  const int blocks = g.item0[a.B];
+  if (!blocks) return cudaSuccess;
+  // KV heads of a CTA: four read a token's angles once for all of them and leave room for several CTAs on a
+  // multiprocessor; fewer where the blocks alone would not give every multiprocessor four
+  int hc = a.Hkv < 4 ? a.Hkv : 4;
+  while (hc > 1 && (int64_t)blocks * ((a.Hkv + hc - 1) / hc) < 4 * sms) hc = (hc + 1) / 2;
+  const dim3 grid(blocks, (a.Hkv + hc - 1) / hc);
+  const size_t smem = (size_t)2 * hc * kBlock * a.d * 2;
   if (a.d == 128) {
-    if (a.in_f32) rope_prefill_kernel<128, float><<<grid, 256, 0, st>>>(g);
-    else rope_prefill_kernel<128, __nv_bfloat16><<<grid, 256, 0, st>>>(g);
+    if (a.in_f32) rope_prefill_kernel<128, float><<<grid, 256, smem, st>>>(g, hc);
+    else rope_prefill_kernel<128, __nv_bfloat16><<<grid, 256, smem, st>>>(g, hc);
   } else {
-    if (a.in_f32) rope_prefill_kernel<64, float><<<grid, 256, 0, st>>>(g);
-    else rope_prefill_kernel<64, __nv_bfloat16><<<grid, 256, 0, st>>>(g);
+    if (a.in_f32) rope_prefill_kernel<64, float><<<grid, 256, smem, st>>>(g, hc);
+    else rope_prefill_kernel<64, __nv_bfloat16><<<grid, 256, smem, st>>>(g, hc);
   }
   return cudaGetLastError();
 }
