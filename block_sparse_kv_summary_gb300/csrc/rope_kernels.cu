@@ -4,23 +4,30 @@
 // cache, and the block summaries of section "무엇과 다른가" formed on the way).
 //
 //   y = w x / sqrt(mean(x^2) + eps)              (skipped without a weight)
-//   (a, b) -> (a cos - b sin, b cos + a sin)     for each pair of the first
+//   (u, v) -> (u cos - v sin, v cos + u sin)     for each pair of the first
 //                                                rot_dim coordinates
 //
-// A head is held by D/8 lanes, 8 coordinates each: one 16-byte load of bf16.
+// A head is held by D/8 lanes, four pairs (u, v) each: both members of a pair
+// stand in one lane, so nothing but the sum of squares crosses lanes.  With
+// the weights folded into the angles, (w_u cos, w_v sin, w_v cos, w_u sin),
+// which hold for all heads of a token, a head costs two products a value and
+// its norm's factor.
 //
-// Queries are computed in fp32.  Keys are computed as unevaluated sums of two
-// floats, so that the fp32 value that is then rounded to bf16 is the nearest
-// one: the summaries are those of the stored keys, and a key that falls on the
-// wrong side of a rounding border moves its block's mean and variance by a
-// bf16 step, some thousand times more than the fp32 arithmetic of the summary
-// itself loses.
+// Queries are computed in fp32.  The fp32 value of a key that is rounded to
+// bf16 is the nearest one: the summaries are those of the stored keys, and a
+// key that falls on the wrong side of a rounding border moves its block's mean
+// and variance by a bf16 step, some thousand times more than the fp32
+// arithmetic of the summary itself loses.  Where fp32 cannot tell the side,
+// keys are computed again as unevaluated sums of two floats.
+#include <type_traits>
+
 #include "compkv_launch.h"
 
 namespace compkv {
 
 namespace {
 
+// ---------------------------------------------------------------- two floats
 struct F2 {  // hi + lo, |lo| <= ulp(hi) / 2
   float hi, lo;
 };
@@ -40,114 +47,6 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   const float hi = __fadd_rn(s.hi, lo);
   return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
 }
-
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* x);
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* x) {
-  const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float* x) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-
-__device__ __forceinline__ uint32_t pack2(__nv_bfloat16 a, __nv_bfloat16 b) {
-  return (uint32_t)__bfloat16_as_ushort(a) | ((uint32_t)__bfloat16_as_ushort(b) << 16);
-}
-__device__ __forceinline__ uint4 pack8(const __nv_bfloat16* y) {
-  return make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
-}
-
-// Where a lane's pairs are: `l` is its place among the D/8 lanes of a head.
-struct Pairing {
-  bool rotated;    // its coordinates are among the first rot_dim
-  bool first;      // half-split pairs: it holds the first coordinate of its pairs
-  int partner;     // half-split pairs: the warp lane that holds the other coordinate
-  int col;         // column of its first angle in the table's cos part
-};
-template <int LPH>
-__device__ __forceinline__ Pairing pairing(int lane, int rot, int interleaved) {
-  const int l = lane & (LPH - 1);
-  Pairing p;
-  p.rotated = 8 * l < rot;
-  const int half = rot / 16;  // lanes of half a rotation
-  p.first = l < half;
-  p.partner = interleaved || !p.rotated ? lane : (p.first ? lane + half : lane - half);
-  p.col = interleaved ? 4 * l : 8 * (p.first ? l : l - half);
-  return p;
-}
-
-// One head's 8 coordinates of this lane, normed and rotated, in fp32.
-template <int D>
-__device__ __forceinline__ void head_f32(float* x, const float* w, const float* row, const RopeArgs& a, Pairing p) {
-  constexpr int LPH = D / 8;
-  if (w) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
-#pragma unroll
-    for (int o = LPH / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float r = rsqrtf(s * (1.f / D) + a.eps);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-  }
-  if (a.interleaved) {
-    if (p.rotated) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float c = row[p.col + i], s = row[a.rot / 2 + p.col + i];
-        const float u = x[2 * i], v = x[2 * i + 1];
-        x[2 * i] = u * c - v * s;
-        x[2 * i + 1] = v * c + u * s;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float other = __shfl_sync(0xffffffffu, x[i], p.partner);
-      if (p.rotated) {
-        const float c = row[p.col + i], s = row[a.rot / 2 + p.col + i];
-        x[i] = p.first ? x[i] * c - other * s : x[i] * c + other * s;
-      }
-    }
-  }
-}
-
-// u c + v s' (s' = s or -s) of two-float u, v.
-__device__ __forceinline__ F2 turn2(F2 u, float c, F2 v, float s) {
-  F2 p = two_prod(u.hi, c), q = two_prod(v.hi, s);
-  p.lo = __fmaf_rn(u.lo, c, p.lo);
-  q.lo = __fmaf_rn(v.lo, s, q.lo);
-  return add2(p, q);
-}
-
-// 1 / sqrt(mean(x^2) + eps) of the head whose coordinates these lanes hold, in two floats: one step of Newton's
-// iteration on rsqrtf with its residual 1 - m r^2 in two floats.
-template <int D>
-__device__ __forceinline__ F2 inverse_norm(const float* x, float eps) {
-  F2 s = {0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s = add2(s, two_prod(x[i], x[i]));
-#pragma unroll
-  for (int o = D / 16; o > 0; o >>= 1)
-    s = add2(s, {__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)});
-  s.hi *= 1.f / D;  // exact: D is a power of two
-  s.lo *= 1.f / D;
-  const F2 m = add2(s, {eps, 0.f});
-  const float r0 = rsqrtf(m.hi);
-  const F2 h = two_prod(m.hi, r0);
-  const float e = __fmaf_rn(-h.hi, r0, 1.f) - (h.lo + m.lo * r0) * r0;
-  return {r0, isfinite(r0) ? 0.5f * r0 * e : 0.f};
-}
 // x w r
 __device__ __forceinline__ F2 scaled(float x, float w, F2 r) {
   const F2 t = two_prod(x, w);
@@ -155,63 +54,255 @@ __device__ __forceinline__ F2 scaled(float x, float w, F2 r) {
   y.lo = __fmaf_rn(t.hi, r.lo, __fmaf_rn(t.lo, r.hi, y.lo));
   return y;
 }
+// a c + b s
+__device__ __forceinline__ F2 turn2(F2 a, float c, F2 b, float s) {
+  F2 p = two_prod(a.hi, c), q = two_prod(b.hi, s);
+  p.lo = __fmaf_rn(a.lo, c, p.lo);
+  q.lo = __fmaf_rn(b.lo, s, q.lo);
+  return add2(p, q);
+}
 
-// The same with two floats per value, rounded to fp32 and then to bf16.
-template <int D>
-__device__ __forceinline__ void head_bf16(const float* x, const float* w, const float* row, const RopeArgs& a,
-                                          Pairing p, __nv_bfloat16* out) {
-  F2 y[8];
-  if (w) {
-    const F2 r = inverse_norm<D>(x, a.eps);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = scaled(x[i], w[i], r);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = {x[i], 0.f};
+// ---------------------------------------------------------------- a lane's part of a head
+// Four pairs: `u` their first members, `v` their second.
+struct Pairs {
+  float u[4], v[4];
+};
+__device__ __forceinline__ float2 two(const float* x, int i) { return make_float2(x[2 * i], x[2 * i + 1]); }
+
+// Where they stand: four coordinates from `a` on and four from `b` on.  INTER:
+// eight coordinates in a row, pairs (2i, 2i + 1).  Otherwise u and v are half
+// a rotation apart, and the coordinates behind the rotation make pairs alike,
+// half of what is left apart, that do not turn.  rot is a multiple of 16.
+struct Place {
+  int a, b, col;  // col: the first pair's column in the table
+  bool turns;
+};
+template <int D, bool INTER>
+__device__ __forceinline__ Place place(int l, int rot) {
+  if (INTER) return {8 * l, 8 * l + 4, 4 * l, 8 * l < rot};
+  const int i = 4 * l;
+  if (i < rot / 2) return {i, i + rot / 2, i, true};
+  return {i + rot / 2, i + D / 2, 0, false};
+}
+
+// Eight coordinates as they come.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  uint2 a, b;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, const Place& at, bool live) {
+    a = b = make_uint2(0, 0);
+    if (live) {
+      a = __ldcs(reinterpret_cast<const uint2*>(p + at.a));
+      b = __ldcs(reinterpret_cast<const uint2*>(p + at.b));
+    }
   }
-  if (a.interleaved) {
+  template <bool INTER>
+  __device__ __forceinline__ Pairs pairs() const {
+    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+    Pairs p;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (p.rotated) {
-        const float c = row[p.col + i], s = row[a.rot / 2 + p.col + i];
-        const F2 u = y[2 * i], v = y[2 * i + 1];
-        y[2 * i] = turn2(u, c, v, -s);
-        y[2 * i + 1] = turn2(v, c, u, s);
+      const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
+      if (INTER) {
+        p.u[i] = lo;
+        p.v[i] = hi;
+      } else {
+        (i < 2 ? p.u : p.v)[2 * (i & 1)] = lo;
+        (i < 2 ? p.u : p.v)[2 * (i & 1) + 1] = hi;
       }
     }
+    return p;
+  }
+  __device__ __forceinline__ uint4 bf16() const { return make_uint4(a.x, a.y, b.x, b.y); }
+};
+template <bool INTER>
+__device__ __forceinline__ Pairs ordered(float4 a, float4 b) {
+  if (INTER) return {{a.x, a.z, b.x, b.z}, {a.y, a.w, b.y, b.w}};
+  return {{a.x, a.y, a.z, a.w}, {b.x, b.y, b.z, b.w}};
+}
+__device__ __forceinline__ uint32_t round2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p, const Place& at, bool live) {
+    a = b = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) {
+      a = __ldcs(reinterpret_cast<const float4*>(p + at.a));
+      b = __ldcs(reinterpret_cast<const float4*>(p + at.b));
+    }
+  }
+  template <bool INTER>
+  __device__ __forceinline__ Pairs pairs() const {
+    return ordered<INTER>(a, b);
+  }
+  __device__ __forceinline__ uint4 bf16() const {
+    return make_uint4(round2(a.x, a.y), round2(a.z, a.w), round2(b.x, b.y), round2(b.z, b.w));
+  }
+};
+// Back in the order of the coordinates: the four from a on, then those from b on.
+template <bool INTER>
+__device__ __forceinline__ void coordinates(const Pairs& p, float4& a, float4& b) {
+  if (INTER) {
+    a = make_float4(p.u[0], p.v[0], p.u[1], p.v[1]);
+    b = make_float4(p.u[2], p.v[2], p.u[3], p.v[3]);
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const F2 other = {__shfl_sync(0xffffffffu, y[i].hi, p.partner), __shfl_sync(0xffffffffu, y[i].lo, p.partner)};
-      if (p.rotated) {
-        const float c = row[p.col + i], s = row[a.rot / 2 + p.col + i];
-        y[i] = turn2(y[i], c, other, p.first ? -s : s);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) out[i] = __float2bfloat16_rn(__fadd_rn(y[i].hi, y[i].lo));
-}
-
-__device__ __forceinline__ void weights8(const float* w, int l, float* out) {
-  if (w) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(w) + 2 * l), b = __ldg(reinterpret_cast<const float4*>(w) + 2 * l + 1);
-    out[0] = a.x; out[1] = a.y; out[2] = a.z; out[3] = a.w;
-    out[4] = b.x; out[5] = b.y; out[6] = b.z; out[7] = b.w;
+    a = make_float4(p.u[0], p.u[1], p.u[2], p.u[3]);
+    b = make_float4(p.v[0], p.v[1], p.v[2], p.v[3]);
   }
 }
-
-__device__ __forceinline__ void store_q(const RopeArgs& a, int64_t at, const float* x) {
+template <bool INTER>
+__device__ __forceinline__ uint4 rounded(const Pairs& p) {
+  float4 a, b;
+  coordinates<INTER>(p, a, b);
+  return make_uint4(round2(a.x, a.y), round2(a.z, a.w), round2(b.x, b.y), round2(b.z, b.w));
+}
+// bf16 values into four coordinates from `a` on and four from `b` on.
+__device__ __forceinline__ void put(__nv_bfloat16* p, const Place& at, uint4 x) {
+  *reinterpret_cast<uint2*>(p + at.a) = make_uint2(x.x, x.y);
+  *reinterpret_cast<uint2*>(p + at.b) = make_uint2(x.z, x.w);
+}
+template <bool INTER>
+__device__ __forceinline__ void put_query(const RopeArgs& a, int64_t head, const Place& at, const Pairs& y) {
   if (a.q_bf16) {
-    __nv_bfloat16 y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __float2bfloat16_rn(x[i]);
-    __stcs(reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.q) + at), pack8(y));
+    const uint4 x = rounded<INTER>(y);
+    __nv_bfloat16* q = reinterpret_cast<__nv_bfloat16*>(a.q) + head;
+    __stcs(reinterpret_cast<uint2*>(q + at.a), make_uint2(x.x, x.y));
+    __stcs(reinterpret_cast<uint2*>(q + at.b), make_uint2(x.z, x.w));
   } else {
-    float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.q) + at);
-    __stcs(q, make_float4(x[0], x[1], x[2], x[3]));
-    __stcs(q + 1, make_float4(x[4], x[5], x[6], x[7]));
+    float4 c, d;
+    coordinates<INTER>(y, c, d);
+    float* q = reinterpret_cast<float*>(a.q) + head;
+    __stcs(reinterpret_cast<float4*>(q + at.a), c);
+    __stcs(reinterpret_cast<float4*>(q + at.b), d);
   }
+}
+
+// ---------------------------------------------------------------- a token's angles
+struct Angles {
+  float c[4], s[4];
+};
+__device__ __forceinline__ Angles angles(const float* row, int rot, const Place& at) {
+  if (!at.turns) return {{1.f, 1.f, 1.f, 1.f}, {0.f, 0.f, 0.f, 0.f}};
+  const float4 c = __ldg(reinterpret_cast<const float4*>(row + at.col));
+  const float4 s = __ldg(reinterpret_cast<const float4*>(row + rot / 2 + at.col));
+  return {{c.x, c.y, c.z, c.w}, {s.x, s.y, s.z, s.w}};
+}
+template <bool INTER>
+__device__ __forceinline__ Pairs weights(const float* w, const Place& at) {
+  if (!w) return {{1.f, 1.f, 1.f, 1.f}, {1.f, 1.f, 1.f, 1.f}};
+  return ordered<INTER>(__ldg(reinterpret_cast<const float4*>(w + at.a)), __ldg(reinterpret_cast<const float4*>(w + at.b)));
+}
+// y_u = (u uc + v vs) r, y_v = (v vc + u us) r
+struct Factors {
+  float2 uc[2], vs[2], vc[2], us[2];
+};
+__device__ __forceinline__ Factors factors(const Pairs& w, const Angles& t) {
+  Factors f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    f.uc[i] = __fmul2_rn(two(w.u, i), two(t.c, i));
+    f.vs[i] = __fmul2_rn(two(w.v, i), make_float2(-t.s[2 * i], -t.s[2 * i + 1]));
+    f.vc[i] = __fmul2_rn(two(w.v, i), two(t.c, i));
+    f.us[i] = __fmul2_rn(two(w.u, i), two(t.s, i));
+  }
+  return f;
+}
+
+__device__ __forceinline__ float rsqrt_approx(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A head in fp32; returns r, the norm's factor (1 without `normed`).
+template <int D>
+__device__ __forceinline__ float turn_head(const Pairs& x, const Factors& f, bool normed, float eps, Pairs& y) {
+  float r = 1.f;
+  if (normed) {
+    float2 m = __fmul2_rn(two(x.u, 0), two(x.u, 0));
+    m = __ffma2_rn(two(x.u, 1), two(x.u, 1), m);
+    m = __ffma2_rn(two(x.v, 0), two(x.v, 0), m);
+    m = __ffma2_rn(two(x.v, 1), two(x.v, 1), m);
+    float q = m.x + m.y;
+#pragma unroll
+    for (int k = D / 16; k > 0; k >>= 1) q += __shfl_xor_sync(0xffffffffu, q, k);
+    r = rsqrt_approx(fmaf(q, 1.f / D, eps));
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float2 u = __ffma2_rn(two(x.u, i), f.uc[i], __fmul2_rn(two(x.v, i), f.vs[i]));
+    float2 v = __ffma2_rn(two(x.v, i), f.vc[i], __fmul2_rn(two(x.u, i), f.us[i]));
+    u = __fmul2_rn(u, make_float2(r, r));
+    v = __fmul2_rn(v, make_float2(r, r));
+    y.u[2 * i] = u.x;
+    y.u[2 * i + 1] = u.y;
+    y.v[2 * i] = v.x;
+    y.v[2 * i + 1] = v.y;
+  }
+  return r;
+}
+
+// Whether an error of 16 roundings of 2^-24 could carry y over the border halfway between two bf16 values.  The
+// roundings: the sum of squares 7, halved by the root, its eps 1/2, the root 4 (2^-22.9), weight times angle 1
+// each, a product 1, the sum 1, the factor 1; `size` is the size of what is added up.
+__device__ __forceinline__ bool near_border(float y, float size) {
+  const float border = __uint_as_float((__float_as_uint(y) & 0xffff0000u) | 0x8000u);
+  return fabsf(y - border) <= size * (16.f / 16777216.f);
+}
+
+// A key head in two floats per value, rounded to fp32 and then to bf16.  Not inlined: it is rare and long.  The
+// root: one step of Newton's iteration with its residual 1 - m r^2 in two floats.
+template <int D, bool INTER>
+__device__ __noinline__ uint4 key_exact(Pairs x, const float* row, int rot, Place at, const float* weight, float eps) {
+  const Pairs w = weights<INTER>(weight, at);
+  const Angles t = angles(row, rot, at);
+  F2 r = {1.f, 0.f};
+  if (weight) {
+    F2 s = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = add2(add2(s, two_prod(x.u[i], x.u[i])), two_prod(x.v[i], x.v[i]));
+#pragma unroll
+    for (int o = D / 16; o > 0; o >>= 1)
+      s = add2(s, {__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)});
+    s.hi *= 1.f / D;  // exact: D is a power of two
+    s.lo *= 1.f / D;
+    const F2 m = add2(s, {eps, 0.f});
+    const float r0 = rsqrtf(m.hi);
+    const F2 h = two_prod(m.hi, r0);
+    const float e = __fmaf_rn(-h.hi, r0, 1.f) - (h.lo + m.lo * r0) * r0;
+    r = {r0, isfinite(r0) ? 0.5f * r0 * e : 0.f};
+  }
+  Pairs y;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const F2 u = scaled(x.u[i], w.u[i], r), v = scaled(x.v[i], w.v[i], r);
+    const F2 a = turn2(u, t.c[i], v, -t.s[i]), b = turn2(v, t.c[i], u, t.s[i]);
+    y.u[i] = __fadd_rn(a.hi, a.lo);
+    y.v[i] = __fadd_rn(b.hi, b.lo);
+  }
+  return rounded<INTER>(y);
+}
+
+template <int D, bool INTER>
+__device__ __forceinline__ uint4 turn_key(const Pairs& x, const Factors& f, const float* row, const RopeArgs& a, const Place& at) {
+  Pairs y;
+  const float r = turn_head<D>(x, f, a.k_weight != nullptr, a.eps, y);
+  bool doubt = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool odd = i & 1;
+    const float uc = odd ? f.uc[i / 2].y : f.uc[i / 2].x, vs = odd ? f.vs[i / 2].y : f.vs[i / 2].x;
+    const float vc = odd ? f.vc[i / 2].y : f.vc[i / 2].x, us = odd ? f.us[i / 2].y : f.us[i / 2].x;
+    doubt |= near_border(y.u[i], (fabsf(x.u[i] * uc) + fabsf(x.v[i] * vs)) * r);
+    doubt |= near_border(y.v[i], (fabsf(x.v[i] * vc) + fabsf(x.u[i] * us)) * r);
+  }
+  if (__any_sync(0xffffffffu, doubt)) return key_exact<D, INTER>(x, row, a.rot, at, a.k_weight, a.eps);
+  return rounded<INTER>(y);
 }
 
 // The table row of a token's position; a position outside the table is
@@ -224,139 +315,39 @@ __device__ __forceinline__ const float* table_row(const RopeArgs& a, int pos, in
   return a.table + (int64_t)pos * a.rot;
 }
 
-// One token per sequence.  A group of D/8 lanes per (sequence, head); the
-// heads of a token are its queries, keys and values in the projection's order.
-template <int D, typename T>
+// ---------------------------------------------------------------- one token per sequence
+// A group of D/8 lanes per (sequence, head); the heads of a token are its
+// queries, keys and values in the projection's order.  Bound by latency: the
+// position, the angles and one head's arithmetic in a row, 2.5 us; for 64
+// sequences of 48 heads 3.2 us.
+template <int D, typename T, bool INTER>
 __global__ void __launch_bounds__(128) rope_step_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int LPH = D / 8;
-  const int lane = threadIdx.x & 31, l = lane & (LPH - 1);
+  const int lane = threadIdx.x & 31;
   const int heads = a.Hq + 2 * a.Hkv, items = a.B * heads;
-  const int raw = (blockIdx.x * blockDim.x + threadIdx.x) / LPH;
-  const int item = raw < items ? raw : items - 1;  // lanes behind the last item repeat it and store nothing
+  const int raw_item = (blockIdx.x * blockDim.x + threadIdx.x) / LPH;
+  const int item = min(raw_item, items - 1);  // lanes behind the last item repeat it and store nothing
   const int s = item / heads, h = item % heads;
-  const Pairing p = pairing<LPH>(lane, a.rot, a.interleaved);
+  const Place at = place<D, INTER>(lane & (LPH - 1), a.rot);
+  Raw<T> raw;
+  raw.load(reinterpret_cast<const T*>(a.qkv) + (int64_t)s * a.stride + h * D, at, true);
   const int pos = a.positions ? __ldg(a.positions + s) : __ldcg(a.seq_len + s);
-  float x[8], w[8];
-  load8<T>(reinterpret_cast<const T*>(a.qkv) + (int64_t)s * a.stride + h * D + 8 * l, x);
-  const float* row = table_row(a, pos, s, raw < items && h == 0 && l == 0);
-  // every lane of the warp takes the same shuffles, whatever its head is
+  const float* row = table_row(a, pos, s, raw_item < items && h == 0 && (lane & (LPH - 1)) == 0);
   const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
-  const float* wt = is_q ? a.q_weight : a.k_weight;
-  weights8(wt, l, w);
-  float y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = x[i];
-  __nv_bfloat16 z[8];
-  if (__any_sync(0xffffffffu, is_q)) head_f32<D>(y, a.q_weight ? w : nullptr, row, a, p);
-  if (__any_sync(0xffffffffu, is_k)) head_bf16<D>(x, a.k_weight ? w : nullptr, row, a, p, z);
-  if (raw >= items) return;
-  if (is_q) {
-    store_q(a, ((int64_t)s * a.Hq + h) * D + 8 * l, y);
-  } else if (is_k) {
-    *reinterpret_cast<uint4*>(a.k_new + ((int64_t)s * a.Hkv + h - a.Hq) * D + 8 * l) = pack8(z);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = __float2bfloat16_rn(x[i]);
-    *reinterpret_cast<uint4*>(a.v_new + ((int64_t)s * a.Hkv + h - a.Hq - a.Hkv) * D + 8 * l) = pack8(z);
-  }
+  const Pairs x = raw.template pairs<INTER>();
+  const Factors f = factors(weights<INTER>(is_q ? a.q_weight : a.k_weight, at), angles(row, a.rot, at));
+  // every lane of the warp takes the same shuffles, whatever its head is
+  Pairs y;
+  uint4 z;
+  if (__any_sync(0xffffffffu, is_q)) turn_head<D>(x, f, a.q_weight != nullptr, a.eps, y);
+  if (__any_sync(0xffffffffu, is_k)) z = turn_key<D, INTER>(x, f, row, a, at);
+  if (raw_item >= items) return;
+  if (is_q) put_query<INTER>(a, ((int64_t)s * a.Hq + h) * D, at, y);
+  else if (is_k) put(a.k_new + ((int64_t)s * a.Hkv + h - a.Hq) * D, at, z);
+  else put(a.v_new + ((int64_t)s * a.Hkv + h - a.Hq - a.Hkv) * D, at, raw.bf16());
 }
 
-// Many tokens: a lane's part of one token's rotation, the same for all heads.
-//   y_i = x_i cos_i + o_i sin_i,  o_i the other coordinate of the pair, the sign in sin_i
-template <int D>
-struct Turn {
-  float c[8], s[8];
-  int partner;   // the lane that holds the o_i; interleaved pairs are in the lane itself
-  bool inside;   // interleaved
-  __device__ __forceinline__ Turn(const RopeArgs& a, const float* row, int lane) {
-    const Pairing p = pairing<D / 8>(lane, a.rot, a.interleaved);
-    partner = p.partner;
-    inside = a.interleaved;
-    if (!p.rotated) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
-    } else if (inside) {
-      const float4 u = __ldg(reinterpret_cast<const float4*>(row + p.col));
-      const float4 v = __ldg(reinterpret_cast<const float4*>(row + a.rot / 2 + p.col));
-      const float cc[4] = {u.x, u.y, u.z, u.w}, ss[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c[2 * i] = c[2 * i + 1] = cc[i];
-        s[2 * i] = -ss[i];
-        s[2 * i + 1] = ss[i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 u = __ldg(reinterpret_cast<const float4*>(row + p.col) + i);
-        const float4 v = __ldg(reinterpret_cast<const float4*>(row + a.rot / 2 + p.col) + i);
-        const float sign = p.first ? -1.f : 1.f;
-        c[4 * i] = u.x, c[4 * i + 1] = u.y, c[4 * i + 2] = u.z, c[4 * i + 3] = u.w;
-        s[4 * i] = sign * v.x, s[4 * i + 1] = sign * v.y, s[4 * i + 2] = sign * v.z, s[4 * i + 3] = sign * v.w;
-      }
-    }
-  }
-  // Weights of this lane's coordinates and of their partners.
-  __device__ __forceinline__ void weights(const float* w, int lane, float* own, float* other) const {
-    weights8(w, lane & (D / 8 - 1), own);
-    if (inside) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) other[i] = own[i ^ 1];
-    } else {
-      weights8(w, partner & (D / 8 - 1), other);
-    }
-  }
-};
-
-// 8 coordinates as they come.
-template <typename T>
-struct Raw {
-  uint4 v[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T* p, bool live) {
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-      v[i] = live ? __ldcs(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ Raw from(int lane) const {
-    Raw r;
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-      r.v[i].x = __shfl_sync(0xffffffffu, v[i].x, lane);
-      r.v[i].y = __shfl_sync(0xffffffffu, v[i].y, lane);
-      r.v[i].z = __shfl_sync(0xffffffffu, v[i].z, lane);
-      r.v[i].w = __shfl_sync(0xffffffffu, v[i].w, lane);
-    }
-    return r;
-  }
-  __device__ __forceinline__ void floats(float* x) const {
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (sizeof(T) == 2) {
-          x[2 * k] = __uint_as_float(w[k] << 16);
-          x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-        } else {
-          x[4 * i + k] = __uint_as_float(w[k]);
-        }
-      }
-    }
-  }
-};
-
-// The lane's coordinates and their partners'.
-template <int D, typename T>
-__device__ __forceinline__ void pairs(const Raw<T>& raw, const Turn<D>& t, float* x, float* o) {
-  raw.floats(x);
-  if (t.inside) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = x[i ^ 1];
-  } else {
-    raw.from(t.partner).floats(o);  // the values as they came: half the exchanges of the normed ones
-  }
-}
-
+// ---------------------------------------------------------------- many tokens
 // Summary of a block from its tokens in shared memory, by one warp: mean of
 // the first n tokens and, for keys, the grouped mean of the population
 // variances, both in two passes over registers and in the order of
@@ -364,44 +355,41 @@ __device__ __forceinline__ void pairs(const Raw<T>& raw, const Turn<D>& t, float
 template <int D>
 __device__ __forceinline__ void tile_summary(const __nv_bfloat16* tile, int n, float* bar, float* dbar, int r, int lane) {
   constexpr int V = D / 32;
-  float t[kBlock][V], mean[V] = {};
+  float2 t[kBlock][V / 2], mean[V / 2] = {};
 #pragma unroll
   for (int j = 0; j < kBlock; ++j) {
-    if (j < n) {
-      if (V == 4) {
-        const uint2 u = *reinterpret_cast<const uint2*>(tile + j * D + lane * V);
-        t[j][0] = __uint_as_float(u.x << 16);
-        t[j][1] = __uint_as_float(u.x & 0xffff0000u);
-        t[j][V - 2] = __uint_as_float(u.y << 16);
-        t[j][V - 1] = __uint_as_float(u.y & 0xffff0000u);
-      } else {
-        const uint32_t u = *reinterpret_cast<const uint32_t*>(tile + j * D + lane * V);
-        t[j][0] = __uint_as_float(u << 16);
-        t[j][1] = __uint_as_float(u & 0xffff0000u);
-      }
+    if (j >= n) break;
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(tile + j * D + lane * V);
 #pragma unroll
-      for (int i = 0; i < V; ++i) mean[i] += t[j][i];
+    for (int i = 0; i < V / 2; ++i) {
+      t[j][i] = make_float2(__uint_as_float(p[i] << 16), __uint_as_float(p[i] & 0xffff0000u));
+      mean[i] = __fadd2_rn(mean[i], t[j][i]);
     }
   }
   const float fn = (float)n;
+  auto over = [&](float x) { return n == kBlock ? x * (1.f / kBlock) : x / fn; };  // exact alike for 16
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    mean[i] = mean[i] / fn;
-    bar[lane * V + i] = mean[i];
+  for (int i = 0; i < V / 2; ++i) {
+    mean[i] = make_float2(over(mean[i].x), over(mean[i].y));
+    reinterpret_cast<float2*>(bar + lane * V)[i] = mean[i];
   }
   if (!dbar) return;
-  float var[V] = {};
+  float2 v2[V / 2] = {};
 #pragma unroll
-  for (int j = 0; j < kBlock; ++j)
-    if (j < n) {
+  for (int j = 0; j < kBlock; ++j) {
+    if (j >= n) break;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float dlt = t[j][i] - mean[i];
-        var[i] = fmaf(dlt, dlt, var[i]);
-      }
+    for (int i = 0; i < V / 2; ++i) {
+      const float2 dlt = __fadd2_rn(t[j][i], make_float2(-mean[i].x, -mean[i].y));
+      v2[i] = __ffma2_rn(dlt, dlt, v2[i]);
     }
+  }
+  float var[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) var[i] = var[i] / fn;
+  for (int i = 0; i < V / 2; ++i) {
+    var[2 * i] = over(v2[i].x);
+    var[2 * i + 1] = over(v2[i].y);
+  }
   const int gs = D / r;
   if (gs >= V) {
     const int lpg = gs / V;
@@ -421,17 +409,17 @@ __device__ __forceinline__ void tile_summary(const __nv_bfloat16* tile, int n, f
 
 // One CTA per 16-token cache block that receives tokens and `hc` KV heads with
 // their query heads.  A warp has 32 / (D/8) tokens and goes through the heads,
-// kBatch of them in flight, so that a token's angles are read once and stay in
-// registers; the stored keys and values also go to shared memory, the block's
-// earlier tokens with them, and from there the warps form the summaries.
-// Bound by DRAM: 32K tokens x 48 heads of 128 move 0.84 GB.
+// kBatch of them in flight, so that a token's factors are formed once and stay
+// in registers; the stored keys and values also go to shared memory, the
+// block's earlier tokens with them, and from there the warps form the
+// summaries.
 constexpr int kBatch = 4;
-template <int D, typename T>
-__global__ void __launch_bounds__(256) rope_prefill_kernel(const __grid_constant__ RopePrefillArgs g, int hc) {
+template <int D, typename T, bool INTER>
+__global__ void __launch_bounds__(256, 3) rope_prefill_kernel(const __grid_constant__ RopePrefillArgs g, int hc) {
   const RopeArgs& a = g.rope;
   constexpr int LPH = D / 8, TPW = 32 / LPH, WT = kBlock / TPW, TEAMS = 8 / WT;
   extern __shared__ __align__(16) __nv_bfloat16 tiles[];  // [K, V][hc][16][D]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (LPH - 1);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int s = 0;
   while (s + 1 < a.B && g.item0[s + 1] <= (int)blockIdx.x) ++s;
   const int b = g.starts[s] / kBlock + ((int)blockIdx.x - g.item0[s]);
@@ -440,103 +428,64 @@ __global__ void __launch_bounds__(256) rope_prefill_kernel(const __grid_constant
   const int kv0 = blockIdx.y * hc, kvn = min(hc, a.Hkv - kv0);
   if ((int)blockIdx.x == g.item0[s] && blockIdx.y == 0 && threadIdx.x == 0) a.seq_len[s] = g.starts[s] + g.counts[s];
 
-  const int j = warp % WT * TPW + lane / LPH;  // this lane's token
+  const int j = warp % WT * TPW + lane / LPH, team = warp / WT;  // this lane's token; warps of a team share heads
   const bool live = j >= lo && j < hi;
   const int64_t tok = (int64_t)g.token0[s] + b * kBlock - g.starts[s] + j;
   const int pos = !live ? 0 : a.positions ? __ldg(a.positions + tok) : b * kBlock + j;
-  const Turn<D> turn(a, table_row(a, pos, s, live && blockIdx.y == 0 && warp < WT && l == 0), lane);
+  const float* row = table_row(a, pos, s, live && blockIdx.y == 0 && team == 0 && (lane & (LPH - 1)) == 0);
+  const Place at = place<D, INTER>(lane & (LPH - 1), a.rot);
+  const T* src = reinterpret_cast<const T*>(a.qkv) + tok * a.stride;
 
-  // the CTA's heads: kvn G query heads, kvn key heads, kvn value heads; a team of warps takes every TEAMS-th
-  const int G = a.Hq / a.Hkv, nq = kvn * G, heads = nq + 2 * kvn, team = warp / WT;
-  const T* src = reinterpret_cast<const T*>(a.qkv) + tok * a.stride + 8 * l;
-  auto column = [&](int i) {
-    return i < nq ? kv0 * G + i : i < nq + kvn ? a.Hq + kv0 + i - nq : a.Hq + a.Hkv + kv0 + i - nq - kvn;
-  };
-  Raw<T> next[kBatch];
+  {
+    const int G = a.Hq / a.Hkv, nq = kvn * G;
+    const T* q = src + kv0 * G * D;
+    const int64_t out = (tok * a.Hq + kv0 * G) * D;
+    const Factors f = factors(weights<INTER>(a.q_weight, at), angles(row, a.rot, at));
+    for (int i0 = team; i0 < nq; i0 += kBatch * TEAMS) {
+      Raw<T> raw[kBatch];
 #pragma unroll
-  for (int u = 0; u < kBatch; ++u) {
-    const int i = team + u * TEAMS;
-    next[u].load(src + column(i) * D, live && i < heads);
-  }
-  float w[8], wo[8];
-  const float* weight = a.q_weight;
-  if (weight) turn.weights(weight, lane, w, wo);
-  bool keys = false;
-  for (int i0 = team; i0 < heads; i0 += kBatch * TEAMS) {
-    Raw<T> raw[kBatch];
+      for (int u = 0; u < kBatch; ++u) raw[u].load(q + (i0 + u * TEAMS) * D, at, live && i0 + u * TEAMS < nq);
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) raw[u] = next[u];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int i = i0 + (kBatch + u) * TEAMS;
-      next[u].load(src + column(i) * D, live && i < heads);
+      for (int u = 0; u < kBatch; ++u) {
+        if (i0 + u * TEAMS >= nq) break;
+        Pairs y;
+        turn_head<D>(raw[u].template pairs<INTER>(), f, a.q_weight != nullptr, a.eps, y);
+        if (live) put_query<INTER>(a, out + (i0 + u * TEAMS) * D, at, y);
+      }
     }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int i = i0 + u * TEAMS;
-      if (i >= heads) break;
-      if (i < nq) {
-        float x[8], o[8];
-        pairs<D, T>(raw[u], turn, x, o);
-        if (weight) {
-          float m = 0.f;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) m = fmaf(x[k], x[k], m);
-#pragma unroll
-          for (int k = LPH / 2; k > 0; k >>= 1) m += __shfl_xor_sync(0xffffffffu, m, k);
-          const float r = rsqrtf(m * (1.f / D) + a.eps);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            x[k] = x[k] * r * w[k];
-            o[k] = o[k] * r * wo[k];
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = fmaf(x[k], turn.c[k], o[k] * turn.s[k]);
-        if (live) store_q(a, (tok * a.Hq + kv0 * G + i) * D + 8 * l, x);
-        continue;
+  }
+  {
+    const T* k = src + (a.Hq + kv0) * D;
+    const T* v = k + a.Hkv * D;
+    const Factors f = factors(weights<INTER>(a.k_weight, at), angles(row, a.rot, at));
+    const int64_t first = (g.seq_row0[s] + (int64_t)kv0 * g.cap_blocks[s] + b) * kBlock + j, step = (int64_t)g.cap_blocks[s] * kBlock;
+#pragma unroll 1
+    for (int h = team; h < kvn; h += TEAMS) {
+      Raw<T> rk, rv;
+      rk.load(k + h * D, at, live);
+      rv.load(v + h * D, at, live);
+      __nv_bfloat16* kd = a.k + (first + h * step) * D;
+      __nv_bfloat16* vd = a.v + (first + h * step) * D;
+      uint4 x = make_uint4(0, 0, 0, 0), y = x;
+      if (j < lo) {
+        const uint2 xa = __ldcg(reinterpret_cast<const uint2*>(kd + at.a)), xb = __ldcg(reinterpret_cast<const uint2*>(kd + at.b));
+        const uint2 ya = __ldcg(reinterpret_cast<const uint2*>(vd + at.a)), yb = __ldcg(reinterpret_cast<const uint2*>(vd + at.b));
+        x = make_uint4(xa.x, xa.y, xb.x, xb.y);
+        y = make_uint4(ya.x, ya.y, yb.x, yb.y);
       }
-      const bool is_k = i < nq + kvn;
-      const int h = i - nq - (is_k ? 0 : kvn);
-      const int64_t r = g.seq_row0[s] + (int64_t)(kv0 + h) * g.cap_blocks[s] + b;
-      uint4* dst = reinterpret_cast<uint4*>((is_k ? a.k : a.v) + (r * kBlock + j) * D + 8 * l);
-      uint4 y = make_uint4(0, 0, 0, 0);
-      if (j < lo) y = __ldcg(dst);
-      if (is_k) {
-        if (!keys) {
-          keys = true;
-          weight = a.k_weight;
-          if (weight) turn.weights(weight, lane, w, wo);
-        }
-        float x[8], o[8];
-        pairs<D, T>(raw[u], turn, x, o);
-        F2 r2 = {1.f, 0.f};
-        if (weight) r2 = inverse_norm<D>(x, a.eps);
-        __nv_bfloat16 z[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const F2 p = weight ? scaled(x[k], w[k], r2) : F2{x[k], 0.f}, q = weight ? scaled(o[k], wo[k], r2) : F2{o[k], 0.f};
-          const F2 t = turn2(p, turn.c[k], q, turn.s[k]);
-          z[k] = __float2bfloat16_rn(__fadd_rn(t.hi, t.lo));
-        }
-        if (live) y = pack8(z);
-      } else if (live) {
-        if (sizeof(T) == 2) {
-          y = raw[u].v[0];
-        } else {
-          float x[8];
-          __nv_bfloat16 z[8];
-          raw[u].floats(x);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) z[k] = __float2bfloat16_rn(x[k]);
-          y = pack8(z);
-        }
+      const uint4 z = turn_key<D, INTER>(rk.template pairs<INTER>(), f, row, a, at);
+      if (live) {
+        x = z;
+        y = rv.bf16();
+        put(kd, at, x);
+        put(vd, at, y);
       }
-      if (live) *dst = y;
-      *reinterpret_cast<uint4*>(tiles + (((is_k ? 0 : hc) + h) * kBlock + j) * D + 8 * l) = y;
+      put(tiles + (h * kBlock + j) * D, at, x);
+      put(tiles + ((hc + h) * kBlock + j) * D, at, y);
     }
   }
   __syncthreads();
+#pragma unroll 1
   for (int i = warp; i < 2 * kvn; i += 8) {
     const bool is_k = i < kvn;
     const int h = is_k ? i : i - kvn;
@@ -546,20 +495,25 @@ __global__ void __launch_bounds__(256) rope_prefill_kernel(const __grid_constant
   }
 }
 
+// Calls fn with the compile-time form of (d, type of the projection, kind of pairs).
+template <class F>
+cudaError_t form(const RopeArgs& a, F&& fn) {
+  auto pairs = [&](auto d, auto t) {
+    return a.interleaved ? fn(d, t, std::true_type()) : fn(d, t, std::false_type());
+  };
+  auto type = [&](auto d) { return a.in_f32 ? pairs(d, float()) : pairs(d, __nv_bfloat16()); };
+  return a.d == 128 ? type(std::integral_constant<int, 128>()) : type(std::integral_constant<int, 64>());
+}
+
 }  // namespace
 
 cudaError_t launch_rope_step(const RopeArgs& a, cudaStream_t st) {
-  const int lph = a.d / 8;
-  const int64_t threads = (int64_t)a.B * (a.Hq + 2 * a.Hkv) * lph;
+  const int64_t threads = (int64_t)a.B * (a.Hq + 2 * a.Hkv) * (a.d / 8);
   const unsigned grid = (unsigned)((threads + 127) / 128);
-  if (a.d == 128) {
-    if (a.in_f32) rope_step_kernel<128, float><<<grid, 128, 0, st>>>(a);
-    else rope_step_kernel<128, __nv_bfloat16><<<grid, 128, 0, st>>>(a);
-  } else {
-    if (a.in_f32) rope_step_kernel<64, float><<<grid, 128, 0, st>>>(a);
-    else rope_step_kernel<64, __nv_bfloat16><<<grid, 128, 0, st>>>(a);
-  }
-  return cudaGetLastError();
+  return form(a, [&](auto d, auto t, auto inter) {
+    rope_step_kernel<decltype(d)::value, decltype(t), decltype(inter)::value><<<grid, 128, 0, st>>>(a);
+    return cudaGetLastError();
+  });
 }
 
 cudaError_t launch_rope_prefill(const RopePrefillArgs& g, int sms, cudaStream_t st) {
@@ -572,14 +526,10 @@ cudaError_t launch_rope_prefill(const RopePrefillArgs& g, int sms, cudaStream_t 
   while (hc > 1 && (int64_t)blocks * ((a.Hkv + hc - 1) / hc) < 4 * sms) hc = (hc + 1) / 2;
   const dim3 grid(blocks, (a.Hkv + hc - 1) / hc);
   const size_t smem = (size_t)2 * hc * kBlock * a.d * 2;
-  if (a.d == 128) {
-    if (a.in_f32) rope_prefill_kernel<128, float><<<grid, 256, smem, st>>>(g, hc);
-    else rope_prefill_kernel<128, __nv_bfloat16><<<grid, 256, smem, st>>>(g, hc);
-  } else {
-    if (a.in_f32) rope_prefill_kernel<64, float><<<grid, 256, smem, st>>>(g, hc);
-    else rope_prefill_kernel<64, __nv_bfloat16><<<grid, 256, smem, st>>>(g, hc);
-  }
-  return cudaGetLastError();
+  return form(a, [&](auto d, auto t, auto inter) {
+    rope_prefill_kernel<decltype(d)::value, decltype(t), decltype(inter)::value><<<grid, 256, smem, st>>>(g, hc);
+    return cudaGetLastError();
+  });
 }
 
 }  // namespace compkv
