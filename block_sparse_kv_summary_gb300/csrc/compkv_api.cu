@@ -472,8 +472,12 @@ compkv_status page_base(const compkv_ctx* c, int layer0, int layers, int n, cons
   for (int i = 0; i < n; ++i)
     if (writes[dst[i]] > 1 || reads[dst[i]] > (src[i] == dst[i] ? 1 : 0))
       return fail(COMPKV_ERR_INVALID_ARG, "pair %d: sequence %d is written and takes part in another pair", i, dst[i]);
-  PageArgs a;
-  memset(&a, 0, sizeof(a));
+  PageArgs& a = *out;
+  a.verdict = nullptr;
+  a.keep = nullptr;
+  a.keep_blocks = 0;
+  a.groups = 0;
+  a.kv_host = c->kv_host;
   a.k = reinterpret_cast<__nv_bfloat16*>(c->buf.k);
   a.v = reinterpret_cast<__nv_bfloat16*>(c->buf.v);
   a.kbar = c->buf.kbar;
@@ -493,7 +497,6 @@ compkv_status page_base(const compkv_ctx* c, int layer0, int layers, int n, cons
     a.seq_row0[s] = c->lay.seq_row0[s];
     a.cap_blocks[s] = c->lay.cap_blocks[s];
   }
-  *out = a;
   return COMPKV_OK;
 }
 
@@ -545,6 +548,7 @@ compkv_status compkv_init(const compkv_config* cfg, const compkv_buffers* bufs, 
   // the kernels' shared memory limits and cluster size, once for this configuration
   cudaError_t e = prepare_stream(cfg->head_dim, cfg->r, cfg->group_size);
   if (e == cudaSuccess) e = prepare_post(cfg->head_dim, cfg->group_size, L.C, L.bpc_max, L.K);
+  if (e == cudaSuccess) e = prepare_pages(cfg->head_dim);
   if (e == cudaSuccess) e = prepare_shared(cfg->head_dim);
   if (e != cudaSuccess) {
     delete c;
@@ -778,7 +782,7 @@ compkv_status compkv_fork(compkv_ctx* c, int layer0, int layers, int n, const in
   a.item0[a.groups] = items;
   if (items > 0x7fffffff) return fail(COMPKV_ERR_UNSUPPORTED_SHAPE, "the copies need more than 2^31 - 1 work items");
   cudaStream_t st = (cudaStream_t)stream;
-  return launch(c, COMPKV_KERNEL_FORK, st, "fork launch", [&] { return launch_fork(a, st); });
+  return launch(c, COMPKV_KERNEL_FORK, st, "fork launch", [&] { return launch_fork(a, device_sms(), st); });
 }
 
 compkv_status compkv_compact(compkv_ctx* c, int layer0, int layers, int n, const int* src, const int* dst,

@@ -134,6 +134,7 @@ struct PageArgs {
   int64_t rows_per_layer;
   int layer0, layers, n;       // n pairs
   int B, Hkv, d, r;
+  int kv_host;                 // k and v are host memory
   int groups;                  // copies: pairs with one source stand together and make a group
   int64_t seq_row0[kMaxBatch];
   int cap_blocks[kMaxBatch];

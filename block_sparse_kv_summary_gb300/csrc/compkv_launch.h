@@ -33,7 +33,8 @@ cudaError_t launch_rope_prefill(const RopePrefillArgs& a, int sms, cudaStream_t 
 // Pages: copies between sequences, and listed blocks to the front of a sequence.
 constexpr int kForkBlocks = 16;  // blocks of one work item of a copy
 inline int fork_chunks(int blocks) { return blocks < 1 ? 1 : (blocks + kForkBlocks - 1) / kForkBlocks; }
-cudaError_t launch_fork(const PageArgs& a, cudaStream_t st);
+cudaError_t prepare_pages(int d);
+cudaError_t launch_fork(const PageArgs& a, int sms, cudaStream_t st);
 cudaError_t launch_compact(const PageArgs& a, cudaStream_t st);
 // Attention over a shared prefix and the sequences' own tokens.
 // Query rows of one entry at most, and the workspace's rows: every entry's rows of every head once, and an

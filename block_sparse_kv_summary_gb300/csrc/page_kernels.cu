@@ -30,9 +30,6 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, int chunks) {
       if (i + u * kThreads < chunks) d[i + u * kThreads] = t[u];
   }
 }
-__device__ __forceinline__ void copy4(float* dst, const float* src, int n) {
-  for (int i = threadIdx.x; i < n; i += kThreads) dst[i] = src[i];
-}
 
 // Tokens that pair i of this layer copies; -1 when it is refused.
 __device__ __forceinline__ int pair_len(const PageArgs& a, int layer, int i, int held, bool report) {
@@ -44,56 +41,186 @@ __device__ __forceinline__ int pair_len(const PageArgs& a, int layer, int i, int
   return len;
 }
 
-// One CTA per (group of pairs with one source, layer, head, 16 blocks).
-template <int D>
-__global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ PageArgs a) {
-  int g = 0;
-  while (g + 1 < a.groups && a.item0[g + 1] <= (int64_t)blockIdx.x) ++g;
-  const int64_t per = (a.item0[g + 1] - a.item0[g]) / (a.layers * a.Hkv);  // chunks of a (layer, head)
-  int64_t x = (int64_t)blockIdx.x - a.item0[g];
-  const int b0 = (int)(x % per) * kForkBlocks;
-  x /= per;
-  const int h = (int)(x % a.Hkv), layer = a.layer0 + (int)(x / a.Hkv);
-  const int s = a.src[a.pair0[g]];
-  const int held = max(0, min(__ldcg(a.seq_len + (int64_t)layer * a.B + s), a.cap_blocks[s] * kBlock));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// A work item of a copy: 16 blocks of a (group of pairs with one source, layer, head).
+struct Item {
+  int g, layer, h, b0;
+};
+__device__ __forceinline__ Item fork_item(const PageArgs& a, int64_t it) {
+  Item x;
+  x.g = 0;
+  while (x.g + 1 < a.groups && a.item0[x.g + 1] <= it) ++x.g;
+  const int64_t per = (a.item0[x.g + 1] - a.item0[x.g]) / (a.layers * a.Hkv);  // chunks of a (layer, head)
+  it -= a.item0[x.g];
+  x.b0 = (int)(it % per) * kForkBlocks;
+  it /= per;
+  x.h = (int)(it % a.Hkv);
+  x.layer = a.layer0 + (int)(it / a.Hkv);
+  return x;
+}
+__device__ __forceinline__ int held_tokens(const PageArgs& a, int layer, int s) {
+  return max(0, min(__ldcg(a.seq_len + (int64_t)layer * a.B + s), a.cap_blocks[s] * kBlock));
+}
 
-  for (int i = a.pair0[g]; i < a.pair0[g + 1]; ++i) {
+// What remains of an item beside the bulk of it, by one warp: lengths, grouped variances, the summary of a block
+// that the copy leaves incomplete, cuts in place.
+template <int D>
+__device__ __forceinline__ void fork_rest(const PageArgs& a, const Item& x, int held, int lane) {
+  const int s = a.src[a.pair0[x.g]];
+  const bool first = !x.h && !x.b0;
+  for (int i = a.pair0[x.g]; i < a.pair0[x.g + 1]; ++i) {
     const int to = a.dst[i];
-    if (to == s) {  // a cut in place: one CTA for all heads, the length last
-      if (h || b0) continue;
-      const int len = pair_len(a, layer, i, held, threadIdx.x == 0);
-      const int part = len % kBlock;
-      __syncthreads();  // every thread has read the length
-      if (len < 0) continue;
-      if (part && len < held)
-        for (int hh = warp; hh < a.Hkv; hh += kThreads / 32) {
-          const int64_t row = first_row(a, layer, s, hh) + len / kBlock;
-          warp_block_summary<D>(a.k + row * kBlock * D, a.v + row * kBlock * D, part, nullptr, nullptr,
-                                a.kbar + row * D, a.vbar + row * D, a.dbar + row * a.r, a.r, lane);
-        }
-      if (threadIdx.x == 0) a.seq_len[(int64_t)layer * a.B + to] = len;
+    if (to == s && !first) continue;
+    const int len = pair_len(a, x.layer, i, held, first && lane == 0);
+    if (len < 0) continue;
+    const int part = len % kBlock;
+    if (to == s) {  // a cut in place: one warp for all heads, the length last
+      for (int h = 0; part && len < held && h < a.Hkv; ++h) {
+        const int64_t row = first_row(a, x.layer, s, h) + len / kBlock;
+        warp_block_summary<D>(a.k + row * kBlock * D, a.v + row * kBlock * D, part, nullptr, nullptr, a.kbar + row * D,
+                              a.vbar + row * D, a.dbar + row * a.r, a.r, lane);
+      }
+      if (lane == 0) a.seq_len[(int64_t)x.layer * a.B + to] = len;
       continue;
     }
-    const bool first = !h && !b0;
-    const int len = pair_len(a, layer, i, held, first && threadIdx.x == 0);
-    if (len < 0) continue;
-    if (first && threadIdx.x == 0) a.seq_len[(int64_t)layer * a.B + to] = len;
-    const int tokens = min(len - b0 * kBlock, kForkBlocks * kBlock);
+    if (first && lane == 0) a.seq_len[(int64_t)x.layer * a.B + to] = len;
+    const int tokens = min(len - x.b0 * kBlock, kForkBlocks * kBlock);
     if (tokens <= 0) continue;
-    const int64_t rs = first_row(a, layer, s, h) + b0, rd = first_row(a, layer, to, h) + b0;
-    copy16(a.k + rd * kBlock * D, a.k + rs * kBlock * D, tokens * D / 8);
-    copy16(a.v + rd * kBlock * D, a.v + rs * kBlock * D, tokens * D / 8);
-    // the summary of a block that this cut leaves incomplete is formed from its tokens; others are copied
-    const int part = tokens % kBlock;
-    const bool cut = part && len < held;
-    const int nb = tokens / kBlock + (part && !cut);
-    copy16(a.kbar + rd * D, a.kbar + rs * D, nb * D / 4);
-    copy16(a.vbar + rd * D, a.vbar + rs * D, nb * D / 4);
-    copy4(a.dbar + rd * a.r, a.dbar + rs * a.r, nb * a.r);
-    if (cut && warp == 0)
+    const int64_t rs = first_row(a, x.layer, s, x.h) + x.b0, rd = first_row(a, x.layer, to, x.h) + x.b0;
+    const bool cut = part && len < held && tokens < kForkBlocks * kBlock;
+    const int nb = tokens / kBlock + (tokens % kBlock && !cut);
+    for (int c = lane; c < nb * a.r; c += 32) a.dbar[rd * a.r + c] = a.dbar[rs * a.r + c];
+    if (cut)
       warp_block_summary<D>(a.k + (rs + nb) * kBlock * D, a.v + (rs + nb) * kBlock * D, part, nullptr, nullptr,
                             a.kbar + (rd + nb) * D, a.vbar + (rd + nb) * D, a.dbar + (rd + nb) * a.r, a.r, lane);
+  }
+}
+
+// Persistent CTAs.  One thread moves the runs of K, V, kbar and vbar by bulk
+// copies through a ring of stages in shared memory: each run is read once and
+// written to every destination of the group; a warp does the rest of the items.
+// Bound by DRAM, mostly by its writes.
+constexpr int kStageBytes = 32 * 1024, kForkStages = 3;
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+template <int D>
+__global__ void __launch_bounds__(64) fork_bulk_kernel(const __grid_constant__ PageArgs a) {
+  extern __shared__ __align__(128) char ring[];
+  __shared__ __align__(8) uint64_t full[kForkStages];
+  const int64_t items = a.item0[a.groups];
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kForkStages; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (threadIdx.x >= 32) {
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+      const Item x = fork_item(a, it);
+      fork_rest<D>(a, x, held_tokens(a, x.layer, a.src[a.pair0[x.g]]), lane);
+    }
+    return;
+  }
+  if (lane) return;
+
+  struct Run {
+    Item x;
+    int held, kind, off, bytes;  // array, and bytes of the item's run in it
+  };
+  constexpr int kRow[4] = {kBlock * D * 2, kBlock * D * 2, D * 4, D * 4};  // bytes of a block
+  char* base[4] = {reinterpret_cast<char*>(a.k), reinterpret_cast<char*>(a.v), reinterpret_cast<char*>(a.kbar),
+                   reinterpret_cast<char*>(a.vbar)};
+  // bytes of an item that `len` tokens give in an array; the summary of a block left incomplete is not copied
+  auto extent = [&](const Run& r, int len, int kind) {
+    const int tokens = max(0, min(len - r.x.b0 * kBlock, kForkBlocks * kBlock));
+    if (kind < 2) return tokens * D * 2;
+    return (tokens / kBlock + (tokens % kBlock && len == r.held)) * (D * 4);
+  };
+  Run run[kForkStages];
+  int64_t it = blockIdx.x;
+  Run cur;
+  int most = 0;  // tokens that the longest copy of the current item's group takes
+  bool open = false;
+  auto next = [&](Run& r) {  // the next run with bytes in it
+    for (;;) {
+      if (!open) {
+        if (it >= items) return false;
+        cur.x = fork_item(a, it);
+        it += gridDim.x;
+        const int s = a.src[a.pair0[cur.x.g]];
+        cur.held = held_tokens(a, cur.x.layer, s);
+        most = -1;
+        for (int i = a.pair0[cur.x.g]; i < a.pair0[cur.x.g + 1]; ++i)
+          if (a.dst[i] != s) most = max(most, pair_len(a, cur.x.layer, i, cur.held, false));
+        if (most < 0) continue;
+        cur.kind = cur.off = 0;
+        open = true;
+      }
+      const int all = extent(cur, most, cur.kind);
+      if (cur.off >= all) {
+        cur.off = 0;
+        open = ++cur.kind < 4;
+        continue;
+      }
+      cur.bytes = min(all - cur.off, kStageBytes);
+      r = cur;
+      cur.off += cur.bytes;
+      return true;
+    }
+  };
+  int loads = 0, done = 0;
+  bool more = true, lost = false;
+  while (!lost) {
+    while (more && loads < done + kForkStages - 1) {
+      const int st = loads % kForkStages;
+      // the stores out of this stage, kForkStages loads ago, have read it: all but the last group have
+      if (loads >= kForkStages) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      if (!(more = next(run[st]))) break;
+      const Run& r = run[st];
+      const char* src = base[r.kind] + (first_row(a, r.x.layer, a.src[a.pair0[r.x.g]], r.x.h) + r.x.b0) * kRow[r.kind] + r.off;
+      mbar_arrive_expect_tx(&full[st], r.bytes);
+      bulk_g2s(ring + st * kStageBytes, src, r.bytes, &full[st]);
+      ++loads;
+    }
+    if (done == loads) break;
+    const int st = done % kForkStages;
+    lost = !mbar_wait_bounded(&full[st], (done / kForkStages) & 1, a.status, -1, -1, 60);
+    const Run& r = run[st];
+    const int s = a.src[a.pair0[r.x.g]];
+    for (int i = a.pair0[r.x.g]; !lost && i < a.pair0[r.x.g + 1]; ++i) {
+      if (a.dst[i] == s) continue;
+      const int len = pair_len(a, r.x.layer, i, r.held, false);
+      const int n = len < 0 ? 0 : min(extent(r, len, r.kind) - r.off, r.bytes);
+      if (n > 0)
+        bulk_s2g(base[r.kind] + (first_row(a, r.x.layer, a.dst[i], r.x.h) + r.x.b0) * kRow[r.kind] + r.off, ring + st * kStageBytes, n);
+    }
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    ++done;
+  }
+  if (lost)
+    for (; done < loads; ++done) mbar_drain_bounded(&full[done % kForkStages]);
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// The same with plain loads and stores, for K and V in host memory: one CTA
+// per item.
+template <int D>
+__global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ PageArgs a) {
+  const Item x = fork_item(a, blockIdx.x);
+  const int s = a.src[a.pair0[x.g]], held = held_tokens(a, x.layer, s);
+  __syncthreads();  // every thread has read the length, which a cut in place changes
+  if (threadIdx.x < 32) fork_rest<D>(a, x, held, threadIdx.x);
+  for (int i = a.pair0[x.g]; i < a.pair0[x.g + 1]; ++i) {
+    const int len = a.dst[i] == s ? -1 : pair_len(a, x.layer, i, held, false);
+    const int tokens = min(len - x.b0 * kBlock, kForkBlocks * kBlock);
+    if (tokens <= 0) continue;
+    const int64_t rs = first_row(a, x.layer, s, x.h) + x.b0, rd = first_row(a, x.layer, a.dst[i], x.h) + x.b0;
+    copy16(a.k + rd * kBlock * D, a.k + rs * kBlock * D, tokens * D / 8);
+    copy16(a.v + rd * kBlock * D, a.v + rs * kBlock * D, tokens * D / 8);
+    const int nb = tokens / kBlock + (tokens % kBlock && len == held);
+    copy16(a.kbar + rd * D, a.kbar + rs * D, nb * D / 4);
+    copy16(a.vbar + rd * D, a.vbar + rs * D, nb * D / 4);
   }
 }
 
@@ -264,11 +391,23 @@ __global__ void __launch_bounds__(kThreads) compact_in_place_kernel(const __grid
 
 }  // namespace
 
-cudaError_t launch_fork(const PageArgs& a, cudaStream_t st) {
-  const unsigned grid = (unsigned)a.item0[a.groups];
-  if (a.d == 128) fork_kernel<128><<<grid, kThreads, 0, st>>>(a);
-  else fork_kernel<64><<<grid, kThreads, 0, st>>>(a);
+cudaError_t launch_fork(const PageArgs& a, int sms, cudaStream_t st) {
+  const int64_t items = a.item0[a.groups];
+  if (a.kv_host) {
+    if (a.d == 128) fork_kernel<128><<<(unsigned)items, kThreads, 0, st>>>(a);
+    else fork_kernel<64><<<(unsigned)items, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  const unsigned grid = (unsigned)(items < 2 * sms ? items : 2 * sms);
+  const int smem = kForkStages * kStageBytes;
+  if (a.d == 128) fork_bulk_kernel<128><<<grid, 64, smem, st>>>(a);
+  else fork_bulk_kernel<64><<<grid, 64, smem, st>>>(a);
   return cudaGetLastError();
+}
+
+cudaError_t prepare_pages(int d) {
+  return raise_smem_limit(d == 128 ? (const void*)fork_bulk_kernel<128> : (const void*)fork_bulk_kernel<64>,
+                          kForkStages * kStageBytes);
 }
 
 cudaError_t launch_compact(const PageArgs& a, cudaStream_t st) {
