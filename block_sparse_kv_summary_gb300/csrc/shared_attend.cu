@@ -13,11 +13,12 @@
 //
 // Within a CTA (tcgen05; a step is one K/V tile times 128 rows, one or two
 // steps a tile, one step in flight behind the other):
-//   warp 8   copies K and V tiles by tensor maps into a ring of stages,
-//   warp 9   issues S = Q K^T into one of two TMEM buffers,
-//   warp 10  issues O += P V,
-//   warps 0-7 load Q, take the weights and their sum (thread = row and half of
-//            the keys), and write the weights P over S in TMEM.
+//   warp 16  copies K and V tiles by tensor maps into a ring of stages,
+//   warp 17  issues S = Q K^T into one of two TMEM buffers,
+//   warp 18  issues O += P V,
+//   warps 0-15 load Q, take the weights and their sum (thread = row and quarter
+//            of the keys; with halves, in eight warps, a step took half as long
+//            again), and write the weights P over S in TMEM.
 // Weights are e^(z - reference).  The reference is the row's maximum in the
 // piece's first tile and stays while the weights of a tile add up to less than
 // 2^30: floating point loses nothing by a common factor, and the join divides
@@ -39,7 +40,8 @@ namespace compkv {
 namespace {
 
 constexpr int kTile = 128;                // keys of a tile, and query rows of an item at most
-constexpr int kSoftmaxWarps = 8;
+constexpr int kSoftmaxWarps = 16;
+constexpr int kCols = kTile / (kSoftmaxWarps / 4);  // keys of a tile that a softmax thread has, for one row
 constexpr int kThreads = 32 * (kSoftmaxWarps + 4);  // registers are dealt out by groups of four warps
 constexpr float kMostWeight = 1073741824.f;  // 2^30: what a tile's weights of a row may add up to
 constexpr size_t kSmemLimit = 232448;
@@ -209,37 +211,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float* f) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld64(uint32_t addr, float* f) {
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float* f) {
   uint32_t* r = reinterpret_cast<uint32_t*>(f);
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%2"
-      "6,%27,%28,%29,%30,%31"
-      "}, [%64];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,"
-      "%56,%57,%58,%59,%60,%61,%62,%63"
-      "}, [%65];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15"
+      "}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
-        "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
-        "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
-        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
-        "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-      : "r"(addr), "r"(addr + 32)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
@@ -283,7 +264,7 @@ struct Shape {
 struct Control {
   Plan plan;
   unsigned char member[kMaxBatch];  // of the arguments: there a warp's lanes would read them one after another
-  float row_max[2][kTile];  // [half of the keys][row]; sums at the end of a segment
+  float row_max[kTile / kCols][kTile];  // [part of the keys][row]; sums at the end of a segment
   uint64_t full[8], empty[8], q_full, s_full[2], p_full[2], o_full[2];  // [tile & 1]
   uint32_t tmem;
   int abort;
@@ -319,18 +300,18 @@ __device__ __forceinline__ bool warp_wait(Control* ctl, uint64_t* bar, uint32_t 
 
 // Scores behind the last key.
 __device__ __forceinline__ void mask(float* s, int valid) {
-  if (valid < 64) {
+  if (valid < kCols) {
 #pragma unroll
-    for (int i = 0; i < 64; ++i)
+    for (int i = 0; i < kCols; ++i)
       if (i >= valid) s[i] = -INFINITY;
   }
 }
-// Weights 2^(scale s - m) in the place of 64 scores (m = -inf, before a piece's first tile: as if 0); their sum.
+// Weights 2^(scale s - m) in the place of scores (m = -inf, before a piece's first tile: as if 0); their sum.
 __device__ __forceinline__ float weights(float* s, float scale, float m) {
   const float ref = m == -INFINITY ? 0.f : m;
   float2 sum[2] = {};
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
+  for (int i = 0; i < kCols / 2; ++i) {
     const float2 x = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), make_float2(scale, scale), make_float2(-ref, -ref));
     s[2 * i] = exp2_approx(x.x);
     s[2 * i + 1] = exp2_approx(x.y);
@@ -338,14 +319,16 @@ __device__ __forceinline__ float weights(float* s, float scale, float m) {
   }
   return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
-// Whether `p` holds for a lane of the two warps that meet at barrier `id`.
-__device__ __forceinline__ bool pair_any(int id, bool p) {
+// The warps of the same 32 rows meet at barrier `id`; whether `p` holds for one of their lanes.
+constexpr int kRowThreads = kSoftmaxWarps / 4 * 32;
+__device__ __forceinline__ void meet(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kRowThreads) : "memory"); }
+__device__ __forceinline__ bool any_of(int id, bool p) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %2, 0;\n\tbarrier.cta.red.or.pred b, %1, 64, a;\n\t"
+      "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %2, 0;\n\tbarrier.cta.red.or.pred b, %1, %3, a;\n\t"
       "selp.u32 %0, 1, 0, b;\n\t}"
       : "=r"(r)
-      : "r"(id), "r"((uint32_t)p)
+      : "r"(id), "r"((uint32_t)p), "n"(kRowThreads)
       : "memory");
   return r != 0;
 }
@@ -575,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
   Segment g;
 
   if (warp >= kSoftmaxWarps) {
-    fewer_registers<72>();  // 128 x 72 + 256 x 216: the 384 x 168 of the launch
+    fewer_registers<64>();  // 128 x 64 + 512 x 104: the 640 x 96 of the launch
     if (warp == kSoftmaxWarps) {
       // ---- copies: K and V of every tile in turn, 16-token boxes where the item ends inside the tile
       if (lane == 0) {
@@ -699,9 +682,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
       }
     }
   } else {
-    more_registers<216>();
-    // ---- softmax: thread = row (its TMEM lane) and half of the keys
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    more_registers<104>();
+    // ---- softmax: thread = row (its TMEM lane) and a quarter of the keys, and of O's coordinates
+    constexpr int OC = D * kCols / kTile;
+    const int quarter = warp >> 2, row = (warp & 3) * 32 + lane, bar = 1 + (warp & 3);
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const float scale = 1.4426950408889634f / sqrtf((float)D);  // logits in powers of two
     int n = 0;
@@ -716,35 +700,37 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
       const Segment cur = g;
       const int rows = a.rows[cur.e], subs = (rows + kTile - 1) / kTile;
       float m2[2] = {-INFINITY, -INFINITY}, l2[2] = {0.f, 0.f};  // per 128 rows: reference of the weights, their sum here
-      float acc[S::kTileO ? D / 2 : 1] = {};                     // kTileO: O so far, in units of the reference
+      float acc[S::kTileO ? OC : 1] = {};                        // kTileO: O so far, in units of the reference
       for (int t = cur.tile0; t < cur.tile1; ++t) {
         for (int sub = 0; sub < subs; ++sub, ++n) {
           warp_wait(ctl, &ctl->s_full[n & 1], (n >> 1) & 1, a.status, 56);
           fence_after();
-          if (sub * kTile + (warp & 3) * 32 < rows) {  // the same for both warps of these rows
+          if (sub * kTile + (warp & 3) * 32 < rows) {  // the same for all warps of these rows
             const uint32_t buf = tmem + lanes + (n & 1) * S::kBuffer;
-            const uint32_t o_at = tmem + lanes + S::kO + sub * D + half * (D / 2);
-            float s[64];
-            tmem_ld64(buf + half * 64, s);
-            const int valid = cur.valid(t) - half * 64;  // keys of this half
+            const uint32_t o_at = tmem + lanes + S::kO + sub * D + quarter * OC;
+            float s[kCols];
+            tmem_ld32(buf + quarter * kCols, s);
+            const int valid = cur.valid(t) - quarter * kCols;  // keys of this quarter
             mask(s, valid);
             float m = sub ? m2[1] : m2[0], l = sub ? l2[1] : l2[0], f = 1.f;
             float sum = weights(s, scale, m);
-            // both halves have read S when they have passed, and P may take its place
+            // all have read S when they have passed, and P may take its place
             fence_before();
-            bool raise = pair_any(1 + (warp & 3), sub * kTile + row < rows && (t == cur.tile0 || !(sum < kMostWeight)));
+            const bool raise = any_of(bar, sub * kTile + row < rows && (t == cur.tile0 || !(sum < kMostWeight)));
             fence_after();
             if (raise) {
-              tmem_ld64(buf + half * 64, s);
+              tmem_ld32(buf + quarter * kCols, s);
               mask(s, valid);
               float top = s[0];
 #pragma unroll
-              for (int i = 1; i < 64; ++i) top = fmaxf(top, s[i]);
-              ctl->row_max[half][row] = top * scale;
+              for (int i = 1; i < kCols; ++i) top = fmaxf(top, s[i]);
+              ctl->row_max[quarter][row] = top * scale;
               fence_before();
-              asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
+              meet(bar);
               fence_after();
-              top = fmaxf(fmaxf(top * scale, ctl->row_max[half ^ 1][row]), m);
+              top = m;
+#pragma unroll
+              for (int i = 0; i < kTile / kCols; ++i) top = fmaxf(top, ctl->row_max[i][row]);
               if (top == -INFINITY) top = 0.f;
               f = exp2_approx(m - top);  // 0 in the first tile: m = -inf
               m = top;
@@ -756,15 +742,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 if (subs == 1) warp_wait(ctl, &ctl->o_full[(n - 1) & 1], ((n - 1) >> 1) & 1, a.status, 57);
                 fence_after();
 #pragma unroll
-                for (int x = 0; x < D / 64; ++x) {
-                  float o[32];
-                  tmem_ld32(o_at + 32 * x, o);
+                for (int x = 0; x < OC / 16; ++x) {
+                  float o[16];
+                  tmem_ld16(o_at + 16 * x, o);
 #pragma unroll
-                  for (int i = 0; i < 32; ++i) o[i] *= f;
-                  tmem_st32(o_at + 32 * x, reinterpret_cast<const uint32_t*>(o));
+                  for (int i = 0; i < 16; ++i) o[i] *= f;
+                  tmem_st16(o_at + 16 * x, reinterpret_cast<const uint32_t*>(o));
                 }
               }
-              asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");  // the maxima have been read
+              meet(bar);  // the maxima have been read
             }
             l += sum;
             if (sub) {
@@ -776,28 +762,25 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             }
 #pragma unroll
             for (int part = 0; part < PARTS; ++part) {
+              uint32_t w[kCols / 2];
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                uint32_t w[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = split2(s[32 * x + 2 * i], s[32 * x + 2 * i + 1]);
-                tmem_st16(buf + part * 64 + half * 32 + 16 * x, w);
-              }
+              for (int i = 0; i < kCols / 2; ++i) w[i] = split2(s[2 * i], s[2 * i + 1]);
+              tmem_st16(buf + part * 64 + quarter * (kCols / 2), w);
             }
             if (S::kTileO && t > cur.tile0) {
               // O of the tile before, in the reference of its weights; the next product waits for p_full
               warp_wait(ctl, &ctl->o_full[(n - 1) & 1], ((n - 1) >> 1) & 1, a.status, 57);
               fence_after();
 #pragma unroll
-              for (int x = 0; x < D / 64; ++x) {
-                float o[32];
-                tmem_ld32(o_at + 32 * x, o);
+              for (int x = 0; x < OC / 16; ++x) {
+                float o[16];
+                tmem_ld16(o_at + 16 * x, o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) acc[(32 * x + i) % (S::kTileO ? D / 2 : 1)] += o[i];
+                for (int i = 0; i < 16; ++i) acc[(16 * x + i) % (S::kTileO ? OC : 1)] += o[i];
               }
               if (raise) {
 #pragma unroll
-                for (int i = 0; i < D / 2; ++i) acc[i % (S::kTileO ? D / 2 : 1)] *= f;
+                for (int i = 0; i < OC; ++i) acc[i % (S::kTileO ? OC : 1)] *= f;
               }
             }
             wait_st();
@@ -821,26 +804,29 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         const int r = sub * kTile + row;
         if (sub * kTile + (warp & 3) * 32 >= rows) break;
         float l = sub ? l2[1] : l2[0];
-        if (half) ctl->row_max[0][row] = l;
-        asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
-        if (!half) l += ctl->row_max[0][row];
-        const int64_t at = segment_row(a, cur.e, cur.h, c) + r;
-        float* dst = a.acc + at * D + half * (D / 2);
+        ctl->row_max[quarter][row] = l;
+        meet(bar);
+        if (!quarter) {
 #pragma unroll
-        for (int x = 0; x < D / 64; ++x) {
-          float o[32];
-          tmem_ld32(tmem + lanes + S::kO + sub * D + half * (D / 2) + 32 * x, o);
+          for (int i = 1; i < kTile / kCols; ++i) l += ctl->row_max[i][row];
+        }
+        const int64_t at = segment_row(a, cur.e, cur.h, c) + r;
+        float* dst = a.acc + at * D + quarter * OC;
+#pragma unroll
+        for (int x = 0; x < OC / 16; ++x) {
+          float o[16];
+          tmem_ld16(tmem + lanes + S::kO + sub * D + quarter * OC + 16 * x, o);
           if (S::kTileO) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] += acc[(32 * x + i) % (S::kTileO ? D / 2 : 1)];
+            for (int i = 0; i < 16; ++i) o[i] += acc[(16 * x + i) % (S::kTileO ? OC : 1)];
           }
           if (r < rows) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) store_sector(dst + 32 * x + 8 * i, o + 8 * i);
+            store_sector(dst + 16 * x, o);
+            store_sector(dst + 16 * x + 8, o + 8);
           }
         }
-        if (!half && r < rows) a.ml[at] = make_float2(sub ? m2[1] : m2[0], l);
-        asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");  // the sums have been read
+        if (!quarter && r < rows) a.ml[at] = make_float2(sub ? m2[1] : m2[0], l);
+        meet(bar);  // the sums have been read
       }
       fence_before();
     }
@@ -858,8 +844,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
   if (!all_arrived(a, ctl)) return;
   // rows are dealt to the CTAs; few rows leave several warps for each
   constexpr int kWarps = kThreads / 32;
-  const int rows = a.B * a.Hkv * a.G, share = rows * 12 <= a.P * kWarps ? 12 : rows * 4 <= a.P * kWarps ? 4 : 1;
-  static_assert(kWarps == 12, "warps of a row");
+  const int rows = a.B * a.Hkv * a.G, share = rows <= a.P ? kWarps : rows * 4 <= a.P * kWarps ? 4 : 1;
+  static_assert(kWarps % 4 == 0, "warps of a row");
   for (int r0 = blockIdx.x * (kWarps / share); r0 < rows; r0 += a.P * (kWarps / share))
     join_row<D>(a, ctl->plan, r0 + warp / share, warp % share, share, reinterpret_cast<float*>(ring), lane);
 }
