@@ -262,6 +262,7 @@ LayerArgs base_args(const compkv_ctx* c, int layer) {
   static_assert(sizeof(a.tmap_k) == sizeof(CUtensorMap), "tensor map size");
   memcpy(a.tmap_k, &c->tmap_k, sizeof(CUtensorMap));
   memcpy(a.tmap_v, &c->tmap_v, sizeof(CUtensorMap));
+  a.layer_row0 = c->lay.rows_per_layer * (int64_t)layer;
   a.kv_host = c->kv_host;
   a.tmap_ok = c->tmap_ok;
   const int d = c->cfg.head_dim, r = c->cfg.r, G = c->cfg.group_size;

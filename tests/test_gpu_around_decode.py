@@ -650,3 +650,33 @@ def test_a_selection_compacts_and_decodes_on():
             a = heads_of(c, old[0], 0, s)[h][sel[s, h].long()].flatten(0, 1)[:lens[s]]
             assert torch.equal(c.token_view(0, s, h)[0][:lens[s]], a)
             check_summaries(c, 0, s, h, range(16), lens[s])
+
+
+def test_every_layer_reads_its_own_rows():
+    # the same tokens in layer 0 and in layer 2 of two caches: each call of layer 2 gives what it gives in layer 0
+    hkv, g, d = 2, 4, 128
+    one = filled([512, 256], [500, 130], layers=1, hkv=hkv, g=g, d=d, budget=128)
+    three = filled([512, 256], [9, 250], layers=3, hkv=hkv, g=g, d=d, seed=50, budget=128)
+    rows = one.k.shape[0]
+    for x, y in zip(state(three)[:5], (one.k, one.v, one.kbar, one.vbar, one.dbar)):
+        assert x.shape[0] == 3 * rows and y.shape[0] == rows
+    for x, y in zip((three.k, three.v, three.kbar, three.vbar, three.dbar), (one.k, one.v, one.kbar, one.vbar, one.dbar)):
+        x[2 * rows:] = y
+    three.seq_len[2] = one.seq_len[0]
+    q = randn(3, 2, hkv * g, d)
+    new = [randn(s, 2, hkv, d, dtype=torch.bfloat16) for s in (4, 5)]
+    a, b = (c.attend_shared(l, q, [0, 0], [400, 0]) for c, l in ((one, 0), (three, 2)))
+    assert torch.equal(a, b)
+    a, b = (c.decode(l, q, *new) for c, l in ((one, 0), (three, 2)))
+    assert torch.equal(a, b)
+    qkv, tab = randn(6, 40, (g + 2) * hkv * d), table(600, d)
+    a, b = (c.prefill_qkv(l, qkv, [3, 37], tab, starts=[500, 0]) for c, l in ((one, 0), (three, 2)))
+    assert torch.equal(a, b)
+    one.fork([0], [1], [200])
+    three.fork([0], [1], [200], layers=(2, 3))
+    keep = torch.tensor([[[0, 2, 5, 12]] * hkv], dtype=torch.int32, device="cuda")[None]
+    one.compact(keep, [1])
+    three.compact(keep, [1], layers=(2, 3))
+    for x, y in zip((three.k, three.v, three.kbar, three.vbar, three.dbar), (one.k, one.v, one.kbar, one.vbar, one.dbar)):
+        assert torch.equal(x[2 * rows:], y)
+    assert torch.equal(three.seq_len[2], one.seq_len[0]) and one.device_status() == 0 and three.device_status() == 0
