@@ -528,10 +528,11 @@ cudaError_t launch_rope_prefill(const RopePrefillArgs& g, int sms, cudaStream_t 
   const RopeArgs& a = g.rope;
   const int blocks = g.item0[a.B];
   if (!blocks) return cudaSuccess;
-  // KV heads of a CTA: four read a token's angles once for all of them and leave room for several CTAs on a
-  // multiprocessor; fewer where the blocks alone would not give every multiprocessor four
+  // KV heads of a CTA: four read a token's angles once for all of them and leave room for three CTAs on a
+  // multiprocessor; fewer where that would not give every multiprocessor eight (32K tokens: 164 us with four, 205
+  // with one; 2500 tokens with 80 heads: 34 with two, 29 with one)
   int hc = a.Hkv < 4 ? a.Hkv : 4;
-  while (hc > 1 && (int64_t)blocks * ((a.Hkv + hc - 1) / hc) < 4 * sms) hc = (hc + 1) / 2;
+  while (hc > 1 && (int64_t)blocks * ((a.Hkv + hc - 1) / hc) < 8 * sms) hc = (hc + 1) / 2;
   const dim3 grid(blocks, (a.Hkv + hc - 1) / hc);
   const size_t smem = (size_t)2 * hc * kBlock * a.d * 2;
   // the prefetch pays where DRAM is the limit (32K tokens 170 -> 164 us) and costs where one wave of CTAs does it

@@ -200,6 +200,19 @@ def test_prefill_many_tokens(case, plan, r):
         assert torch.equal(o[~m], x[~m])
 
 
+def test_prefill_into_host_memory():
+    # K and V in page-locked memory: the same rows and summaries as in device memory
+    a, b = (make_cache([64, 96], hkv=2, g=2, kv_memory=m) for m in ("device", "host"))
+    tab, w = table(128, 64), 1 + 0.1 * randn(9, 64)
+    for x in (a, b):
+        for counts, starts, seed in (([9, 50], None, 1), ([30, 0], [9, 0], 2), ([0, 30], [0, 50], 3)):
+            x.prefill_qkv(0, randn(seed, sum(counts), 6 * 64 + 128), counts, tab, starts=starts, q_weight=w, k_weight=w)
+    torch.cuda.synchronize()
+    for x, y in zip(state(a), state(b)):
+        assert torch.equal(x, y.to(x.device))
+    assert a.seq_len.tolist() == [[39, 80]]
+
+
 def test_prefill_empty_and_positions_outside_the_table():
     c = make_cache([64, 64], hkv=1, g=1)
     q = c.prefill_qkv(0, torch.empty(0, 192, device="cuda"), [0, 0], table(64, 64))
@@ -303,10 +316,11 @@ def lists(c, layers, choice):
 
 @pytest.mark.parametrize("d,r,hkv", [(64, 1, 1), (128, 4, 8), (128, 128, 3), (64, 64, 2)])
 @pytest.mark.parametrize("inplace", [True, False])
-def test_compact(d, r, hkv, inplace):
+@pytest.mark.parametrize("kv_memory", ["device", "host"])
+def test_compact(d, r, hkv, inplace, kv_memory):
     held = [1999, 640, 5, 700]
     caps = [2048, 640, 64, 1024] * 2
-    c = filled(caps, held + [0] * 4, hkv=hkv, d=d, r=r)
+    c = filled(caps, held + [0] * 4, hkv=hkv, d=d, r=r, kv_memory=kv_memory)
     g = torch.Generator().manual_seed(3)
 
     def pick(n, blocks, last):
@@ -327,8 +341,8 @@ def test_compact(d, r, hkv, inplace):
         for i in range(4):
             want[5][l, dst[i]] = new_len[i]
             for h in range(hkv):
-                idx = torch.tensor(choice[l][i][h], dtype=torch.long, device="cuda")
                 for x, o in zip(want[:5], old[:5]):
+                    idx = torch.tensor(choice[l][i][h], dtype=torch.long, device=o.device)
                     a, b = heads_of(c, o, l, src[i])[h], heads_of(c, x, l, dst[i])[h]
                     if x.dim() == 3:
                         b.flatten(0, 1)[:new_len[i]] = a[idx].flatten(0, 1)[:new_len[i]]
@@ -471,6 +485,15 @@ def test_shared_extreme_logits(dtype):
     q = q.to(dtype)
     got = c.attend_shared(0, q, [0, 0], [900, 0])
     check_shared(got, *shared64(c, 0, q, [0, 0], [900, 0], [1000, 520]))
+
+
+def test_shared_nothing_at_all():
+    c = shared_cache([64, 64], [0, 0], 1, 8, 128)
+    q = randn(5, 2, 8, 128)
+    out = torch.full_like(q, 3.0)
+    assert not c.attend_shared(0, q, [0, 0], [0, 0], out=out).any()
+    out.fill_(3.0)
+    assert (c.attend_shared(0, q, [-2, -2], [0, 0], out=out) == 3).all() and c.device_status() == 0
 
 
 def test_shared_prefix_longer_than_its_holder():
@@ -680,3 +703,33 @@ def test_every_layer_reads_its_own_rows():
     for x, y in zip((three.k, three.v, three.kbar, three.vbar, three.dbar), (one.k, one.v, one.kbar, one.vbar, one.dbar)):
         assert torch.equal(x[2 * rows:], y)
     assert torch.equal(three.seq_len[2], one.seq_len[0]) and one.device_status() == 0 and three.device_status() == 0
+
+
+def test_rows_far_into_a_large_cache():
+    # 5 GB of keys: rows whose byte offsets pass 32 bits give what they give in a small cache
+    hkv, g, d = 8, 1, 128
+    big = make_cache([131072] * 20, hkv=hkv, g=g, d=d)
+    small = make_cache([1024] * 2, hkv=hkv, g=g, d=d)
+    assert big.k.numel() * 2 > 2 ** 32
+    qkv, tab = randn(1, 700, (g + 2) * hkv * d).bfloat16(), table(1024, d)
+    q = randn(2, 20, hkv * g, d)
+    counts = [0] * 19 + [700]
+    a = big.prefill_qkv(0, qkv, counts, tab)
+    b = small.prefill_qkv(0, qkv, [0, 700], tab)
+    assert torch.equal(a, b)
+    prefix_len = [0] * 19 + [650]
+    a = big.attend_shared(0, q, [-2] * 18 + [19, 19], prefix_len)
+    b = small.attend_shared(0, q[18:].contiguous(), [1, 1], [0, 650])
+    # pieces end elsewhere (other items come before): the same numbers, added in another order
+    assert (a[18:] - b).abs().max().item() <= 1e-5
+    keep = torch.tensor([[[0, 3, 9, 43]] * hkv], dtype=torch.int32, device="cuda")[None]
+    big.fork([19], [18], [690])
+    small.fork([1], [0], [690])
+    big.compact(keep, [18])
+    small.compact(keep, [0])
+    for s, t in ((18, 0), (19, 1)):
+        for h in range(hkv):
+            for x, y in zip(big.token_view(0, s, h) + big.summary_view(0, s, h), small.token_view(0, t, h) + small.summary_view(0, t, h)):
+                assert torch.equal(x[:40], y[:40])
+    assert big.seq_len[0, 18:].tolist() == small.seq_len[0].tolist() == [3 * 16 + 2, 700]
+    assert big.device_status() == 0 and small.device_status() == 0
