@@ -427,7 +427,7 @@ __device__ __forceinline__ void join_row(const SharedArgs& a, const Plan& plan, 
   const int total = plan.cum[a.entries];
   int count[2] = {0, 0}, c0[2] = {0, 0}, row[2] = {0, 0}, entry[2] = {0, 0}, begin[2] = {0, 0};
 #pragma unroll 1
-  for (int side = 0; side < 2; ++side) {
+  for (int side = 0; mine && side < 2; ++side) {
     if (side == 0 && a.prefix_entry[s] < 0) continue;
     const int e = side ? a.own_entry[s] : a.prefix_entry[s];
     const int units = entry_units(a, plan, e), b = plan.cum[e] + h * units;
@@ -439,7 +439,7 @@ __device__ __forceinline__ void join_row(const SharedArgs& a, const Plan& plan, 
     else count[1] = last - first + 1, c0[1] = first, row[1] = r, entry[1] = e, begin[1] = b;
   }
   float m = -INFINITY, l = 0.f, o[V] = {};
-  const int pieces = mine ? count[0] + count[1] : 0;
+  const int pieces = count[0] + count[1];
 #pragma unroll 1
   for (int x0 = part; x0 < pieces; x0 += 32 * share) {
     const int x = x0 + lane * share, side = x >= count[0];
