@@ -315,9 +315,8 @@ __device__ __forceinline__ void mask(float* s, int valid) {
       if (i >= valid) s[i] = -INFINITY;
   }
 }
-// Weights 2^(scale s - m) in the place of scores (m = -inf, before a piece's first tile: as if 0); their sum.
-__device__ __forceinline__ float weights(float* s, float scale, float m) {
-  const float ref = m == -INFINITY ? 0.f : m;
+// Weights 2^(scale s - ref) in the place of scores; their sum.
+__device__ __forceinline__ float weights(float* s, float scale, float ref) {
   float2 sum[2] = {};
 #pragma unroll
   for (int i = 0; i < kCols / 2; ++i) {
@@ -348,6 +347,39 @@ __device__ __forceinline__ void store_sector(float* p, const float* x) {
                "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
                : "memory");
 }
+
+// The queries of an item with few rows, a chunk of 8 coordinates a thread at
+// most: fetched a segment ahead, put into shared memory when the segment
+// before is through with its own.
+template <int D, int PARTS>
+struct NextQueries {
+  static constexpr int CH = D / 8, W = PARTS == 1 ? 1 : 2;
+  uint4 x[W];
+  __device__ __forceinline__ static bool fits(const SharedArgs& a, const Segment& g) { return a.rows[g.e] * CH <= 32 * kSoftmaxWarps; }
+  __device__ __forceinline__ void fetch(const SharedArgs& a, const Control* ctl, const Segment& g) {
+    const int r = threadIdx.x / CH, gs = 31 - __clz(a.G);
+    if (r >= a.rows[g.e]) return;
+    const int s = g.e < a.prefixes ? ctl->member[a.member0[g.e] + (r >> gs)] : a.holder[g.e];
+    const int64_t at = ((int64_t)s * a.Hkv * a.G + g.h * a.G + (r & (a.G - 1))) * D + 8 * (threadIdx.x % CH);
+    const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(a.q) + at * (2 * W));
+#pragma unroll
+    for (int w = 0; w < W; ++w) x[w] = __ldg(src + w);
+  }
+  __device__ __forceinline__ void put(const SharedArgs& a, const Segment& g, char* q_smem) const {
+    const int r = threadIdx.x / CH, c = threadIdx.x % CH;
+    if (r >= a.rows[g.e]) return;
+    char* to = q_smem + (c / 8) * Shape<D, PARTS>::kHalf + r * 128 + (((c % 8) ^ (r & 7)) << 4);
+    if (PARTS == 1) {
+      *reinterpret_cast<uint4*>(to) = x[0];
+    } else {
+      float4 u = *reinterpret_cast<const float4*>(&x[0]), v = *reinterpret_cast<const float4*>(&x[W - 1]);
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p)
+        *reinterpret_cast<uint4*>(to + p * Shape<D, PARTS>::kStage) =
+            make_uint4(split2(u.x, u.y), split2(u.z, u.w), split2(v.x, v.y), split2(v.z, v.w));
+    }
+  }
+};
 
 // Rows of the segment's queries into shared memory, swizzled, in PARTS parts; by
 // the softmax warps.  A thread keeps its 16-byte column and goes down the
@@ -707,6 +739,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
     }
     while (more) {
       const Segment cur = g;
+      more = walk.next(a, ctl->plan, g);
+      NextQueries<D, PARTS> ahead;
+      const bool few = more && ahead.fits(a, g);
+      if (few) ahead.fetch(a, ctl, g);
       const int rows = a.rows[cur.e], subs = (rows + kTile - 1) / kTile;
       float m2[2] = {-INFINITY, -INFINITY}, l2[2] = {0.f, 0.f};  // per 128 rows: reference of the weights, their sum here
       float acc[S::kTileO ? OC : 1] = {};                        // kTileO: O so far, in units of the reference
@@ -722,14 +758,20 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             const int valid = cur.valid(t) - quarter * kCols;  // keys of this quarter
             mask(s, valid);
             float m = sub ? m2[1] : m2[0], l = sub ? l2[1] : l2[0], f = 1.f;
-            float sum = weights(s, scale, m);
-            // all have read S when they have passed, and P may take its place
-            fence_before();
-            const bool raise = any_of(bar, sub * kTile + row < rows && (t == cur.tile0 || !(sum < kMostWeight)));
-            fence_after();
+            float sum;
+            bool raise = t == cur.tile0;
+            if (!raise) {
+              sum = weights(s, scale, m);
+              // all have read S when they have passed, and P may take its place
+              fence_before();
+              raise = any_of(bar, sub * kTile + row < rows && !(sum < kMostWeight));
+              fence_after();
+              if (raise) {
+                tmem_ld32(buf + quarter * kCols, s);
+                mask(s, valid);
+              }
+            }
             if (raise) {
-              tmem_ld32(buf + quarter * kCols, s);
-              mask(s, valid);
               float top = s[0];
 #pragma unroll
               for (int i = 1; i < kCols; ++i) top = fmaxf(top, s[i]);
@@ -800,9 +842,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         }
       }
       // every S of this segment has been computed: the next one's queries may overwrite these
-      more = walk.next(a, ctl->plan, g);
       if (more) {
-        load_queries<D, PARTS>(a, ctl, g, q_smem);
+        if (few) ahead.put(a, g, q_smem);
+        else load_queries<D, PARTS>(a, ctl, g, q_smem);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->q_full);
