@@ -455,6 +455,23 @@ def test_shared_many_rows(dtype, batch, hkv, g, d):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("hkv,g,d", [(8, 4, 128), (3, 8, 64), (32, 1, 128), (4, 2, 128)])
+@pytest.mark.parametrize("prefix", [0, 333])
+def test_shared_many_short_sequences(dtype, hkv, g, d, prefix):
+    # more sequences x heads than multiprocessors, with few tokens of their own
+    lens = [prefix] + [[0, 1, 15, 16, 31, 32, 33, 63, 64, 65, 130][s % 11] for s in range(1, 64)]
+    c = shared_cache([max(16, (prefix + 15) // 16 * 16)] + [144] * 63, lens, hkv, g, d)
+    q = (2 * randn(5, 64, hkv * g, d)).to(dtype)
+    prefix_seq = [0] * 60 + [-1, -1, -2, -1]
+    out = torch.full_like(q, 7.0)
+    got = c.attend_shared(0, q, prefix_seq, [prefix] + [0] * 63, out=out)
+    assert c.device_status() == 0
+    take = torch.tensor([p != -2 for p in prefix_seq], device="cuda")
+    check_shared(got, *shared64(c, 0, q, prefix_seq, [prefix] + [0] * 63, lens), take)
+    assert (out[~take] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_shared_groups_and_sequences_without_a_part(dtype):
     # two prefixes, one held by a sequence without a part, one by a member of the other; sequences alone; one with nothing
     prefix_seq = [-2, 0, 0, 4, 0, 4, -1, -1, -2, 0]
