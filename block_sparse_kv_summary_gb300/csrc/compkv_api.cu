@@ -759,29 +759,35 @@ compkv_status compkv_fork(compkv_ctx* c, int layer0, int layers, int n, const in
                     a.cap_blocks[s] * kBlock, s);
   }
   // pairs with one source stand together: its tokens are then read once from DRAM
-  int at = 0;
-  int64_t items = 0;
+  int at = 0, most[kMaxBatch];  // blocks of the longest copy of a group
   for (int s = 0; s < a.B; ++s) {
     const int first = at;
-    int most = 0;
+    most[a.groups] = 1;
     for (int i = 0; i < n; ++i) {
       if (src[i] != s) continue;
       a.src[at] = s;
       a.dst[at] = dst[i];
       a.lens[at] = lens ? lens[i] : -1;
       const int blocks = a.lens[at] < 0 ? a.cap_blocks[s] : (a.lens[at] + kBlock - 1) / kBlock;
-      if (dst[i] != s && blocks > most) most = blocks;
+      if (dst[i] != s && blocks > most[a.groups]) most[a.groups] = blocks;
       ++at;
     }
     if (at == first) continue;
-    a.pair0[a.groups] = first;
-    a.item0[a.groups] = items;
-    ++a.groups;
-    items += (int64_t)layers * a.Hkv * fork_chunks(most);
+    a.pair0[a.groups++] = first;
   }
   a.pair0[a.groups] = n;
-  a.item0[a.groups] = items;
-  if (items > 0x7fffffff) return fail(COMPKV_ERR_UNSUPPORTED_SHAPE, "the copies need more than 2^31 - 1 work items");
+  auto items_of = [&](int chunk) {
+    int64_t items = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      a.item0[g] = (int)items;
+      items += (int64_t)layers * a.Hkv * ((most[g] + chunk - 1) / chunk);
+    }
+    a.item0[a.groups] = (int)items;
+    return items;
+  };
+  a.chunk = fork_chunk(items_of(4), device_sms());
+  if (items_of(a.chunk) > 0x7fffffff)
+    return fail(COMPKV_ERR_UNSUPPORTED_SHAPE, "the copies need more than 2^31 - 1 work items");
   cudaStream_t st = (cudaStream_t)stream;
   return launch(c, COMPKV_KERNEL_FORK, st, "fork launch", [&] { return launch_fork(a, device_sms(), st); });
 }
@@ -805,11 +811,12 @@ compkv_status compkv_compact(compkv_ctx* c, int layer0, int layers, int n, const
   char* sc = reinterpret_cast<char*>(c->buf.scratch);
   a.verdict = reinterpret_cast<int2*>(sc + c->lay.off_comp);
   const int64_t room = (int64_t)((c->lay.off_zs - c->lay.off_comp) / sizeof(int2));
-  if ((int64_t)layers * n > room)
-    return fail(COMPKV_ERR_UNSUPPORTED_SHAPE, "%d layers x %d pairs in one call; at most %lld", layers, n, (long long)room);
+  const int64_t most = room < 65535 ? room : 65535;  // and a grid's second dimension
+  if ((int64_t)layers * n > most)
+    return fail(COMPKV_ERR_UNSUPPORTED_SHAPE, "%d layers x %d pairs in one call; at most %lld", layers, n, (long long)most);
   cudaStream_t st = (cudaStream_t)stream;
-  return launch(c, COMPKV_KERNEL_COMPACT, st, "compact launch", [&] { return launch_compact(a, st); },
-                1 + (in > 0) + (in < n));
+  return launch(c, COMPKV_KERNEL_COMPACT, st, "compact launch", [&] { return launch_compact(a, in, st); },
+                compact_kernels(a, in));
 }
 
 size_t compkv_attend_shared_bytes(const compkv_config* cfg) {

@@ -136,13 +136,14 @@ struct PageArgs {
   int B, Hkv, d, r;
   int kv_host;                 // k and v are host memory
   int groups;                  // copies: pairs with one source stand together and make a group
+  int chunk;                   // copies: blocks of a work item
   int64_t seq_row0[kMaxBatch];
   int cap_blocks[kMaxBatch];
   int src[kMaxBatch];          // per pair
   int dst[kMaxBatch];
   int lens[kMaxBatch];         // tokens to copy; -1: all that the source holds
   int pair0[kMaxBatch + 1];    // copies: first pair of a group
-  int64_t item0[kMaxBatch + 1];  // work items of the groups (copies) or pairs (compaction) before this one
+  int item0[kMaxBatch + 1];    // copies: work items of the groups before this one
 };
 
 // Arguments of the attention over a shared prefix and the sequences' own tokens.

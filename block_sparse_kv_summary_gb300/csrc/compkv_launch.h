@@ -31,11 +31,16 @@ cudaError_t launch_stage_in(void* d0, const void* s0, size_t b0, void* d1, const
 cudaError_t launch_rope_step(const RopeArgs& a, cudaStream_t st);
 cudaError_t launch_rope_prefill(const RopePrefillArgs& a, int sms, cudaStream_t st);
 // Pages: copies between sequences, and listed blocks to the front of a sequence.
-constexpr int kForkBlocks = 16;  // blocks of one work item of a copy
-inline int fork_chunks(int blocks) { return blocks < 1 ? 1 : (blocks + kForkBlocks - 1) / kForkBlocks; }
+// Blocks of one work item of a copy: 16, or 4 where that still leaves a multiprocessor two items at most (three
+// copies of 1025 tokens: 8.3 us with 16, 7.8 with 4).
+inline int fork_chunk(int64_t items_of_4, int sms) { return items_of_4 <= 2 * sms ? 4 : 16; }
 cudaError_t prepare_pages(int d);
 cudaError_t launch_fork(const PageArgs& a, int sms, cudaStream_t st);
-cudaError_t launch_compact(const PageArgs& a, cudaStream_t st);
+// `in` of the pairs are in place.  Short lists of pairs that are not are checked by the CTAs that move their blocks;
+// others by a kernel before.
+inline bool compact_at_once(const PageArgs& a, int in) { return !in && (int64_t)a.Hkv * a.keep_blocks <= 2048; }
+inline int compact_kernels(const PageArgs& a, int in) { return compact_at_once(a, in) ? 1 : 1 + (in > 0) + (in < a.n); }
+cudaError_t launch_compact(const PageArgs& a, int in, cudaStream_t st);
 // Attention over a shared prefix and the sequences' own tokens.
 // Query rows of one entry at most, and the workspace's rows: every entry's rows of every head once, and an
 // entry's more per CTA where a segment ends inside an item.

@@ -41,20 +41,20 @@ __device__ __forceinline__ int pair_len(const PageArgs& a, int layer, int i, int
   return len;
 }
 
-// A work item of a copy: 16 blocks of a (group of pairs with one source, layer, head).
+// A work item of a copy: `chunk` blocks of a (group of pairs with one source, layer, head).
 struct Item {
   int g, layer, h, b0;
 };
-__device__ __forceinline__ Item fork_item(const PageArgs& a, int64_t it) {
+__device__ __forceinline__ Item fork_item(const PageArgs& a, int it) {
   Item x;
   x.g = 0;
   while (x.g + 1 < a.groups && a.item0[x.g + 1] <= it) ++x.g;
-  const int64_t per = (a.item0[x.g + 1] - a.item0[x.g]) / (a.layers * a.Hkv);  // chunks of a (layer, head)
+  const int per = (a.item0[x.g + 1] - a.item0[x.g]) / (a.layers * a.Hkv);  // chunks of a (layer, head)
   it -= a.item0[x.g];
-  x.b0 = (int)(it % per) * kForkBlocks;
+  x.b0 = it % per * a.chunk;
   it /= per;
-  x.h = (int)(it % a.Hkv);
-  x.layer = a.layer0 + (int)(it / a.Hkv);
+  x.h = it % a.Hkv;
+  x.layer = a.layer0 + it / a.Hkv;
   return x;
 }
 __device__ __forceinline__ int held_tokens(const PageArgs& a, int layer, int s) {
@@ -83,10 +83,10 @@ __device__ __forceinline__ void fork_rest(const PageArgs& a, const Item& x, int 
       continue;
     }
     if (first && lane == 0) a.seq_len[(int64_t)x.layer * a.B + to] = len;
-    const int tokens = min(len - x.b0 * kBlock, kForkBlocks * kBlock);
+    const int tokens = min(len - x.b0 * kBlock, a.chunk * kBlock);
     if (tokens <= 0) continue;
     const int64_t rs = first_row(a, x.layer, s, x.h) + x.b0, rd = first_row(a, x.layer, to, x.h) + x.b0;
-    const bool cut = part && len < held && tokens < kForkBlocks * kBlock;
+    const bool cut = part && len < held && tokens < a.chunk * kBlock;
     const int nb = tokens / kBlock + (tokens % kBlock && !cut);
     for (int c = lane; c < nb * a.r; c += 32) a.dbar[rd * a.r + c] = a.dbar[rs * a.r + c];
     if (cut)
@@ -108,7 +108,7 @@ template <int D>
 __global__ void __launch_bounds__(64) fork_bulk_kernel(const __grid_constant__ PageArgs a) {
   extern __shared__ __align__(128) char ring[];
   __shared__ __align__(8) uint64_t full[kForkStages];
-  const int64_t items = a.item0[a.groups];
+  const int items = a.item0[a.groups];
   const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kForkStages; ++i) mbar_init(&full[i], 1);
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(64) fork_bulk_kernel(const __grid_constant__ P
   }
   __syncthreads();
   if (threadIdx.x >= 32) {
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    for (int it = blockIdx.x; it < items; it += gridDim.x) {
       const Item x = fork_item(a, it);
       fork_rest<D>(a, x, held_tokens(a, x.layer, a.src[a.pair0[x.g]]), lane);
     }
@@ -133,12 +133,12 @@ __global__ void __launch_bounds__(64) fork_bulk_kernel(const __grid_constant__ P
                    reinterpret_cast<char*>(a.vbar)};
   // bytes of an item that `len` tokens give in an array; the summary of a block left incomplete is not copied
   auto extent = [&](const Run& r, int len, int kind) {
-    const int tokens = max(0, min(len - r.x.b0 * kBlock, kForkBlocks * kBlock));
+    const int tokens = max(0, min(len - r.x.b0 * kBlock, a.chunk * kBlock));
     if (kind < 2) return tokens * D * 2;
     return (tokens / kBlock + (tokens % kBlock && len == r.held)) * (D * 4);
   };
   Run run[kForkStages];
-  int64_t it = blockIdx.x;
+  int it = blockIdx.x;
   Run cur;
   int most = 0;  // tokens that the longest copy of the current item's group takes
   bool open = false;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(64) fork_bulk_kernel(const __grid_constant__ P
   }
   if (lost)
     for (; done < loads; ++done) mbar_drain_bounded(&full[done % kForkStages]);
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the stages stay until they have been read
 }
 
 // The same with plain loads and stores, for K and V in host memory: one CTA
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
   if (threadIdx.x < 32) fork_rest<D>(a, x, held, threadIdx.x);
   for (int i = a.pair0[x.g]; i < a.pair0[x.g + 1]; ++i) {
     const int len = a.dst[i] == s ? -1 : pair_len(a, x.layer, i, held, false);
-    const int tokens = min(len - x.b0 * kBlock, kForkBlocks * kBlock);
+    const int tokens = min(len - x.b0 * kBlock, a.chunk * kBlock);
     if (tokens <= 0) continue;
     const int64_t rs = first_row(a, x.layer, s, x.h) + x.b0, rd = first_row(a, x.layer, a.dst[i], x.h) + x.b0;
     copy16(a.k + rd * kBlock * D, a.k + rs * kBlock * D, tokens * D / 8);
@@ -224,24 +224,25 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
   }
 }
 
-// One CTA per (layer, pair): are the lists of all heads ascending block
-// indices of the source, equally long, padded by -1, and does the source's
-// last block stand in all of them or in none (it may hold fewer tokens)?
-// Writes the kept blocks and tokens for the kernel that moves, and the length.
-__global__ void __launch_bounds__(kThreads) compact_check_kernel(const __grid_constant__ PageArgs a) {
+// By a CTA, for pair `x` = (layer, i) of the call: are the lists of all heads
+// ascending block indices of the source, equally long, padded by -1, and does
+// the source's last block stand in all of them or in none (it may hold fewer
+// tokens)?  Kept blocks (-1: refused) and tokens.  `tell`: reports a refusal,
+// or sets the destination's length.
+__device__ int2 compact_verdict(const PageArgs& a, int x, bool tell) {
   __shared__ int s_count[32], s_last[32], s_bad;
-  const int i = blockIdx.x % a.n, l = blockIdx.x / a.n, layer = a.layer0 + l;
+  const int i = x % a.n, layer = a.layer0 + x / a.n;
   const int src = a.src[i], to = a.dst[i];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int held = max(0, min(__ldcg(a.seq_len + (int64_t)layer * a.B + src), a.cap_blocks[src] * kBlock));
+  const int held = held_tokens(a, layer, src);
   const int N = ceil_blocks(held);
   if (threadIdx.x == 0) s_bad = 0;
   __syncthreads();
   for (int h = warp; h < a.Hkv; h += kThreads / 32) {
-    const int* list = a.keep + (((int64_t)l * a.n + i) * a.Hkv + h) * a.keep_blocks;
+    const int* list = a.keep + ((int64_t)x * a.Hkv + h) * a.keep_blocks;
     int count = 0, last = 0, bad = 0;
     for (int j = lane; j < a.keep_blocks; j += 32) {
-      const int b = list[j], before = j ? list[j - 1] : -1;
+      const int b = __ldg(list + j), before = j ? __ldg(list + j - 1) : -1;
       if (b >= 0) {
         ++count;
         bad |= b >= N || before >= b || (j && before < 0);
@@ -259,66 +260,66 @@ __global__ void __launch_bounds__(kThreads) compact_check_kernel(const __grid_co
     }
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    const int count = s_count[0];
-    bool bad = s_bad != 0;
-    for (int h = 1; h < a.Hkv; ++h) bad |= s_count[h] != count || s_last[h] != s_last[0];
-    const bool full = count > a.cap_blocks[to];
-    const int tokens = !count ? 0 : s_last[0] ? (count - 1) * kBlock + held - (N - 1) * kBlock : count * kBlock;
+  const int count = s_count[0];
+  bool bad = s_bad != 0;
+  for (int h = 1; h < a.Hkv; ++h) bad |= s_count[h] != count || s_last[h] != s_last[0];
+  const bool full = count > a.cap_blocks[to];
+  const int tokens = !count ? 0 : s_last[0] ? (count - 1) * kBlock + held - (N - 1) * kBlock : count * kBlock;
+  if (tell && threadIdx.x == 0) {
     if (bad || full) set_error(a.status, bad ? kDevBadSelection : kDevCapacity, src, -1, 4);
     else a.seq_len[(int64_t)layer * a.B + to] = tokens;
-    a.verdict[(int64_t)l * a.n + i] = bad || full ? make_int2(-1, 0) : make_int2(count, tokens);
   }
+  return bad || full ? make_int2(-1, 0) : make_int2(count, tokens);
 }
 
-// Out of place: one warp per (layer, pair, head, block).
-template <int D>
+__global__ void __launch_bounds__(kThreads) compact_check_kernel(const __grid_constant__ PageArgs a) {
+  const int2 v = compact_verdict(a, blockIdx.x, true);
+  if (threadIdx.x == 0) a.verdict[blockIdx.x] = v;
+}
+
+// Out of place: one CTA per (layer, pair) and 8 blocks of its heads' lists, a
+// warp a block.  AT_ONCE: it checks the lists itself; the source's length stays.
+template <int D, bool AT_ONCE>
 __global__ void __launch_bounds__(kThreads) compact_copy_kernel(const __grid_constant__ PageArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-  const int64_t items = (int64_t)a.layers * a.n * a.Hkv * a.keep_blocks;
-  for (int64_t it = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += warps) {
-    const int j = (int)(it % a.keep_blocks);
-    int64_t x = it / a.keep_blocks;
-    const int h = (int)(x % a.Hkv);
-    x /= a.Hkv;
-    const int i = (int)(x % a.n), layer = a.layer0 + (int)(x / a.n);
-    if (a.src[i] == a.dst[i]) continue;
-    const int2 v = __ldcg(a.verdict + x);
-    if (j >= v.x) continue;
-    const int64_t rs = first_row(a, layer, a.src[i], h) + __ldg(a.keep + it), rd = first_row(a, layer, a.dst[i], h) + j;
-    const int chunks = min(v.y - j * kBlock, kBlock) * D / 8;
-    const uint4* ks = reinterpret_cast<const uint4*>(a.k + rs * kBlock * D);
-    const uint4* vs = reinterpret_cast<const uint4*>(a.v + rs * kBlock * D);
-    uint4* kd = reinterpret_cast<uint4*>(a.k + rd * kBlock * D);
-    uint4* vd = reinterpret_cast<uint4*>(a.v + rd * kBlock * D);
-    constexpr int U = kBlock * D / 8 / 32;
-    uint4 kt[U], vt[U];
+  const int lane = threadIdx.x & 31, x = blockIdx.y, i = x % a.n, layer = a.layer0 + x / a.n;
+  if (a.src[i] == a.dst[i]) return;
+  const int2 v = AT_ONCE ? compact_verdict(a, x, blockIdx.x == 0) : __ldcg(a.verdict + x);
+  const int it = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);  // (head, place in its list)
+  const int h = it / a.keep_blocks, j = it % a.keep_blocks;
+  if (h >= a.Hkv || j >= v.x) return;
+  const int64_t rs = first_row(a, layer, a.src[i], h) + __ldg(a.keep + ((int64_t)x * a.Hkv + h) * a.keep_blocks + j);
+  const int64_t rd = first_row(a, layer, a.dst[i], h) + j;
+  const int chunks = min(v.y - j * kBlock, kBlock) * D / 8;
+  const uint4* ks = reinterpret_cast<const uint4*>(a.k + rs * kBlock * D);
+  const uint4* vs = reinterpret_cast<const uint4*>(a.v + rs * kBlock * D);
+  uint4* kd = reinterpret_cast<uint4*>(a.k + rd * kBlock * D);
+  uint4* vd = reinterpret_cast<uint4*>(a.v + rd * kBlock * D);
+  constexpr int U = kBlock * D / 8 / 32;
+  uint4 kt[U], vt[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (u * 32 + lane < chunks) {
-        kt[u] = ks[u * 32 + lane];
-        vt[u] = vs[u * 32 + lane];
-      }
-    const int e = lane * (D / 32);
-    float mk[D / 32], mv[D / 32];
-#pragma unroll
-    for (int u = 0; u < D / 32; ++u) {
-      mk[u] = a.kbar[rs * D + e + u];
-      mv[u] = a.vbar[rs * D + e + u];
+  for (int u = 0; u < U; ++u)
+    if (u * 32 + lane < chunks) {
+      kt[u] = ks[u * 32 + lane];
+      vt[u] = vs[u * 32 + lane];
     }
-    for (int c = lane; c < a.r; c += 32) a.dbar[rd * a.r + c] = a.dbar[rs * a.r + c];
+  const int e = lane * (D / 32);
+  float mk[D / 32], mv[D / 32];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (u * 32 + lane < chunks) {
-        kd[u * 32 + lane] = kt[u];
-        vd[u * 32 + lane] = vt[u];
-      }
+  for (int u = 0; u < D / 32; ++u) {
+    mk[u] = a.kbar[rs * D + e + u];
+    mv[u] = a.vbar[rs * D + e + u];
+  }
+  for (int c = lane; c < a.r; c += 32) a.dbar[rd * a.r + c] = a.dbar[rs * a.r + c];
 #pragma unroll
-    for (int u = 0; u < D / 32; ++u) {
-      a.kbar[rd * D + e + u] = mk[u];
-      a.vbar[rd * D + e + u] = mv[u];
+  for (int u = 0; u < U; ++u)
+    if (u * 32 + lane < chunks) {
+      kd[u * 32 + lane] = kt[u];
+      vd[u * 32 + lane] = vt[u];
     }
+#pragma unroll
+  for (int u = 0; u < D / 32; ++u) {
+    a.kbar[rd * D + e + u] = mk[u];
+    a.vbar[rd * D + e + u] = mv[u];
   }
 }
 
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(kThreads) compact_in_place_kernel(const __grid
 }  // namespace
 
 cudaError_t launch_fork(const PageArgs& a, int sms, cudaStream_t st) {
-  const int64_t items = a.item0[a.groups];
+  const int items = a.item0[a.groups];
   if (a.kv_host) {
     if (a.d == 128) fork_kernel<128><<<(unsigned)items, kThreads, 0, st>>>(a);
     else fork_kernel<64><<<(unsigned)items, kThreads, 0, st>>>(a);
@@ -410,23 +411,25 @@ cudaError_t prepare_pages(int d) {
                           kForkStages * kStageBytes);
 }
 
-cudaError_t launch_compact(const PageArgs& a, cudaStream_t st) {
-  compact_check_kernel<<<(unsigned)(a.layers * a.n), kThreads, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  int in = 0;
-  for (int i = 0; i < a.n; ++i) in += a.src[i] == a.dst[i];
-  if (in < a.n) {
-    int64_t ctas = ((int64_t)a.layers * a.n * a.Hkv * a.keep_blocks + kThreads / 32 - 1) / (kThreads / 32);
-    if (ctas > 1 << 20) ctas = 1 << 20;
-    if (a.d == 128) compact_copy_kernel<128><<<(unsigned)ctas, kThreads, 0, st>>>(a);
-    else compact_copy_kernel<64><<<(unsigned)ctas, kThreads, 0, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+cudaError_t launch_compact(const PageArgs& a, int in, cudaStream_t st) {
+  const int pairs = a.layers * a.n;
+  const dim3 grid((unsigned)(((int64_t)a.Hkv * a.keep_blocks + kThreads / 32 - 1) / (kThreads / 32)), pairs);
+  if (compact_at_once(a, in)) {
+    if (a.d == 128) compact_copy_kernel<128, true><<<grid, kThreads, 0, st>>>(a);
+    else compact_copy_kernel<64, true><<<grid, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
   }
-  if (in) {
-    const unsigned grid = (unsigned)(a.layers * a.n * a.Hkv) * (2 * kBlock * a.d * 2 / 512 + 3);
-    if (a.d == 128) compact_in_place_kernel<128><<<grid, kThreads, 0, st>>>(a);
-    else compact_in_place_kernel<64><<<grid, kThreads, 0, st>>>(a);
+  compact_check_kernel<<<pairs, kThreads, 0, st>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess && in < a.n) {
+    if (a.d == 128) compact_copy_kernel<128, false><<<grid, kThreads, 0, st>>>(a);
+    else compact_copy_kernel<64, false><<<grid, kThreads, 0, st>>>(a);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess && in) {
+    const unsigned ctas = (unsigned)(pairs * a.Hkv) * (2 * kBlock * a.d * 2 / 512 + 3);
+    if (a.d == 128) compact_in_place_kernel<128><<<ctas, kThreads, 0, st>>>(a);
+    else compact_in_place_kernel<64><<<ctas, kThreads, 0, st>>>(a);
     e = cudaGetLastError();
   }
   return e;
