@@ -13,8 +13,12 @@ from . import compkv as C
 BLOCK = 16
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
 def _stream(device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return _raw_stream(device.index)
 
 
 _TYPES = {torch.bfloat16: C.COMPKV_BF16, torch.float32: C.COMPKV_F32}
@@ -68,7 +72,11 @@ class CompKVCache:
         self.bufs = C.compkv_buffers(self.k.data_ptr(), self.v.data_ptr(), self.kbar.data_ptr(),
                                      self.vbar.data_ptr(), self.dbar.data_ptr(),
                                      self.seq_len.data_ptr(), self.scratch.data_ptr(), nbytes)
+        self._index = self.device.index
         self._shared_ws = None
+        # shapes of a call's outputs, and of the rows of the projection that it reads
+        self._q_shape, self._kv_shape = (batch, num_kv_heads * group_size, head_dim), (batch, num_kv_heads, head_dim)
+        self._width = (group_size + 2) * num_kv_heads * head_dim
         with torch.cuda.device(dev):
             self.ctx = C.compkv_init(self.cfg, self.bufs)
 
@@ -162,11 +170,12 @@ class CompKVCache:
     # (these calls take microseconds, so their checks are written out for speed)
     def _call(self, fn, *args):
         """A library call with the cache's device as the current one."""
-        if torch._C._cuda_getDevice() == self.device.index:
-            fn(self.ctx, *args, _stream(self.device))
+        index = self._index
+        if _current_device() == index:
+            fn(self.ctx, *args, _raw_stream(index))
         else:
-            with torch.cuda.device(self.device):
-                fn(self.ctx, *args, _stream(self.device))
+            with torch.cuda.device(index):
+                fn(self.ctx, *args, _raw_stream(index))
 
     def _is(self, t, name, dtype, shape):
         """Address of a contiguous tensor of this type and shape."""
@@ -175,21 +184,22 @@ class CompKVCache:
         return t.data_ptr()
 
     def _rope_args(self, qkv, tokens, table, q_weight, k_weight, eps, positions, interleaved, q_dtype):
-        width = (self.G + 2) * self.Hkv * self.d
+        width, dev, d = self._width, self.device, (self.d,)
         if q_dtype not in _TYPES:
             raise ValueError(f"q_dtype must be torch.float32 or torch.bfloat16, got {q_dtype}")
         if table.dim() != 2:
             raise ValueError(f"table must be [positions, rot_dim], got {tuple(table.shape)}")
         stride = qkv.stride()
-        if (qkv.dtype not in _TYPES or qkv.shape != (tokens, width) or qkv.device != self.device
+        if (qkv.dtype not in _TYPES or qkv.shape != (tokens, width) or qkv.device != dev
                 or stride[1] != 1 or (tokens > 1 and stride[0] < width)):
-            raise ValueError(f"qkv: expected rows {(tokens, width)} of {' or '.join(map(str, _TYPES))} on {self.device}, "
+            raise ValueError(f"qkv: expected rows {(tokens, width)} of {' or '.join(map(str, _TYPES))} on {dev}, "
                              f"got {qkv.dtype} {tuple(qkv.shape)} with strides {stride} on {qkv.device}")
-        d = (self.d,)
+        positions_rows, rot = table.shape
+        if table.dtype is not torch.float32 or table.device != dev or not table.is_contiguous():
+            self._t(table, "table", torch.float32, table.shape)
         return C.compkv_rope_args(
-            qkv.data_ptr(), _TYPES[qkv.dtype], stride[0] if tokens > 1 else width,
-            self._is(table, "table", torch.float32, table.shape), table.shape[0], table.shape[1], 1 if interleaved else 0,
-            None if q_weight is None else self._is(q_weight, "q_weight", torch.float32, d),
+            qkv.data_ptr(), _TYPES[qkv.dtype], stride[0] if tokens > 1 else width, table.data_ptr(), positions_rows, rot,
+            1 if interleaved else 0, None if q_weight is None else self._is(q_weight, "q_weight", torch.float32, d),
             None if k_weight is None else self._is(k_weight, "k_weight", torch.float32, d), eps,
             None if positions is None else self._is(positions, "positions", torch.int32, (tokens,)), _TYPES[q_dtype])
 
@@ -201,20 +211,18 @@ class CompKVCache:
         sin of every position; q_weight, k_weight: fp32 [d] or None (no norm); positions: int32 [B] or None (the
         sequences' lengths).  See include/compkv.h."""
         a = self._rope_args(qkv, self.batch, table, q_weight, k_weight, eps, positions, interleaved, q_dtype)
-        dev = self.device
-        qs, ks = (self.batch, self.Hkv * self.G, self.d), (self.batch, self.Hkv, self.d)
         if q is None:
-            q = torch.empty(qs, dtype=q_dtype, device=dev)
+            q = torch.empty(self._q_shape, dtype=q_dtype, device=self.device)
         else:
-            self._is(q, "q", q_dtype, qs)
+            self._is(q, "q", q_dtype, self._q_shape)
         if k_new is None:
-            k_new = torch.empty(ks, dtype=torch.bfloat16, device=dev)
+            k_new = torch.empty(self._kv_shape, dtype=torch.bfloat16, device=self.device)
         else:
-            self._is(k_new, "k_new", torch.bfloat16, ks)
+            self._is(k_new, "k_new", torch.bfloat16, self._kv_shape)
         if v_new is None:
-            v_new = torch.empty(ks, dtype=torch.bfloat16, device=dev)
+            v_new = torch.empty_like(k_new)
         else:
-            self._is(v_new, "v_new", torch.bfloat16, ks)
+            self._is(v_new, "v_new", torch.bfloat16, self._kv_shape)
         self._call(C.compkv_rope, layer, a, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr())
         return q, k_new, v_new
 
@@ -286,12 +294,12 @@ class CompKVCache:
         prefix_seq, prefix_len = C.ints(prefix_seq), C.ints(prefix_len)
         if len(prefix_seq) != self.batch or len(prefix_len) != self.batch:
             raise ValueError(f"prefix_seq and prefix_len need {self.batch} entries")
-        dtype, shape = q.dtype, (self.batch, self.Hkv * self.G, self.d)
+        dtype, shape = q.dtype, self._q_shape
         if dtype not in _TYPES:
             raise ValueError(f"q must be torch.float32 or torch.bfloat16, got {dtype}")
         qp = self._is(q, "q", dtype, shape)
         if out is None:
-            out = torch.empty(shape, dtype=dtype, device=self.device)
+            out = torch.empty_like(q)
         else:
             self._is(out, "out", dtype, shape)
         ws = self.shared_workspace()

@@ -224,8 +224,8 @@ def _at(x):
 
 def compkv_rope(ctx, layer, args, q, k_new, v_new, stream):
     """Norms and rotation of one token per sequence; args: a compkv_rope_args."""
-    st = lib().compkv_rope(ctx, layer, args, q, k_new, v_new, stream)
-    if st != COMPKV_OK:
+    st = (_lib or lib()).compkv_rope(ctx, layer, args, q, k_new, v_new, stream)
+    if st:
         _check(st, "compkv_rope")
 
 

@@ -339,7 +339,10 @@ compkv_status compkv_compact(compkv_ctx *ctx, int layer0, int layers, int n, con
  * [B][Hq][d], both of `type`.  With COMPKV_F32 queries and softmax weights
  * enter the products to 24 bits; with COMPKV_BF16 the weights are rounded to bf16.
  * workspace: device memory of compkv_attend_shared_bytes(), 256-byte aligned,
- * that no other call uses meanwhile.  k and v must be in device memory. */
+ * that no other call uses meanwhile.  k and v must be in device memory.  The
+ * call is one cooperative launch with a CTA on every multiprocessor: it waits
+ * until all of them are free, and a context that may use only some of them
+ * gives COMPKV_ERR_CUDA. */
 size_t compkv_attend_shared_bytes(const compkv_config *cfg);
 compkv_status compkv_attend_shared(compkv_ctx *ctx, int layer, const void *q, int type, const int *prefix_seq,
                                    const int *prefix_len, void *out, void *workspace, size_t workspace_bytes,
