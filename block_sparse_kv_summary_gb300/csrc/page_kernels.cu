@@ -329,9 +329,10 @@ __global__ void __launch_bounds__(kThreads) compact_copy_kernel(const __grid_con
 // In place.  Block j comes from keep[j] >= j, so blocks have to be moved in
 // ascending order, but the columns of a row are independent of one another: a
 // CTA takes a 512-byte column slice of one array of one (layer, pair, head)
-// and walks the list alone (8 sequences x 8 heads x 2 layers, forked whole and
-// then cut from 2048 blocks to 256: 833 us, 0.96 of the copy rate in all), kInBlocks blocks a turn (all loaded before any is
-// stored; later turns read behind what this one wrote).
+// and walks the list alone, kInBlocks blocks a turn (all loaded before any is
+// stored; later turns read behind what this one wrote).  8 sequences of 8 heads
+// and 2 layers, forked whole and then cut from 2048 blocks to 256, take 833 us,
+// 0.96 of the copy rate in all.
 constexpr int kInBlocks = 32;
 template <int D>
 __global__ void __launch_bounds__(kThreads) compact_in_place_kernel(const __grid_constant__ PageArgs a) {
