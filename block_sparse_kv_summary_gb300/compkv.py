@@ -214,8 +214,9 @@ def compkv_decode_static(cfg, bufs, layer, q, k_new, v_new, out, sel, stream):
 
 
 def ints(x):
-    """Host int32 array of a list's integers (None: NULL); what the calls below take for one."""
-    return None if x is None else x if isinstance(x, array) else array("i", x)
+    """Host int32 array of a list's integers (None: NULL); what the calls below take for one.  An int32 array stays
+    as it is; anything else is converted entry by entry (entries that are no int32 raise)."""
+    return x if x is None or (isinstance(x, array) and x.typecode == "i") else array("i", [*x])
 
 
 def _at(x):
