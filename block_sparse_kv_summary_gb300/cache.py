@@ -290,7 +290,9 @@ class CompKVCache:
     def attend_shared(self, layer, q, prefix_seq, prefix_len, out=None):
         """Exact attention over a prefix that sequence prefix_seq[s] holds for sequence s (its first
         prefix_len[prefix_seq[s]] tokens) and over the sequence's own tokens; -1: no prefix, -2: no part.
-        q: [B, Hq, d] fp32 or bf16; out has its type."""
+        q: [B, Hq, d] fp32 or bf16; out has its type.  With fp32, queries and softmax weights keep 24 bits; with bf16,
+        the weights too are rounded to bf16, each by up to 2^-8 of itself, before they multiply the values (their sum
+        is that of the rounded ones)."""
         prefix_seq, prefix_len = C.ints(prefix_seq), C.ints(prefix_len)
         if len(prefix_seq) != self.batch or len(prefix_len) != self.batch:
             raise ValueError(f"prefix_seq and prefix_len need {self.batch} entries")

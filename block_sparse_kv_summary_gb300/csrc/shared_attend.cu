@@ -35,7 +35,12 @@
 // the tile done again, so that no other tile pays for a maximum.
 //
 // bf16 queries take one product each, and their weights are rounded to bf16,
-// as the result is.  fp32 queries and weights are split into three bf16 parts
+// as the result is, which doubles the variance of its error (2.3e-3 of the
+// result in the mean square against 1.7e-3 from its own rounding).  The weights'
+// sum is that of the rounded ones.  Weights in two parts bring 1.7e-3 back and
+// cost 28 % (64 sequences behind 128K: 187 us in place of 138), so whoever needs
+// those bits passes fp32 queries.  O stays in TMEM over the tiles of a piece: its
+// truncation (below) is far under a bf16 step.  fp32 queries and weights are split into three bf16 parts
 // of 8 bits each and multiplied part by part (K and V are bf16 as they are),
 // the smallest first: the accumulator truncates what each addition of 16
 // products loses below its last bit, always towards zero, and only the last
@@ -315,15 +320,26 @@ __device__ __forceinline__ void mask(float* s, int valid) {
       if (i >= valid) s[i] = -INFINITY;
   }
 }
-// Weights 2^(scale s - ref) in the place of scores; their sum.
+// Weights 2^(scale s - ref) in the place of scores; their sum.  With one part they are rounded to bf16 here, two to a
+// word in the first half of s, and the sum is that of the rounded ones: numerator and denominator then hold the same
+// weights, and a value that all keys share comes out as it is.
+template <int PARTS>
 __device__ __forceinline__ float weights(float* s, float scale, float ref) {
   float2 sum[2] = {};
 #pragma unroll
   for (int i = 0; i < kCols / 2; ++i) {
     const float2 x = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), make_float2(scale, scale), make_float2(-ref, -ref));
-    s[2 * i] = exp2_approx(x.x);
-    s[2 * i + 1] = exp2_approx(x.y);
-    sum[i & 1] = __fadd2_rn(sum[i & 1], make_float2(s[2 * i], s[2 * i + 1]));
+    float2 w = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+    if (PARTS == 1) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(w.x, w.y);
+      const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
+      s[i] = __uint_as_float(u);
+      w = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    } else {
+      s[2 * i] = w.x;
+      s[2 * i + 1] = w.y;
+    }
+    sum[i & 1] = __fadd2_rn(sum[i & 1], w);
   }
   return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
@@ -763,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             float sum;
             bool raise = t == cur.tile0;
             if (!raise) {
-              sum = weights(s, scale, m);
+              sum = weights<PARTS>(s, scale, m);
               // all have read S when they have passed, and P may take its place
               fence_before();
               raise = any_of(bar, sub * kTile + row < rows && !(sum < kMostWeight));
@@ -788,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
               f = exp2_approx(m - top);  // 0 in the first tile: m = -inf
               m = top;
               l = t == cur.tile0 ? 0.f : l * f;
-              sum = weights(s, scale, m);
+              sum = weights<PARTS>(s, scale, m);
               if (!S::kTileO && t > cur.tile0) {
                 // O of the tile before is complete (with two steps a tile: S was issued behind its product),
                 // and the next product into it waits for p_full
@@ -817,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             for (int part = 0; part < PARTS; ++part) {
               uint32_t w[kCols / 2];
 #pragma unroll
-              for (int i = 0; i < kCols / 2; ++i) w[i] = split2(s[2 * i], s[2 * i + 1]);
+              for (int i = 0; i < kCols / 2; ++i) w[i] = PARTS == 1 ? __float_as_uint(s[i]) : split2(s[2 * i], s[2 * i + 1]);
               tmem_st16(buf + part * 64 + quarter * (kCols / 2), w);
             }
             if (S::kTileO && t > cur.tile0) {

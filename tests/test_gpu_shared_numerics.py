@@ -12,6 +12,26 @@ pytestmark = pytest.mark.gpu
 
 
 # ------------------------------------------------------------------ bits
+def test_bf16_weights_and_their_sum_are_the_same():
+    # 99 of 100 keys share a weight of which rounding takes or adds up to 2^-8, and all values are alike: the weights' sum
+    # must be that of the rounded ones for the value to come back (sums are off by less than 100 F32, the rounding of
+    # the result is exact)
+    d, n, batch, hkv, g = 64, 100, 64, 2, 4
+    c = make_cache([112] * batch, hkv=hkv, g=g, d=d, fill=0.0)
+    q = torch.zeros(batch, hkv * g, d, device="cuda")
+    q[..., 0] = torch.linspace(0, 40, batch * hkv * g, device="cuda").view(batch, hkv * g)
+    for s in range(batch):
+        for h in range(hkv):
+            kv, vv = c.token_view(0, s, h)
+            kv[n - 1, 0] = 1.0
+            vv[:n] = torch.linspace(-3, 3, d, device="cuda")
+    c.seq_len.fill_(n)
+    want = c.token_view(0, 0, 0)[1][0]
+    out = c.attend_shared(0, q.bfloat16(), [-1] * batch, [0] * batch)
+    assert c.device_status() == 0
+    assert torch.equal(out, want.expand_as(out))
+
+
 def two_keys(z_lo, z_hi, d=64, batch=64, hkv=2, g=4):
     """Two tokens a sequence: key e_0 and key 0, so that the first one's logit is q_0 / sqrt(d) to the last bit."""
     c = make_cache([16] * batch, hkv=hkv, g=g, d=d, fill=0.0)
