@@ -839,6 +839,8 @@ compkv_status compkv_attend_shared(compkv_ctx* c, int layer, const void* q, int 
   SharedArgs a;
   a.seq_len = c->buf.seq_len + (int64_t)layer * c->cfg.batch;
   a.q = q;
+  a.k = reinterpret_cast<const __nv_bfloat16*>(c->buf.k);
+  a.v = reinterpret_cast<const __nv_bfloat16*>(c->buf.v);
   a.out = out;
   a.status = status_word(c);
   a.q_bf16 = type == COMPKV_BF16;

@@ -154,6 +154,8 @@ constexpr int kMaxSharedEntries = kMaxPrefixEntries + kMaxBatch;
 struct SharedArgs {
   const int* seq_len;          // [B] of this layer
   const void* q;               // [B][Hq][d] fp32, or bf16 where q_bf16
+  const __nv_bfloat16* k;      // the whole cache, as token0 counts it
+  const __nv_bfloat16* v;
   void* out;                   // the same type
   float* acc;                  // workspace: [rows][d] unnormalised outputs of a segment's rows
   float2* ml;                  // workspace: [rows] reference of its weights (log2 units) and their sum

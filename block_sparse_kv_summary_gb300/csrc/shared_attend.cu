@@ -76,6 +76,10 @@ __device__ __forceinline__ int item_units(const SharedArgs& a, int e) { return 4
 __device__ __forceinline__ int entry_units(const SharedArgs& a, const Plan& p, int e) {  // per head
   return (p.cum[e + 1] - p.cum[e]) / a.Hkv;
 }
+__device__ __forceinline__ int item_keys(const SharedArgs& a, const Plan& p, int e) {
+  const int u = entry_units(a, p, e);
+  return u ? ((u - item_units(a, e)) / tile_units(a, e) - 1) * kTile + p.last[e] : 0;
+}
 // By one warp; the caller synchronises.
 __device__ void build_plan(const SharedArgs& a, Plan& p, int lane) {
   int base = 0;
@@ -198,7 +202,8 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t lead) {
 // A value that all lanes hold, in a form that the compiler knows to be uniform: operands of tcgen05 stand in
 // uniform registers, and moving each there anew costs as much as the product.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
-// Registers of this warp from here on; every warp of its group of four says the same.
+// Registers of this warp from here on; every warp of its group of four says the same, and they have met between two
+// changes.
 template <int N>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -475,8 +480,9 @@ __device__ __forceinline__ bool all_arrived(const SharedArgs& a, Control* ctl) {
 // the warp adds up their outputs, several loads in flight.  Warp `part` takes
 // every share-th piece; with share > 1 the CTA's warps come here together, and
 // the first of each row adds up what the others leave in `left`.
+// Returns whether a lane of the row has NaN.
 template <int D>
-__device__ __forceinline__ void join_row(const SharedArgs& a, const Plan& plan, int item, int part, int share,
+__device__ __forceinline__ bool join_row(const SharedArgs& a, const Plan& plan, int item, int part, int share,
                                          float* left, int lane) {
   constexpr int V = D / 32;
   const int Hq = a.Hkv * a.G;
@@ -508,7 +514,9 @@ __device__ __forceinline__ void join_row(const SharedArgs& a, const Plan& plan, 
     const int b = side ? begin[1] : begin[0], e = side ? entry[1] : entry[0], units = entry_units(a, plan, e);
     const Tiles t = tiles_between(a, e, max(cta_unit(c, a.P, total) - b, 0), min(cta_unit(c + 1, a.P, total) - b, units));
     const bool some = x < pieces && t.from < t.to;
-    const float2 w = some ? __ldcg(a.ml + at) : make_float2(-INFINITY, 0.f);
+    float2 w = some ? __ldcg(a.ml + at) : make_float2(-INFINITY, 0.f);
+    // the largest weight is 1; without it (a first tile of scores of -infinity has no reference) nothing here counts
+    if (some && !(w.y >= 0.5f)) w.y = NAN;
     const float top = fmaxf(m, warp_max(w.x));
     const float f0 = m == top ? 1.f : exp2_approx(m - top), f = !some ? 0.f : w.x == top ? 1.f : exp2_approx(w.x - top);
     l = l * f0 + warp_sum(w.y * f);
@@ -555,9 +563,13 @@ __device__ __forceinline__ void join_row(const SharedArgs& a, const Plan& plan, 
     }
     __syncthreads();
   }
-  if (!mine || part) return;
+  if (!mine || part) return false;
+  bool odd = false;
 #pragma unroll
-  for (int i = 0; i < V; ++i) o[i] = l > 0.f ? o[i] / l : l == 0.f ? 0.f : l;  // without a token: zero; NaN stays
+  for (int i = 0; i < V; ++i) {
+    o[i] = l > 0.f ? o[i] / l : l == 0.f ? 0.f : l;  // without a token: zero; NaN stays
+    odd |= isnan(o[i]);
+  }
   const int64_t at = (int64_t)item * D + lane * V;
   if (a.q_bf16) {
 #pragma unroll
@@ -567,6 +579,94 @@ __device__ __forceinline__ void join_row(const SharedArgs& a, const Plan& plan, 
 #pragma unroll
     for (int i = 0; i < V; i += 2)
       *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + at + i) = make_float2(o[i], o[i + 1]);
+  }
+  return odd;
+}
+
+// A warp's rows that came out with NaN, once more, straight from the definition:
+// the largest score, then weights and sums in fp32, a key at a time.  Infinities
+// among the tokens bring them here: a value in parts has parts of either sign and
+// of zero, which an infinite factor turns into NaN where the whole value gives an
+// infinity or, as a score of -infinity, no weight at all.  Finite inputs never
+// come here.  Bound by the loads' latency: four rows behind 128K keys take 12 ms
+// a pass, 2048 rows 68 ms for both.
+template <int D>
+__device__ __noinline__ void plain_rows(const SharedArgs& a, const Plan& plan, int row, int step, int lane) {
+  constexpr int V = D / 32, U = 8;  // coordinates of a lane; keys at a time
+  struct alignas(2 * V) Coords {
+    __nv_bfloat16 c[V];
+  };
+  const int Hq = a.Hkv * a.G;
+  const float scale = 1.4426950408889634f / sqrtf((float)D);
+  auto get = [&](const void* x, int64_t i) {
+    return a.q_bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(x)[i]) : reinterpret_cast<const float*>(x)[i];
+  };
+#pragma unroll 1
+  for (; row < a.B * Hq; row += step) {
+    const int s = row / Hq, h = row % Hq / a.G;
+    const int64_t at = (int64_t)row * D + lane * V;
+    if (!a.part[s]) continue;
+    bool odd = false;
+    float q[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      odd |= isnan(get(a.out, at + i));  // as this lane has left it
+      q[i] = get(a.q, at + i);
+    }
+    if (!__any_sync(0xffffffffu, odd)) continue;
+    float m = -INFINITY, l = 0.f, o[V] = {};
+    bool lost = false;  // a score of NaN or infinity: the sum is no number
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass)
+#pragma unroll 1
+      for (int side = 0; side < 2; ++side) {
+        if (!side && a.prefix_entry[s] < 0) continue;
+        const int e = side ? a.own_entry[s] : a.prefix_entry[s], keys = item_keys(a, plan, e);
+        const int64_t first = ((int64_t)a.token0[e] + (int64_t)h * a.cap[e]) * D + lane * V;
+#pragma unroll 1
+        for (int j0 = 0; j0 < keys && !lost; j0 += kTile) {
+          float lt = 0.f, ot[V] = {};  // of a tile, so that long sums keep their bits
+#pragma unroll 1
+          for (int j = j0; j < min(j0 + kTile, keys); j += U) {
+            Coords x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)  // keys behind the last repeat it
+              x[u] = *reinterpret_cast<const Coords*>(a.k + first + (int64_t)min(j + u, keys - 1) * D);
+            float z[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              z[u] = 0.f;
+#pragma unroll
+              for (int i = 0; i < V; ++i) z[u] += q[i] * __bfloat162float(x[u].c[i]);
+              z[u] = warp_sum(z[u]) * scale;
+              m = pass ? m : fmaxf(m, z[u]);
+              lost |= !(z[u] < INFINITY);
+            }
+            if (lost || !pass) continue;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+              x[u] = *reinterpret_cast<const Coords*>(a.v + first + (int64_t)min(j + u, keys - 1) * D);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              if (j + u >= keys) break;
+              float w = exp2f(z[u] - m);
+              if (w == 0.f && z[u] > -INFINITY) w = 1.4e-45f;  // as good as nothing, but an infinite value counts
+              lt += w;
+#pragma unroll
+              for (int i = 0; i < V; ++i) ot[i] += w * __bfloat162float(x[u].c[i]);
+            }
+          }
+          l += lt;
+#pragma unroll
+          for (int i = 0; i < V; ++i) o[i] += ot[i];
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float y = lost ? NAN : o[i] / l;
+      if (a.q_bf16) reinterpret_cast<__nv_bfloat16*>(a.out)[at + i] = __float2bfloat16(y);
+      else reinterpret_cast<float*>(a.out)[at + i] = y;
+    }
   }
 }
 
@@ -908,6 +1008,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
   fence_before();
   __syncthreads();
   fence_after();
+  // what follows is for all warps alike: each has the launch's registers again (the warps of a group must have met
+  // since their last change, and the softmax warps give back what the others wait for)
+  if (warp >= kSoftmaxWarps) more_registers<96>();
+  else fewer_registers<96>();
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kColumns) : "memory");
   if (!all_arrived(a, ctl)) return;
@@ -915,8 +1019,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
   constexpr int kWarps = kThreads / 32;
   const int rows = a.B * a.Hkv * a.G, share = rows <= a.P ? kWarps : rows * 4 <= a.P * kWarps ? 4 : 1;
   static_assert(kWarps % 4 == 0, "warps of a row");
-  for (int r0 = blockIdx.x * (kWarps / share); r0 < rows; r0 += a.P * (kWarps / share))
-    join_row<D>(a, ctl->plan, r0 + warp / share, warp % share, share, reinterpret_cast<float*>(ring), lane);
+  const int step = a.P * (kWarps / share);
+  bool odd = false;
+  for (int r0 = blockIdx.x * (kWarps / share); r0 < rows; r0 += step)
+    odd |= join_row<D>(a, ctl->plan, r0 + warp / share, warp % share, share, reinterpret_cast<float*>(ring), lane);
+  if (__any_sync(0xffffffffu, odd)) plain_rows<D>(a, ctl->plan, blockIdx.x * (kWarps / share) + warp / share, step, lane);
 }
 
 template <int D, int PARTS>

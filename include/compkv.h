@@ -335,10 +335,13 @@ compkv_status compkv_compact(compkv_ctx *ctx, int layer0, int layers, int n, con
  * and its rows of out are left as they were.  prefix_len: host int32 [B], read
  * for the sequences that hold a prefix.  A holder with fewer tokens than
  * prefix_len raises COMPKV_ERR_INVALID_ARG in the device status and gives those
- * that it has.  A row with no token at all is zero.  q and out: device
- * [B][Hq][d], both of `type`.  With COMPKV_F32 queries and softmax weights
- * enter the products to 24 bits; with COMPKV_BF16 the weights are rounded to
- * bf16, in the numerator and in the denominator alike.
+ * that it has.  A row with no token at all is zero.  Infinities and NaN among
+ * the tokens give what the formula gives, slowly; slots behind a sequence's
+ * tokens are never read as such.  q and out: device [B][Hq][d], both of `type`;
+ * where out is q itself, rows that an infinity reaches are NaN.  With
+ * COMPKV_F32 queries and softmax weights enter the products to 24 bits; with
+ * COMPKV_BF16 the weights are rounded to bf16, in the numerator and in the
+ * denominator alike.
  * workspace: device memory of compkv_attend_shared_bytes(), 256-byte aligned,
  * that no other call uses meanwhile.  k and v must be in device memory.  The
  * call is one cooperative launch with a CTA on every multiprocessor: it waits

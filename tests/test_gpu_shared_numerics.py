@@ -1,5 +1,5 @@
-"""Numerics of the attention over a shared prefix: the bits that each type keeps, and logits that rise and
-jump while a piece of a long item is walked."""
+"""Numerics of the attention over a shared prefix: the bits that each type keeps, infinities and NaN among a
+sequence's tokens, and logits that rise and jump while a piece of a long item is walked."""
 import math
 
 import pytest
@@ -83,6 +83,94 @@ def test_fp32_sums_of_a_long_prefix_lose_nothing():
     bound = (10 + tiles + 3 + 17 + tiles + 4 * pieces + 1) * F32
     assert c.device_status() == 0
     assert (out.double() - 1).abs().max().item() <= bound
+
+
+# ------------------------------------------------------------------ infinities and NaN
+def plain64(k, v, q):
+    """Softmax attention of one head by the definition, products one by one: q [g, d], k, v [n, d] -> (out, sum p |v|)."""
+    k, v, q = k.double(), v.double(), q.double()
+    z = (q[:, None] * k[None]).sum(-1) / math.sqrt(q.shape[-1])
+    w = (z - z.amax(-1, keepdim=True)).exp()
+    w = w / w.sum(-1, keepdim=True)
+    return (w[..., None] * v).sum(1), (w[..., None] * v.abs()).sum(1)
+
+
+INF, NAN = math.inf, math.nan
+# (which buffer, token slice, coordinate, value), on the holder's tokens; the prefix has 300 of its 330
+PLANTS = {
+    "a key of infinity": [("k", slice(77, 78), 5, INF)],
+    "keys of both infinities": [("k", slice(3, 4), 5, INF), ("k", slice(290, 291), 9, -INF)],
+    "an infinite key among own tokens": [("k", slice(310, 311), 5, -INF)],
+    "infinite keys in the whole first tile": [("k", slice(0, 128), 5, INF)],
+    "infinite keys everywhere": [("k", slice(0, 330), 5, INF)],
+    "a value of infinity": [("v", slice(10, 11), 7, INF)],
+    "values of both infinities": [("v", slice(10, 11), 7, INF), ("v", slice(200, 201), 7, -INF), ("v", slice(5, 6), 0, -INF)],
+    "a value of NaN": [("v", slice(299, 300), 63, NAN)],
+    "a key of NaN": [("k", slice(128, 129), 1, NAN)],
+}
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("plant", PLANTS)
+def test_infinities_and_nan_among_the_tokens(dtype, d, plant):
+    hkv, g = 2, 4
+    lens, plen = [330, 9, 0, 140], [300, 0, 0, 0]
+    c = shared_cache([336, 16, 16, 144], lens, hkv, g, d)
+    q = 1.5 * randn(5, 4, hkv * g, d)
+    q[:, :, 5] = q[:, :, 5].abs() + 0.25
+    q[:, 0::2, 5] *= -1   # every other query turns the other way
+    q[1, 1, 5] = 0.0      # and one is orthogonal
+    q = q.to(dtype)
+    for name, at, x, value in PLANTS[plant]:
+        for h in range(hkv):
+            c.token_view(0, 0, h)[name == "v"][at, x] = value
+    prefix_seq = [0, 0, 0, -1]
+    out = c.attend_shared(0, q, prefix_seq, plen)
+    assert c.device_status() == 0
+    for s in range(4):
+        for h in range(hkv):
+            (kp, vp), (ko, vo) = c.token_view(0, 0, h), c.token_view(0, s, h)
+            k, v = ko[:lens[s]], vo[:lens[s]]
+            if s == 1 or s == 2:
+                k, v = torch.cat([kp[:300], k]), torch.cat([vp[:300], v])
+            want, mag = plain64(k, v, q[s, h * g:(h + 1) * g])
+            got = out[s, h * g:(h + 1) * g].double()
+            assert torch.equal(got.isnan(), want.isnan()), (s, h)
+            inf = want.isinf()
+            assert torch.equal(got[inf], want[inf]), (s, h)
+            ok = want.isfinite()
+            tol = 3e-5 * (mag + want.abs()) + (BF16 * (mag + want.abs()) if dtype == torch.bfloat16 else 0)
+            assert ((got - want).abs() <= tol)[ok].all(), (s, h)
+    if plant == "a key of infinity":  # half of the rows are finite
+        assert out[1].isfinite().all(-1).sum().item() == 4
+    if "value" in plant:
+        assert out[1].isfinite().sum().item() > 0.9 * out[1].numel()
+    assert out[3].isfinite().all()
+
+
+def test_infinities_behind_a_long_prefix():
+    # pieces of many tiles in many CTAs: a row whose first tiles have no weight at all, one with an infinite value
+    n, hkv, g, d = 20000, 8, 1, 128
+    c = shared_cache([20000, 16], [n, 2], hkv, g, d)
+    q = randn(5, 2, hkv * g, d)
+    q[..., 3], q[..., 4] = -1.0, 0.0
+    for h in range(hkv):
+        kv, vv = c.token_view(0, 0, h)
+        kv[:9000, 3] = INF
+        vv[15000, 2] = -INF
+        vv[7000, 9] = 5.0
+    out = c.attend_shared(0, q, [0, 0], [n, 0])
+    for s in range(2):
+        for h in range(hkv):
+            (kp, vp), (ko, vo) = c.token_view(0, 0, h), c.token_view(0, 1, h)
+            k, v = (kp, vp) if s == 0 else (torch.cat([kp, ko[:2]]), torch.cat([vp, vo[:2]]))
+            want, mag = plain64(k, v, q[s, h:h + 1])
+            got = out[s, h:h + 1].double()
+            assert (got[:, 2] == -INF).all() and (want[:, 2] == -INF).all()
+            got[:, 2] = want[:, 2] = mag[:, 2] = 0
+            assert ((got - want).abs() <= 3e-5 * (mag + want.abs())).all()
+    assert c.device_status() == 0
 
 
 # ------------------------------------------------------------------ a reference that is raised on the way
