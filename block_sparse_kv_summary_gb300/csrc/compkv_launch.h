@@ -37,7 +37,9 @@ inline int fork_chunk(int64_t items_of_4, int sms) { return items_of_4 <= 2 * sm
 cudaError_t prepare_pages(int d);
 cudaError_t launch_fork(const PageArgs& a, int sms, cudaStream_t st);
 // `in` of the pairs are in place.  Short lists of pairs that are not are checked by the CTAs that move their blocks;
-// others by a kernel before.
+// others by a kernel before: one kernel less, but every CTA of a pair, which moves eight blocks, reads all of its lists,
+// 8 KB at the limit.  8 heads x 64, 256, 320 and 512 blocks, at once / after a kernel: one pair 5.3 / 6.4, 7.7 / 10.0,
+// 11.5 / 12.3 and 13.4 / 15.5 us; eight pairs 12.8 / 13.2, 53.9 / 55.1, 75.1 / 66.8 and 106 / 101 us.
 inline bool compact_at_once(const PageArgs& a, int in) { return !in && (int64_t)a.Hkv * a.keep_blocks <= 2048; }
 inline int compact_kernels(const PageArgs& a, int in) { return compact_at_once(a, in) ? 1 : 1 + (in > 0) + (in < a.n); }
 cudaError_t launch_compact(const PageArgs& a, int in, cudaStream_t st);

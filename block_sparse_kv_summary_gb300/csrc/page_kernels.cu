@@ -98,9 +98,11 @@ __device__ __forceinline__ void fork_rest(const PageArgs& a, const Item& x, int 
 // Persistent CTAs.  One thread moves the runs of K, V, kbar and vbar by bulk
 // copies through a ring of stages in shared memory: each run is read once and
 // written to every destination of the group; a warp does the rest of the items.
-// Bound by DRAM: one copy of 64K tokens of 4 layers moves 2.42 GB in 377 us, 0.95
-// of the copy rate; 15 copies of 8K tokens, almost all of it writes, 2.42 GB in
-// 412 us.  Plain loads and stores took 480 us.
+// Bound by DRAM with r 4: one copy of 64K tokens of 4 layers moves 2.42 GB in
+// 381 us, 0.94 of the copy rate; 15 copies of 8K tokens, almost all of it writes,
+// 2.42 GB in 409 to 424 us (plain loads and stores: 480).  With r 64 and 128 the one warp
+// that copies Dbar, a word a lane at a time, sets the pace: 647 and 999 us for the
+// one copy, 455 and 648 for the 15.
 constexpr int kStageBytes = 32 * 1024, kForkStages = 3;
 __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
@@ -331,8 +333,8 @@ __global__ void __launch_bounds__(kThreads) compact_copy_kernel(const __grid_con
 // CTA takes a 512-byte column slice of one array of one (layer, pair, head)
 // and walks the list alone, kInBlocks blocks a turn (all loaded before any is
 // stored; later turns read behind what this one wrote).  8 sequences of 8 heads
-// and 2 layers, forked whole and then cut from 2048 blocks to 256, take 833 us,
-// 0.96 of the copy rate in all.
+// and 2 layers, forked whole and then cut from 2048 blocks to 256, take 837 to 851
+// us in different runs, 0.96 to 0.94 of the copy rate in all.
 constexpr int kInBlocks = 32;
 template <int D>
 __global__ void __launch_bounds__(kThreads) compact_in_place_kernel(const __grid_constant__ PageArgs a) {

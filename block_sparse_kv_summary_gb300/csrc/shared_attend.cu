@@ -23,10 +23,11 @@
 //            with half the keys each took as long for a step and longer for the
 //            queries and outputs of many rows (512 rows behind 64K: 43 us, 35
 //            with sixteen).
-// A tile with one step takes 1.4 us, the time its K and V need from DRAM; with
-// two, 1.7 us: their scores, weights and outputs wait for one another, and two
-// steps are in flight.  In fp32 a step takes 2.3 us, most of it 48 products of
-// 16 on the tensor cores.
+// Measured behind a long prefix, d 128: a tile with one step takes 1.3 us, the
+// time its K and V need from DRAM; with two, 1.8 us: their scores, weights and
+// outputs wait for one another, and two steps are in flight.  In fp32 a step
+// takes 1.9 to 2.1 us, most of it 48 products of 16 on the tensor cores.  d 64:
+// 0.9 to 1.1, 1.7 and 1.4 us.
 //
 // Weights are e^(z - reference).  The reference is the row's maximum in the
 // piece's first tile and stays while the weights of a tile add up to less than
@@ -61,11 +62,14 @@ constexpr float kMostWeight = 1073741824.f;  // 2^30: what a tile's weights of a
 constexpr size_t kSmemLimit = 232448;
 
 // ---------------------------------------------------------------- the plan
-// Work is dealt in units of half a microsecond: a tile costs two of them, or
-// three with more than 128 rows (measured 1.0 and 1.7 us); an item costs some
-// more, for its queries and its outputs (measured 2 us for a few rows and 7 us
-// for 256).  CTA c of P takes the units [c T / P, (c + 1) T / P) of the T
-// units of all entries and heads, in order, and the tiles that begin there.
+// Work is dealt in units: a tile counts two, or three with more than 128 rows,
+// and an item four more, and one for each 32 rows, for its queries and its
+// outputs.  That is the proportion of bf16 and d 128 (1.3 and 1.8 us a tile, 2 to
+// 3 us an item of a few rows, 7 us one of 256).  In fp32 a tile takes 2 us and in
+// d 64 with few rows 0.9, so there an item counts too much or too little beside
+// it, and CTAs with many short items end before or after the others.  CTA c of P
+// takes the units [c T / P, (c + 1) T / P) of the T units of all entries and
+// heads, in order, and the tiles that begin there.
 struct Plan {
   int cum[kMaxSharedEntries + 1];         // units of all heads of the entries before e
   unsigned char last[kMaxSharedEntries];  // keys of its last tile
@@ -448,8 +452,10 @@ __device__ __forceinline__ void load_queries(const SharedArgs& a, const Control*
 
 // Waits until every CTA of the grid has come here (the CTA's warps have: all
 // that it wrote to the workspace is done).  The count runs on from call to
-// call, a multiple of the CTAs between calls.  The largest cache takes 0.2 s in
-// all, and CTAs are done within a fifth of that of one another.
+// call, a multiple of the CTAs between calls.  By the tiles' times above 280 GB of
+// keys and values take some 60 ms, and four times that where 512 rows in fp32 go
+// through them in four passes; a unit of the plan takes at most about twice as
+// long in one CTA as in another, so the first waits for half of that, 0.12 s.
 constexpr unsigned long long kArriveNs = 1000ull * 1000 * 1000;  // 1 s
 __device__ __forceinline__ bool all_arrived(const SharedArgs& a, Control* ctl) {
   if (threadIdx.x == 0) {

@@ -255,7 +255,8 @@ enum { COMPKV_BF16 = 0, COMPKV_F32 = 1 };
  * and sin of pair i at position p are table[p][i] and table[p][rot_dim/2 + i].
  * Values are only copied.  Queries are computed in fp32; keys to some 40 bits,
  * rounded to fp32 and then to bf16, because the summaries are those of the
- * stored keys.  Inputs are finite, with squares that fp32 holds. */
+ * stored keys.  Inputs are finite, and mean(x^2) + eps of a head that is normed
+ * is a normal fp32 number. */
 typedef struct {
   const void *qkv;        /* device [tokens] rows of (Hq + 2 Hkv) d elements: the query heads,   */
                           /* the key heads, the value heads; 16-byte aligned                     */

@@ -85,6 +85,23 @@ def test_fp32_sums_of_a_long_prefix_lose_nothing():
     assert (out.double() - 1).abs().max().item() <= bound
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_same_call_gives_the_same_bits(dtype, d):
+    # sums are dealt and joined by a plan of the lengths alone, whatever runs first and whatever stood in the workspace
+    hkv, g, batch = 4, 4, 40
+    lens = [9000] + [(s * 53) % 700 for s in range(1, batch)]
+    c = shared_cache([9008] + [704] * (batch - 1), lens, hkv, g, d)
+    q = (2 * randn(5, batch, hkv * g, d)).to(dtype)
+    plen = [8999] + [0] * (batch - 1)
+    want = c.attend_shared(0, q, [0] * batch, plen).clone()
+    for i in range(20):
+        c.shared_workspace().fill_(255 * (i & 1))
+        c.attend_shared(0, randn(i, batch, hkv * g, d).to(dtype), [-1] * batch, plen)
+        assert torch.equal(c.attend_shared(0, q, [0] * batch, plen), want)
+    assert c.device_status() == 0
+
+
 # ------------------------------------------------------------------ infinities and NaN
 def plain64(k, v, q):
     """Softmax attention of one head by the definition, products one by one: q [g, d], k, v [n, d] -> (out, sum p |v|)."""
