@@ -593,9 +593,10 @@ __device__ __forceinline__ bool join_row(const SharedArgs& a, const Plan& plan, 
 // the largest score, then weights and sums in fp32, a key at a time.  Infinities
 // among the tokens bring them here: a value in parts has parts of either sign and
 // of zero, which an infinite factor turns into NaN where the whole value gives an
-// infinity or, as a score of -infinity, no weight at all.  Finite inputs never
-// come here.  Bound by the loads' latency: four rows behind 128K keys take 12 ms
-// a pass, 2048 rows 68 ms for both.
+// infinity or, as a score of -infinity, no weight at all.  Finite scores come here
+// only past 2^23, where the rounding of a reference passes a power of two.  Bound
+// by the loads' latency: four rows behind 128K keys take 12 ms a pass, 2048 rows
+// 68 ms for both.
 template <int D>
 __device__ __noinline__ void plain_rows(const SharedArgs& a, const Plan& plan, int row, int step, int lane) {
   constexpr int V = D / 32, U = 8;  // coordinates of a lane; keys at a time
