@@ -1,10 +1,11 @@
 """The calls around the decode step at sizes where their kernels take other paths: several KV heads to a CTA of the
-prefill, copies of long runs and many work items, long lists; and one block's summary from every call that forms it."""
+prefill, copies of long runs and many work items, long lists; one block's summary from every call that forms it; and
+calls at once on other streams and in graphs."""
 import pytest
 import torch
 
 from test_gpu_around_decode import (BLOCK, _built, check_k, check_q, check_summaries, filled, heads_of, make_cache,  # noqa: F401
-                                    randn, rope64, split_heads, state, table)
+                                    randn, rope64, shared_cache, split_heads, state, table)
 
 pytestmark = pytest.mark.gpu
 
@@ -227,3 +228,60 @@ def test_every_call_forms_the_same_summary(d, r):
             for x, y in zip(got[2:], want[2:]):
                 assert torch.equal(x[:3], y[:3])
     assert all(c.device_status() == 0 for c in cs)
+
+
+# ------------------------------------------------------------------ at once
+def test_two_caches_on_two_streams_at_once():
+    # each call of the attention takes every multiprocessor and waits for its own CTAs; two of them, and a third stream
+    # with decode steps and copies, give what they give alone
+    hkv, g, d, batch, n = 4, 4, 128, 8, 5000
+    cs = [shared_cache([5008] + [304] * (batch - 1), [n] + [(s * 37) % 300 for s in range(1, batch)], hkv, g, d, seed=x) for x in (1, 50)]
+    qs = [2 * randn(x, batch, hkv * g, d) for x in (8, 9)]
+    plen = [n - 3] + [0] * (batch - 1)
+    want = [c.attend_shared(0, q, [0] * batch, plen).clone() for c, q in zip(cs, qs)]
+    busy, idle = (filled([4096, 4096], [3000, 0], layers=1, hkv=8, d=128) for _ in range(2))
+    q, k, v = randn(1, 2, 32, 128), randn(2, 2, 8, 128).bfloat16(), randn(3, 2, 8, 128).bfloat16()
+
+    def other(c):
+        c.fork([0], [1])
+        out = c.decode(0, q, k, v)
+        c.truncate([0], [3000])
+        return out
+    alone = [other(idle) for _ in range(3)][-1].clone()
+    torch.cuda.synchronize()
+    st = [torch.cuda.Stream() for _ in range(3)]
+    outs, steps = [[], []], []
+    for i in range(50):
+        for j in range(2):
+            with torch.cuda.stream(st[j]):
+                outs[j].append(cs[j].attend_shared(0, qs[j], [0] * batch, plen))
+        with torch.cuda.stream(st[2]):
+            steps.append(other(busy))
+    torch.cuda.synchronize()
+    for j in range(2):
+        assert all(torch.equal(o, want[j]) for o in outs[j])
+    assert all(torch.equal(o, alone) for o in steps)
+    assert [c.device_status() for c in cs + [busy, idle]] == [0] * 4
+
+
+def test_two_graphs_share_a_workspace_and_a_query_is_overwritten():
+    hkv, g, d, lens = 2, 4, 64, [1500, 40, 0]
+    c = shared_cache([1504, 48, 16], lens, hkv, g, d)
+    plans = [([0, 0, 0], [1400, 0, 0]), ([-1, 0, -2], [700, 0, 0])]
+    qs = [randn(x, 3, hkv * g, d) for x in (1, 2)]
+    want = [c.attend_shared(0, q, *p, out=torch.zeros_like(q)).clone() for q, p in zip(qs, plans)]
+    graphs, outs = [], [torch.zeros_like(q) for q in qs]
+    torch.cuda.synchronize()
+    for q, p, o in zip(qs, plans, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            c.attend_shared(0, q, *p, out=o)
+    for i in range(6):
+        for j in (0, 1) if i % 2 else (1, 0):
+            outs[j].zero_()
+            graphs[j].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+    q = qs[0].clone()  # the result in the place of the queries
+    assert torch.equal(c.attend_shared(0, q, *plans[0], out=q), want[0])
+    assert c.device_status() == 0
