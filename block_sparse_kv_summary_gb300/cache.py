@@ -22,6 +22,7 @@ def _stream(device) -> int:
 
 
 _TYPES = {torch.bfloat16: C.COMPKV_BF16, torch.float32: C.COMPKV_F32}
+_KV8_TYPES = {torch.int8: C.COMPKV_INT8, torch.float8_e4m3fn: C.COMPKV_E4M3}
 
 
 class CompKVCache:
@@ -31,10 +32,15 @@ class CompKVCache:
     kv_memory: "device" (the K and V rows in GPU memory, the default) or "host"
         (in page-locked host memory, which the GPU reads over its chip-to-chip
         link; the summaries, the scratch and everything else stay in GPU memory).
+    kv_dtype: torch.bfloat16 (the default), or torch.int8 or torch.float8_e4m3fn:
+        K and V in 8 bits with one fp32 scale per 16-token block and head
+        (kscale, vscale [rows]), in GPU memory; include/compkv.h says which calls
+        such a cache takes.
     """
 
     def __init__(self, *, num_layers, batch, num_kv_heads, group_size, head_dim, r,
-                 budget_tokens, capacity_tokens, device="cuda", variant=0, kv_memory="device"):
+                 budget_tokens, capacity_tokens, device="cuda", variant=0, kv_memory="device",
+                 kv_dtype=torch.bfloat16):
         self.device = torch.device(device)
         if self.device.type != "cuda":
             raise RuntimeError("CompKVCache lives in GPU memory; the library has no CPU path")
@@ -57,17 +63,31 @@ class CompKVCache:
         if kv_memory not in ("device", "host"):
             raise ValueError(f"kv_memory must be 'device' or 'host', got {kv_memory!r}")
         self.kv_memory = kv_memory
+        if kv_dtype is not torch.bfloat16 and kv_dtype not in _KV8_TYPES:
+            raise ValueError(f"kv_dtype must be torch.bfloat16 or one of {list(_KV8_TYPES)}, got {kv_dtype}")
+        self.kv_dtype = kv_dtype
+        if kv_dtype in _KV8_TYPES and kv_memory == "host":
+            raise ValueError("K and V in 8 bits live in GPU memory")
         if kv_memory == "host":
             self.k = torch.zeros((total, BLOCK, head_dim), dtype=torch.bfloat16, pin_memory=True)
             self.v = torch.zeros((total, BLOCK, head_dim), dtype=torch.bfloat16, pin_memory=True)
         else:
-            self.k = torch.zeros((total, BLOCK, head_dim), dtype=torch.bfloat16, device=dev)
-            self.v = torch.zeros((total, BLOCK, head_dim), dtype=torch.bfloat16, device=dev)
+            self.k = torch.zeros((total, BLOCK, head_dim), dtype=kv_dtype, device=dev)
+            self.v = torch.zeros((total, BLOCK, head_dim), dtype=kv_dtype, device=dev)
         self.kbar = torch.zeros((total, head_dim), dtype=torch.float32, device=dev)
         self.vbar = torch.zeros((total, head_dim), dtype=torch.float32, device=dev)
         self.dbar = torch.zeros((total, r), dtype=torch.float32, device=dev)
         self.seq_len = torch.zeros((num_layers, batch), dtype=torch.int32, device=dev)
-        nbytes = C.compkv_scratch_bytes(self.cfg)
+        kv8 = None
+        if kv_dtype in _KV8_TYPES:
+            units = num_layers * batch * num_kv_heads
+            self.kscale = torch.zeros((total,), dtype=torch.float32, device=dev)
+            self.vscale = torch.zeros((total,), dtype=torch.float32, device=dev)
+            self.tail = torch.zeros((units, 2, 2, BLOCK, head_dim), dtype=torch.bfloat16, device=dev)
+            self.tail_len = torch.zeros((units, 2), dtype=torch.int32, device=dev)
+            kv8 = C.compkv_kv8(_KV8_TYPES[kv_dtype], self.kscale.data_ptr(), self.vscale.data_ptr(), self.tail.data_ptr(),
+                               self.tail_len.data_ptr())
+        nbytes = C.compkv_scratch_bytes(self.cfg) if kv8 is None else C.compkv_scratch_bytes_kv8(self.cfg)
         self.scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         self.bufs = C.compkv_buffers(self.k.data_ptr(), self.v.data_ptr(), self.kbar.data_ptr(),
                                      self.vbar.data_ptr(), self.dbar.data_ptr(),
@@ -78,7 +98,7 @@ class CompKVCache:
         self._q_shape, self._kv_shape = (batch, num_kv_heads * group_size, head_dim), (batch, num_kv_heads, head_dim)
         self._width = (group_size + 2) * num_kv_heads * head_dim
         with torch.cuda.device(dev):
-            self.ctx = C.compkv_init(self.cfg, self.bufs)
+            self.ctx = C.compkv_init(self.cfg, self.bufs) if kv8 is None else C.compkv_init_kv8(self.cfg, self.bufs, kv8)
 
     # ------------------------------------------------------------------ layout
     def rows(self, layer, seq, head):
@@ -86,7 +106,7 @@ class CompKVCache:
         return C.compkv_row_offset(self.ctx, layer, seq, head)
 
     def token_view(self, layer, seq, head):
-        """Views [capacity_tokens, d] of the K and V tokens of one (layer, sequence, head)."""
+        """Views [capacity_tokens, d] of the K and V tokens (in 8 bits: of their codes) of one (layer, sequence, head)."""
         r0, cap = self.rows(layer, seq, head)
         return (self.k[r0:r0 + cap].view(cap * BLOCK, self.d),
                 self.v[r0:r0 + cap].view(cap * BLOCK, self.d))
@@ -307,6 +327,44 @@ class CompKVCache:
         ws = self.shared_workspace()
         self._call(C.compkv_attend_shared, layer, qp, _TYPES[dtype], prefix_seq, prefix_len, out.data_ptr(),
                    ws.data_ptr(), ws.numel())
+        return out
+
+    # ------------------------------------------------------------------ K and V in 8 bits
+    def read(self, layer, starts, counts, dtype=torch.bfloat16, k=None, v=None):
+        """Tokens [starts[s], starts[s] + counts[s]) of every sequence (starts None: from the first), one sequence
+        after another: (k, v) of [tokens, Hkv, d] in bf16 or fp32.  Any cache has it."""
+        counts, starts = C.ints(counts), C.ints(starts)
+        if len(counts) != self.batch or (starts is not None and len(starts) != self.batch):
+            raise ValueError(f"counts and starts need {self.batch} entries")
+        if min(counts) < 0:
+            raise ValueError(f"counts must not be negative, got {counts.tolist()}")
+        if dtype not in _TYPES:
+            raise ValueError(f"dtype must be torch.float32 or torch.bfloat16, got {dtype}")
+        shape = (sum(counts), self.Hkv, self.d)
+        if k is None:
+            k = torch.empty(shape, dtype=dtype, device=self.device)
+        else:
+            self._is(k, "k", dtype, shape)
+        if v is None:
+            v = torch.empty(shape, dtype=dtype, device=self.device)
+        else:
+            self._is(v, "v", dtype, shape)
+        if shape[0]:
+            self._call(C.compkv_read, layer, starts, counts, _TYPES[dtype], k.data_ptr(), v.data_ptr())
+        return k, v
+
+    def attend_all(self, layer, q, out=None):
+        """Exact attention of one query token per sequence over everything that the sequence holds, in a cache of 8
+        bits.  q: [B, Hq, d] fp32 or bf16; out has its type."""
+        dtype, shape = q.dtype, self._q_shape
+        if dtype not in _TYPES:
+            raise ValueError(f"q must be torch.float32 or torch.bfloat16, got {dtype}")
+        qp = self._is(q, "q", dtype, shape)
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            self._is(out, "out", dtype, shape)
+        self._call(C.compkv_attend_all, layer, qp, _TYPES[dtype], out.data_ptr())
         return out
 
     def device_status(self) -> int:

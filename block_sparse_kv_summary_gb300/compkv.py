@@ -44,6 +44,12 @@ class compkv_buffers(ctypes.Structure):
 # element types (include/compkv.h)
 COMPKV_BF16 = 0
 COMPKV_F32 = 1
+COMPKV_INT8 = 2
+COMPKV_E4M3 = 3
+
+
+class compkv_kv8(ctypes.Structure):
+    _fields_ = [("type", c_int), ("kscale", c_void_p), ("vscale", c_void_p), ("tail", c_void_p), ("tail_len", c_void_p)]
 
 
 class compkv_rope_args(ctypes.Structure):
@@ -81,6 +87,10 @@ _SIGNATURES = [
     ("compkv_attend_shared_bytes", c_size_t, [POINTER(compkv_config)]),
     ("compkv_attend_shared", c_int, [c_void_p, c_int, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
                                      c_void_p]),
+    ("compkv_scratch_bytes_kv8", c_size_t, [POINTER(compkv_config)]),
+    ("compkv_init_kv8", c_int, [POINTER(compkv_config), POINTER(compkv_buffers), POINTER(compkv_kv8), POINTER(c_void_p)]),
+    ("compkv_read", c_int, [c_void_p, c_int, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p]),
+    ("compkv_attend_all", c_int, [c_void_p, c_int, c_void_p, c_int, c_void_p, c_void_p]),
     ("compkv_device_status", c_int, [c_void_p, c_void_p]),
     ("compkv_launch_count", c_int64, [c_void_p]),
     ("compkv_selftest_wait_timeout", c_int, [c_void_p, c_void_p]),
@@ -259,6 +269,32 @@ def compkv_attend_shared(ctx, layer, q, type, prefix_seq, prefix_len, out, works
                                       workspace_bytes, stream), "compkv_attend_shared")
 
 
+def compkv_scratch_bytes_kv8(cfg: compkv_config) -> int:
+    return lib().compkv_scratch_bytes_kv8(ctypes.byref(cfg))
+
+
+def compkv_init_kv8(cfg: compkv_config, bufs: compkv_buffers, kv8: compkv_kv8) -> int:
+    """compkv_init for K and V in 8 bits (bufs.k, bufs.v: the codes)."""
+    ctx = c_void_p()
+    _check(lib().compkv_init_kv8(ctypes.byref(cfg), ctypes.byref(bufs), ctypes.byref(kv8), ctypes.byref(ctx)), "compkv_init_kv8")
+    return ctx.value
+
+
+def compkv_read(ctx, layer, starts, counts, type, k, v, stream):
+    """Tokens [starts[s], starts[s] + counts[s]) of every sequence, packed, in bf16 or fp32."""
+    starts, counts = ints(starts), ints(counts)
+    st = (_lib or lib()).compkv_read(ctx, layer, _at(starts), _at(counts), type, k, v, stream)
+    if st:
+        _check(st, "compkv_read")
+
+
+def compkv_attend_all(ctx, layer, q, type, out, stream):
+    """Exact attention over everything that the sequences of a cache in 8 bits hold."""
+    st = (_lib or lib()).compkv_attend_all(ctx, layer, q, type, out, stream)
+    if st:
+        _check(st, "compkv_attend_all")
+
+
 def compkv_device_status(ctx, stream) -> int:
     """Synchronise, read and clear the device status word; returns the status code."""
     return lib().compkv_device_status(ctx, stream)
@@ -275,7 +311,7 @@ def compkv_launch_count(ctx) -> int:
 
 KERNEL_FAMILIES = {"prefill": 0, "append": 1, "score": 2, "attend": 4, "decode": 5,
                    "k_stream": 6, "k_post": 7, "rope": 8, "prefill_qkv": 9, "fork": 10, "compact": 11,
-                   "attend_shared": 12}
+                   "attend_shared": 12, "read": 13, "attend_all": 14}
 
 
 def compkv_profile_enable(ctx, enable):

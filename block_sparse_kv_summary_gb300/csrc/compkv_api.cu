@@ -40,6 +40,7 @@ struct Layout {
   size_t off_status = 0, off_arrive = 0, off_rec = 0, off_comp = 0, off_zs = 0, off_ss = 0, off_anm = 0, off_sel = 0,
          off_hq = 0,
          off_hk = 0, off_hv = 0, off_hout = 0, total = 0;
+  size_t off_arrive8 = 0, off_parts8 = 0, total8 = 0;  // behind them, of a cache in 8 bits only
 };
 
 bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
@@ -118,6 +119,9 @@ compkv_status make_layout(const compkv_config* c, Layout* L) {
   region(&L->off_hv, (size_t)L->units * d * 2);
   region(&L->off_hout, (size_t)L->units * G * d * sizeof(float));
   L->total = off;
+  region(&L->off_arrive8, (size_t)L->units * sizeof(int));
+  region(&L->off_parts8, attend8_parts(G, d));
+  L->total8 = off;
   return COMPKV_OK;
 }
 
@@ -138,6 +142,8 @@ struct compkv_ctx {
   CUtensorMap tmap_k, tmap_v;  // the whole K and V caches, for the post kernel's block copies
   CUtensorMap tmap_k128, tmap_v128;  // the same in boxes of 128 tokens, for the attention over a shared prefix
   int tmap_ok = 0;             // the maps were built
+  compkv_kv8 kv8;              // K and V in 8 bits (type COMPKV_BF16: they are not)
+  CUtensorMap tmap8[4];        // the codes in boxes of 16 tokens (K, V) and of 32
   int kv_host = 0;             // K and V in page-locked host memory (no tensor maps)
   int64_t launches = 0;
   unsigned long long* trace = nullptr;
@@ -220,7 +226,10 @@ compkv_status make_tensor_maps(compkv_ctx* c) {
   memset(&c->tmap_k128, 0, sizeof(c->tmap_k128));
   memset(&c->tmap_v128, 0, sizeof(c->tmap_v128));
   c->tmap_ok = 0;
-  if (c->kv_host) return COMPKV_OK;
+  if (c->kv_host) {
+    if (c->kv8.type != COMPKV_BF16) return fail(COMPKV_ERR_INVALID_ARG, "k and v in 8 bits must be device memory");
+    return COMPKV_OK;
+  }
   static std::atomic<void*> encode_fn{nullptr};
   void* fn = encode_fn.load();
   if (!fn) {
@@ -239,6 +248,19 @@ compkv_status make_tensor_maps(compkv_ctx* c) {
     return fail(COMPKV_ERR_UNSUPPORTED_SHAPE, "the cache holds %llu token slots; at most 2^31 are addressable",
                 (unsigned long long)tokens);
   const cuuint64_t dims[2] = {(cuuint64_t)d, tokens};
+  if (c->kv8.type != COMPKV_BF16) {
+    const cuuint64_t stride = (cuuint64_t)d;
+    const cuuint32_t ones[2] = {1, 1};
+    for (int i = 0; i < 4; ++i) {
+      const cuuint32_t box[2] = {(cuuint32_t)d, i < 2 ? 16u : 32u};
+      const CUresult r = reinterpret_cast<Encode>(fn)(&c->tmap8[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, i & 1 ? c->buf.v : c->buf.k,
+                                                      dims, &stride, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                                      d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                                                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+      if (r != CUDA_SUCCESS) return fail(COMPKV_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    }
+    return COMPKV_OK;
+  }
   const cuuint64_t strides[1] = {(cuuint64_t)d * 2};
   const cuuint32_t boxes[2][2] = {{64, kBlock}, {64, 128}};
   const cuuint32_t estr[2] = {1, 1};
@@ -267,8 +289,10 @@ LayerArgs base_args(const compkv_ctx* c, int layer) {
   a.tmap_ok = c->tmap_ok;
   const int d = c->cfg.head_dim, r = c->cfg.r, G = c->cfg.group_size;
   const int64_t rows = c->lay.rows_per_layer * (int64_t)layer;
-  a.k = reinterpret_cast<__nv_bfloat16*>(c->buf.k) + rows * kBlock * d;
-  a.v = reinterpret_cast<__nv_bfloat16*>(c->buf.v) + rows * kBlock * d;
+  if (c->kv8.type == COMPKV_BF16) {
+    a.k = reinterpret_cast<__nv_bfloat16*>(c->buf.k) + rows * kBlock * d;
+    a.v = reinterpret_cast<__nv_bfloat16*>(c->buf.v) + rows * kBlock * d;
+  }
   a.kbar = c->buf.kbar + rows * d;
   a.vbar = c->buf.vbar + rows * d;
   a.dbar = c->buf.dbar + rows * r;
@@ -300,6 +324,28 @@ LayerArgs base_args(const compkv_ctx* c, int layer) {
     a.cap_blocks[s] = c->lay.cap_blocks[s];
   }
   return a;
+}
+
+// One layer of a cache in 8 bits (type kKvBf16 where it is none).
+Kv8Args kv8_args(const compkv_ctx* c, int layer) {
+  Kv8Args a;
+  memset(&a, 0, sizeof(a));
+  a.type = c->kv8.type;
+  if (a.type == kKvBf16) return a;
+  const int64_t rows = c->lay.rows_per_layer * (int64_t)layer, units = (int64_t)c->lay.units * layer, block = (int64_t)kBlock * c->cfg.head_dim;
+  a.k = reinterpret_cast<uint8_t*>(c->buf.k) + rows * block;
+  a.v = reinterpret_cast<uint8_t*>(c->buf.v) + rows * block;
+  a.kscale = c->kv8.kscale + rows;
+  a.vscale = c->kv8.vscale + rows;
+  a.tail = reinterpret_cast<__nv_bfloat16*>(c->kv8.tail) + units * 4 * block;
+  a.tail_len = c->kv8.tail_len + units * 2;
+  return a;
+}
+
+// Calls that read or write K and V in bf16 only.
+compkv_status needs_bf16(const compkv_ctx* c, const char* call) {
+  if (c && c->kv8.type != COMPKV_BF16) return fail(COMPKV_ERR_UNSUPPORTED_SHAPE, "%s does not take a cache in 8 bits", call);
+  return COMPKV_OK;
 }
 
 compkv_status check_call(const compkv_ctx* c, int layer) {
@@ -394,6 +440,81 @@ compkv_status launch_chain(compkv_ctx* c, int family, const LayerArgs& a, int mo
   return r;
 }
 
+// Attention over a cache in 8 bits; `la` (or null: over every token) are the arguments of the stream in front of it.
+Attend8Args attend8_args(const compkv_ctx* c, int layer, const void* q, bool q_bf16, void* out, const LayerArgs* la, bool selects) {
+  Attend8Args a;
+  memset(&a, 0, sizeof(a));
+  char* sc = reinterpret_cast<char*>(c->buf.scratch);
+  a.kv8 = kv8_args(c, layer);
+  a.seq_len = c->buf.seq_len + (int64_t)layer * c->cfg.batch;
+  a.q = q;
+  a.out = out;
+  a.acc = reinterpret_cast<float*>(sc + c->lay.off_parts8);
+  a.ml = reinterpret_cast<float2*>(a.acc + (size_t)2 * kMaxAttend8Ctas * c->cfg.group_size * c->cfg.head_dim);
+  a.arrive = reinterpret_cast<int*>(sc + c->lay.off_arrive8);
+  a.status = reinterpret_cast<int*>(sc + c->lay.off_status);
+  a.q_bf16 = q_bf16;
+  a.B = c->cfg.batch;
+  a.Hkv = c->cfg.num_kv_heads;
+  a.G = c->cfg.group_size;
+  a.d = c->cfg.head_dim;
+  a.P = device_sms() < kMaxAttend8Ctas ? device_sms() : kMaxAttend8Ctas;
+  a.layer_row0 = c->lay.rows_per_layer * (int64_t)layer;
+  for (int s = 0; s < a.B; ++s) {
+    a.seq_row0[s] = c->lay.seq_row0[s];
+    a.cap_blocks[s] = c->lay.cap_blocks[s];
+  }
+  if (la) {
+    a.sel = la->sel;
+    a.K = la->K;
+    a.selects = selects;
+    a.no_comp = (la->variant & kVarNoCompensation) != 0;
+    a.stream_P = la->P;
+    a.r = la->r;
+    a.rec = la->rec;
+    a.comp = la->comp;
+    a.zs = la->zs;
+    a.vbar = la->vbar;
+  }
+  static_assert(sizeof(a.k16) == sizeof(CUtensorMap), "tensor map size");
+  memcpy(a.k16, &c->tmap8[0], sizeof(CUtensorMap));
+  memcpy(a.v16, &c->tmap8[1], sizeof(CUtensorMap));
+  memcpy(a.k32, &c->tmap8[2], sizeof(CUtensorMap));
+  memcpy(a.v32, &c->tmap8[3], sizeof(CUtensorMap));
+  return a;
+}
+
+// The attention of a cache in 8 bits over a given selection: the stream for the compensation sums, then the attention.
+compkv_status attend_chain8(compkv_ctx* c, int layer, const LayerArgs& a, cudaStream_t st) {
+  const Attend8Args at = attend8_args(c, layer, a.q, false, a.out, &a, false);
+  return launch(
+      c, COMPKV_KERNEL_ATTEND, st, "attend launch",
+      [&] {
+        const cudaError_t e = launch_stream(a, kFusedAttend, st, true);
+        return e == cudaSuccess ? launch_attend8(at, st) : e;
+      },
+      2);
+}
+
+// A decode step of a cache in 8 bits: append, stream, selection, attention.
+compkv_status decode_chain8(compkv_ctx* c, int layer, const LayerArgs& a, cudaStream_t st) {
+  const Attend8Args at = attend8_args(c, layer, a.q, false, a.out, &a, true);
+  return launch(
+      c, COMPKV_KERNEL_DECODE, st, "decode launch",
+      [&] {
+        cudaError_t e = launch_append8(a, kv8_args(c, layer), st);
+        if (e == cudaSuccess) e = launch_stream(a, kStreamDecode8, st, true);
+        if (e == cudaSuccess) e = launch_post(a, kFusedScoreSelect, st);
+        return e == cudaSuccess ? launch_attend8(at, st) : e;
+      },
+      4);
+}
+
+compkv_status decode_chain(compkv_ctx* c, int layer, const LayerArgs& a, cudaStream_t st) {
+  if (c->kv8.type != COMPKV_BF16) return decode_chain8(c, layer, a, st);
+  return launch_chain(c, COMPKV_KERNEL_DECODE, a, kFusedDecode, st, "decode launch");
+}
+
 int* status_word(const compkv_ctx* c) {
   return reinterpret_cast<int*>(reinterpret_cast<char*>(c->buf.scratch) + c->lay.off_status);
 }
@@ -435,8 +556,11 @@ compkv_status rope_base(const compkv_ctx* c, int layer, const compkv_rope_args* 
   a.status = status_word(c);
   a.q = const_cast<void*>(q);
   a.k_new = a.v_new = nullptr;
-  a.k = reinterpret_cast<__nv_bfloat16*>(c->buf.k) + rows * kBlock * d;
-  a.v = reinterpret_cast<__nv_bfloat16*>(c->buf.v) + rows * kBlock * d;
+  a.k = a.v = nullptr;
+  if (c->kv8.type == COMPKV_BF16) {
+    a.k = reinterpret_cast<__nv_bfloat16*>(c->buf.k) + rows * kBlock * d;
+    a.v = reinterpret_cast<__nv_bfloat16*>(c->buf.v) + rows * kBlock * d;
+  }
   a.kbar = c->buf.kbar + rows * d;
   a.vbar = c->buf.vbar + rows * d;
   a.dbar = c->buf.dbar + rows * c->cfg.r;
@@ -501,6 +625,66 @@ compkv_status page_base(const compkv_ctx* c, int layer0, int layers, int n, cons
   return COMPKV_OK;
 }
 
+compkv_status init_context(const compkv_config* cfg, const compkv_buffers* bufs, const compkv_kv8* kv8, compkv_ctx** out) {
+  g_last_error[0] = 0;
+  if (!out) return fail(COMPKV_ERR_INVALID_ARG, "out is NULL");
+  *out = nullptr;
+  Layout L;
+  COMPKV_TRY(make_layout(cfg, &L));
+  if (!bufs) return fail(COMPKV_ERR_INVALID_ARG, "buffers are NULL");
+  COMPKV_TRY(check_ptr(bufs->k, "k", 16));
+  COMPKV_TRY(check_ptr(bufs->v, "v", 16));
+  COMPKV_TRY(check_ptr(bufs->kbar, "kbar", 16));
+  COMPKV_TRY(check_ptr(bufs->vbar, "vbar", 16));
+  COMPKV_TRY(check_ptr(bufs->dbar, "dbar", 16));
+  COMPKV_TRY(check_ptr(bufs->seq_len, "seq_len", 4));
+  COMPKV_TRY(check_ptr(bufs->scratch, "scratch", 256));
+  if (kv8) {
+    if (kv8->type != COMPKV_INT8 && kv8->type != COMPKV_E4M3)
+      return fail(COMPKV_ERR_INVALID_ARG, "kv8 type must be COMPKV_INT8 or COMPKV_E4M3 (got %d)", kv8->type);
+    COMPKV_TRY(check_ptr(kv8->kscale, "kscale", 16));
+    COMPKV_TRY(check_ptr(kv8->vscale, "vscale", 16));
+    COMPKV_TRY(check_ptr(kv8->tail, "tail", 16));
+    COMPKV_TRY(check_ptr(kv8->tail_len, "tail_len", 4));
+  }
+  const size_t scratch = kv8 ? L.total8 : L.total;
+  if (bufs->scratch_bytes < scratch)
+    return fail(COMPKV_ERR_INVALID_ARG, "scratch_bytes %zu < required %zu", bufs->scratch_bytes, scratch);
+  compkv_ctx* c = new (std::nothrow) compkv_ctx();
+  if (!c) return fail(COMPKV_ERR_INVALID_ARG, "out of host memory");
+  c->cfg = *cfg;
+  c->cfg.capacity_tokens = nullptr;  // copied into the layout
+  c->buf = *bufs;
+  memset(&c->kv8, 0, sizeof(c->kv8));
+  if (kv8) c->kv8 = *kv8;
+  c->lay = L;
+  {
+    const compkv_status st = make_tensor_maps(c);
+    if (st != COMPKV_OK) {
+      delete c;
+      return st;
+    }
+  }
+  // the kernels' shared memory limits and cluster size, once for this configuration
+  cudaError_t e = prepare_stream(cfg->head_dim, cfg->r, cfg->group_size);
+  if (e == cudaSuccess) e = prepare_post(cfg->head_dim, cfg->group_size, L.C, L.bpc_max, L.K);
+  if (e == cudaSuccess) e = prepare_pages(cfg->head_dim);
+  if (e == cudaSuccess) e = kv8 ? prepare_attend8(cfg->head_dim) : prepare_shared(cfg->head_dim);
+  if (e != cudaSuccess) {
+    delete c;
+    return cuda_status(e, "setting the kernels' attributes");
+  }
+  e = cudaMemsetAsync(bufs->scratch, 0, scratch, 0);
+  if (kv8 && e == cudaSuccess) e = cudaMemsetAsync(kv8->tail_len, 0, (size_t)cfg->num_layers * L.units * 2 * sizeof(int), 0);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(0);
+  if (e != cudaSuccess) {
+    delete c;
+    return cuda_status(e, "initialising scratch");
+  }
+  *out = c;
+  return COMPKV_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -517,52 +701,20 @@ size_t compkv_scratch_bytes(const compkv_config* cfg) {
   return L.total;
 }
 
-compkv_status compkv_init(const compkv_config* cfg, const compkv_buffers* bufs, compkv_ctx** out) {
-  g_last_error[0] = 0;
-  if (!out) return fail(COMPKV_ERR_INVALID_ARG, "out is NULL");
-  *out = nullptr;
+size_t compkv_scratch_bytes_kv8(const compkv_config* cfg) {
   Layout L;
-  COMPKV_TRY(make_layout(cfg, &L));
-  if (!bufs) return fail(COMPKV_ERR_INVALID_ARG, "buffers are NULL");
-  COMPKV_TRY(check_ptr(bufs->k, "k", 16));
-  COMPKV_TRY(check_ptr(bufs->v, "v", 16));
-  COMPKV_TRY(check_ptr(bufs->kbar, "kbar", 16));
-  COMPKV_TRY(check_ptr(bufs->vbar, "vbar", 16));
-  COMPKV_TRY(check_ptr(bufs->dbar, "dbar", 16));
-  COMPKV_TRY(check_ptr(bufs->seq_len, "seq_len", 4));
-  COMPKV_TRY(check_ptr(bufs->scratch, "scratch", 256));
-  if (bufs->scratch_bytes < L.total)
-    return fail(COMPKV_ERR_INVALID_ARG, "scratch_bytes %zu < required %zu", bufs->scratch_bytes, L.total);
-  compkv_ctx* c = new (std::nothrow) compkv_ctx();
-  if (!c) return fail(COMPKV_ERR_INVALID_ARG, "out of host memory");
-  c->cfg = *cfg;
-  c->cfg.capacity_tokens = nullptr;  // copied into the layout
-  c->buf = *bufs;
-  c->lay = L;
-  {
-    const compkv_status st = make_tensor_maps(c);
-    if (st != COMPKV_OK) {
-      delete c;
-      return st;
-    }
-  }
-  // the kernels' shared memory limits and cluster size, once for this configuration
-  cudaError_t e = prepare_stream(cfg->head_dim, cfg->r, cfg->group_size);
-  if (e == cudaSuccess) e = prepare_post(cfg->head_dim, cfg->group_size, L.C, L.bpc_max, L.K);
-  if (e == cudaSuccess) e = prepare_pages(cfg->head_dim);
-  if (e == cudaSuccess) e = prepare_shared(cfg->head_dim);
-  if (e != cudaSuccess) {
-    delete c;
-    return cuda_status(e, "setting the kernels' attributes");
-  }
-  e = cudaMemsetAsync(bufs->scratch, 0, L.total, 0);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(0);
-  if (e != cudaSuccess) {
-    delete c;
-    return cuda_status(e, "initialising scratch");
-  }
-  *out = c;
-  return COMPKV_OK;
+  if (make_layout(cfg, &L) != COMPKV_OK) return 0;
+  return L.total8;
+}
+
+compkv_status compkv_init(const compkv_config* cfg, const compkv_buffers* bufs, compkv_ctx** out) {
+  return init_context(cfg, bufs, nullptr, out);
+}
+
+compkv_status compkv_init_kv8(const compkv_config* cfg, const compkv_buffers* bufs, const compkv_kv8* kv8, compkv_ctx** out) {
+  g_last_error[0] = 0;
+  if (!kv8) return fail(COMPKV_ERR_INVALID_ARG, "kv8 is NULL");
+  return init_context(cfg, bufs, kv8, out);
 }
 
 compkv_status compkv_row_offset(const compkv_ctx* c, int layer, int seq, int head, int64_t* first_row,
@@ -578,6 +730,7 @@ compkv_status compkv_row_offset(const compkv_ctx* c, int layer, int seq, int hea
 
 compkv_status compkv_prefill(compkv_ctx* c, int layer, const int* lens, void* stream) {
   COMPKV_TRY(check_call(c, layer));
+  COMPKV_TRY(needs_bf16(c, "compkv_prefill"));
   if (!lens) return fail(COMPKV_ERR_INVALID_ARG, "lens is NULL");
   LayerArgs a = base_args(c, layer);
   for (int s = 0; s < c->cfg.batch; ++s) {
@@ -599,7 +752,9 @@ compkv_status compkv_append(compkv_ctx* c, int layer, const void* k_new, const v
   a.k_new = reinterpret_cast<const __nv_bfloat16*>(k_new);
   a.v_new = reinterpret_cast<const __nv_bfloat16*>(v_new);
   cudaStream_t st = (cudaStream_t)stream;
-  COMPKV_TRY(launch(c, COMPKV_KERNEL_APPEND, st, "append launch", [&] { return launch_append(a, st); }));
+  COMPKV_TRY(launch(c, COMPKV_KERNEL_APPEND, st, "append launch", [&] {
+    return c->kv8.type == COMPKV_BF16 ? launch_append(a, st) : launch_append8(a, kv8_args(c, layer), st);
+  }));
   return COMPKV_OK;
 }
 
@@ -628,6 +783,7 @@ compkv_status compkv_attend(compkv_ctx* c, int layer, const float* q, const int*
   a.sel = const_cast<int*>(sel);
   a.out = out;
   cudaStream_t st = (cudaStream_t)stream;
+  if (c->kv8.type != COMPKV_BF16) return attend_chain8(c, layer, a, st);
   COMPKV_TRY(launch_chain(c, COMPKV_KERNEL_ATTEND, a, kFusedAttend, st, "attend launch"));
   return COMPKV_OK;
 }
@@ -647,7 +803,7 @@ compkv_status compkv_decode(compkv_ctx* c, int layer, const float* q, const void
   a.out = out;
   if (sel) a.sel = sel;
   cudaStream_t st = (cudaStream_t)stream;
-  COMPKV_TRY(launch_chain(c, COMPKV_KERNEL_DECODE, a, kFusedDecode, st, "decode launch"));
+  COMPKV_TRY(decode_chain(c, layer, a, st));
   return COMPKV_OK;
 }
 
@@ -689,12 +845,12 @@ compkv_status compkv_decode_host(compkv_ctx* c, int layer, const float* q_host, 
     ++c->launches;
     a.out = out_host;
     if (sel_host) a.sel = sel_host;
-    COMPKV_TRY(launch_chain(c, COMPKV_KERNEL_DECODE, a, kFusedDecode, st, "decode launch"));
+    COMPKV_TRY(decode_chain(c, layer, a, st));
   } else {
     COMPKV_TRY(cuda_status(cudaMemcpyAsync(dq, q_host, qb, cudaMemcpyHostToDevice, st), "q copy"));
     COMPKV_TRY(cuda_status(cudaMemcpyAsync(dk, k_new_host, kb, cudaMemcpyHostToDevice, st), "k_new copy"));
     COMPKV_TRY(cuda_status(cudaMemcpyAsync(dv, v_new_host, kb, cudaMemcpyHostToDevice, st), "v_new copy"));
-    COMPKV_TRY(launch_chain(c, COMPKV_KERNEL_DECODE, a, kFusedDecode, st, "decode launch"));
+    COMPKV_TRY(decode_chain(c, layer, a, st));
     COMPKV_TRY(cuda_status(cudaMemcpyAsync(out_host, dout, qb, cudaMemcpyDeviceToHost, st), "out copy"));
     if (sel_host)
       COMPKV_TRY(cuda_status(cudaMemcpyAsync(sel_host, a.sel, units * (size_t)c->lay.K * 4, cudaMemcpyDeviceToHost, st),
@@ -721,6 +877,7 @@ compkv_status compkv_prefill_qkv(compkv_ctx* c, int layer, const compkv_rope_arg
   RopePrefillArgs p;
   RopeArgs& a = p.rope;
   COMPKV_TRY(rope_base(c, layer, args, q, &a));
+  p.kv8 = kv8_args(c, layer);
   if (!counts) return fail(COMPKV_ERR_INVALID_ARG, "counts is NULL");
   int64_t tokens = 0, blocks = 0;
   for (int s = 0; s < a.B; ++s) {
@@ -750,6 +907,7 @@ compkv_status compkv_prefill_qkv(compkv_ctx* c, int layer, const compkv_rope_arg
 compkv_status compkv_fork(compkv_ctx* c, int layer0, int layers, int n, const int* src, const int* dst, const int* lens,
                           void* stream) {
   PageArgs a;
+  COMPKV_TRY(needs_bf16(c, "compkv_fork"));
   COMPKV_TRY(page_base(c, layer0, layers, n, src, dst, &a));
   for (int i = 0; lens && i < n; ++i) {
     if (lens[i] < -1) return fail(COMPKV_ERR_INVALID_ARG, "lens[%d] = %d is below -1", i, lens[i]);
@@ -795,6 +953,7 @@ compkv_status compkv_fork(compkv_ctx* c, int layer0, int layers, int n, const in
 compkv_status compkv_compact(compkv_ctx* c, int layer0, int layers, int n, const int* src, const int* dst,
                              const int* keep, int keep_blocks, void* stream) {
   PageArgs a;
+  COMPKV_TRY(needs_bf16(c, "compkv_compact"));
   COMPKV_TRY(page_base(c, layer0, layers, n, src, dst, &a));
   COMPKV_TRY(check_ptr(keep, "keep", 4));
   if (keep_blocks < 1 || keep_blocks > c->lay.max_cap_blocks)
@@ -829,6 +988,7 @@ compkv_status compkv_attend_shared(compkv_ctx* c, int layer, const void* q, int 
                                    const int* prefix_len, void* out, void* workspace, size_t workspace_bytes,
                                    void* stream) {
   COMPKV_TRY(check_call(c, layer));
+  COMPKV_TRY(needs_bf16(c, "compkv_attend_shared"));
   COMPKV_TRY(check_ptr(q, "q", 16));
   COMPKV_TRY(check_ptr(out, "out", 16));
   COMPKV_TRY(check_ptr(workspace, "workspace", 256));
@@ -916,6 +1076,69 @@ compkv_status compkv_attend_shared(compkv_ctx* c, int layer, const void* q, int 
                 [&] { return launch_attend_shared(a, st); });
 }
 
+compkv_status compkv_read(compkv_ctx* c, int layer, const int* starts, const int* counts, int type, void* k, void* v,
+                          void* stream) {
+  COMPKV_TRY(check_call(c, layer));
+  if (type != COMPKV_BF16 && type != COMPKV_F32)
+    return fail(COMPKV_ERR_INVALID_ARG, "type must be COMPKV_BF16 or COMPKV_F32 (got %d)", type);
+  COMPKV_TRY(check_ptr(k, "k", 32));
+  COMPKV_TRY(check_ptr(v, "v", 32));
+  if (!counts) return fail(COMPKV_ERR_INVALID_ARG, "counts is NULL");
+  ReadArgs a;
+  memset(&a, 0, sizeof(a));
+  a.kv8 = kv8_args(c, layer);
+  const int d = c->cfg.head_dim;
+  const int64_t rows = c->lay.rows_per_layer * (int64_t)layer;
+  if (a.kv8.type == kKvBf16) {
+    a.bk = reinterpret_cast<const __nv_bfloat16*>(c->buf.k) + rows * kBlock * d;
+    a.bv = reinterpret_cast<const __nv_bfloat16*>(c->buf.v) + rows * kBlock * d;
+  }
+  a.seq_len = c->buf.seq_len + (int64_t)layer * c->cfg.batch;
+  a.status = status_word(c);
+  a.k = k;
+  a.v = v;
+  a.out_f32 = type == COMPKV_F32;
+  a.B = c->cfg.batch;
+  a.Hkv = c->cfg.num_kv_heads;
+  a.d = d;
+  int64_t tokens = 0, blocks = 0;
+  for (int s = 0; s < a.B; ++s) {
+    const int start = starts ? starts[s] : 0, count = counts[s], cap = c->lay.cap_blocks[s] * kBlock;
+    if (count < 0) return fail(COMPKV_ERR_INVALID_ARG, "counts[%d] = %d is negative", s, count);
+    a.seq_row0[s] = c->lay.seq_row0[s];
+    a.cap_blocks[s] = c->lay.cap_blocks[s];
+    a.token0[s] = (int)tokens;
+    a.item0[s] = (int)blocks;
+    if (!count) continue;
+    if (start < 0) return fail(COMPKV_ERR_INVALID_ARG, "starts[%d] = %d is negative", s, start);
+    if (start > cap || count > cap - start)
+      return fail(COMPKV_ERR_CAPACITY, "tokens [%d, %d + %d) of sequence %d exceed its capacity %d", start, start, count, s, cap);
+    a.starts[s] = start;
+    a.counts[s] = count;
+    tokens += count;
+    blocks += (start + count - 1) / kBlock - start / kBlock + 1;
+    if (tokens > 0x7fffffff) return fail(COMPKV_ERR_UNSUPPORTED_SHAPE, "more than 2^31 - 1 tokens in one call");
+  }
+  a.item0[a.B] = (int)blocks;
+  if (!blocks) return COMPKV_OK;
+  cudaStream_t st = (cudaStream_t)stream;
+  return launch(c, COMPKV_KERNEL_READ, st, "read launch", [&] { return launch_read(a, st); });
+}
+
+compkv_status compkv_attend_all(compkv_ctx* c, int layer, const void* q, int type, void* out, void* stream) {
+  COMPKV_TRY(check_call(c, layer));
+  if (c->kv8.type == COMPKV_BF16)
+    return fail(COMPKV_ERR_UNSUPPORTED_SHAPE,
+                "compkv_attend_all takes a cache in 8 bits; compkv_attend_shared without a prefix does it for bf16");
+  COMPKV_TRY(check_ptr(q, "q", 16));
+  COMPKV_TRY(check_ptr(out, "out", 16));
+  if (type != COMPKV_BF16 && type != COMPKV_F32)
+    return fail(COMPKV_ERR_INVALID_ARG, "type must be COMPKV_BF16 or COMPKV_F32 (got %d)", type);
+  const Attend8Args a = attend8_args(c, layer, q, type == COMPKV_BF16, out, nullptr, false);
+  cudaStream_t st = (cudaStream_t)stream;
+  return launch(c, COMPKV_KERNEL_ATTEND_ALL, st, "attention launch", [&] { return launch_attend8(a, st); });
+}
+
 compkv_status compkv_device_status(compkv_ctx* c, void* stream) {
   if (!c) return fail(COMPKV_ERR_INVALID_ARG, "context is NULL");
   cudaStream_t st = (cudaStream_t)stream;
@@ -948,6 +1171,7 @@ compkv_status compkv_trace(compkv_ctx* c, void* buf, size_t bytes) {
     c->trace_cap = 0;
     return COMPKV_OK;
   }
+  COMPKV_TRY(needs_bf16(c, "compkv_trace"));
   COMPKV_TRY(check_ptr(buf, "trace buffer", 8));
   const size_t header = 8;
   if (bytes < header + 64) return fail(COMPKV_ERR_INVALID_ARG, "trace buffer of %zu bytes holds no record", bytes);
@@ -1044,6 +1268,7 @@ compkv_status compkv_internal_decode_in(const compkv_config* cfg, const compkv_b
   c.cfg = *cfg;
   c.cfg.capacity_tokens = nullptr;
   c.buf = *bufs;
+  memset(&c.kv8, 0, sizeof(c.kv8));
   c.buf.scratch = scratch;
   c.buf.scratch_bytes = scratch_bytes;
   c.lay = L;

@@ -86,6 +86,21 @@ struct LayerArgs {
   int lens[kMaxBatch];           // prefill lengths (compkv_prefill only)
 };
 
+// How a cache holds K and V (mirrors the element types of the C ABI).
+enum KvType : int { kKvBf16 = 0, kKvInt8 = 2, kKvE4m3 = 3 };
+
+// One layer of a cache in 8 bits.
+struct Kv8Args {
+  uint8_t* k;                  // [rows][16][d] codes
+  uint8_t* v;
+  float* kscale;               // [rows]
+  float* vscale;
+  __nv_bfloat16* tail;         // [B][Hkv][2][K, V][16][d]: tokens of two blocks of each sequence as they came: the last
+                               // one, and the one that its last call of many tokens began in the middle of
+  int* tail_len;               // [B][Hkv][2]: the tokens up to the last one there (0: nothing is)
+  int type;                    // KvType
+};
+
 // Arguments of the kernels that norm and rotate the projection's heads.
 struct RopeArgs {
   const void* qkv;             // [tokens] rows of (Hq + 2 Hkv) d bf16 or fp32, `stride` elements apart
@@ -111,12 +126,65 @@ struct RopeArgs {
 };
 struct RopePrefillArgs {       // many tokens, per sequence
   RopeArgs rope;
+  Kv8Args kv8;                 // a cache in 8 bits (type kKvBf16: rope.k and rope.v)
   int64_t seq_row0[kMaxBatch];
   int cap_blocks[kMaxBatch];
   int starts[kMaxBatch];       // slot of its first token
   int counts[kMaxBatch];       // its tokens
   int token0[kMaxBatch];       // its first token in qkv
   int item0[kMaxBatch + 1];    // cache blocks that receive tokens, before sequence s
+};
+
+// Arguments of the kernel that reads tokens back.
+struct ReadArgs {
+  Kv8Args kv8;                 // where it is not kKvBf16
+  const __nv_bfloat16* bk;     // K and V of this layer where it is
+  const __nv_bfloat16* bv;
+  const int* seq_len;          // [B] of this layer
+  int* status;
+  void* k;                     // [tokens][Hkv][d] bf16, or fp32 where out_f32
+  void* v;
+  int out_f32;
+  int B, Hkv, d;
+  int64_t seq_row0[kMaxBatch];
+  int cap_blocks[kMaxBatch];
+  int starts[kMaxBatch];       // first slot of sequence s
+  int counts[kMaxBatch];       // its tokens
+  int token0[kMaxBatch];       // its first token in the output
+  int item0[kMaxBatch + 1];    // cache blocks read before sequence s
+};
+
+// Arguments of the attention over a cache in 8 bits.
+struct Attend8Args {
+  Kv8Args kv8;
+  const int* seq_len;          // [B] of this layer
+  const void* q;               // [B][Hq][d] fp32, or bf16 where q_bf16
+  void* out;                   // the same type
+  float* acc;                  // partial outputs [2 P][G][d], two of every CTA
+  float2* ml;                  // [2 P][G]: reference of their weights (log2 units) and the weights' sum
+  int* arrive;                 // [units] CTAs that have left their parts of a unit (zero between calls)
+  int* status;
+  int q_bf16;
+  int B, Hkv, G, d;
+  int P;                       // CTAs
+  int64_t layer_row0;          // first row of this layer in the whole cache (tensor-map coordinates)
+  int64_t seq_row0[kMaxBatch];
+  int cap_blocks[kMaxBatch];
+  // a selection with Mean compensation; null: every token
+  const int* sel;              // [B][Hkv][K]
+  int K;
+  int selects;                 // the chain made the selection (its stream then skips what fits the budget)
+  int no_comp;                 // the variant without compensation
+  int stream_P, r;             // the stream's plan
+  const float4* rec;           // its records, sums and mean logits (LayerArgs)
+  const float* comp;
+  const float* zs;
+  const float* vbar;
+  // tensor maps of the whole K and V codes: boxes of d x 16 and d x 32 tokens, swizzled over d bytes
+  alignas(64) unsigned long long k16[16];
+  alignas(64) unsigned long long v16[16];
+  alignas(64) unsigned long long k32[16];
+  alignas(64) unsigned long long v32[16];
 };
 
 // Arguments of the kernels that copy and compact pages (16-token blocks).

@@ -19,6 +19,9 @@ enum FusedFlags : int {
 constexpr int kFusedDecode = kFAppend | kFScore | kFComp | kFSelect | kFAttend;
 constexpr int kFusedScoreSelect = kFScore | kFSelect;
 constexpr int kFusedAttend = kFComp | kFAttend;
+// Of a cache in 8 bits: the stream of a decode step behind an append of its own; the selection is
+// kFusedScoreSelect's and the attention launch_attend8's.
+constexpr int kStreamDecode8 = kFScore | kFComp | kFSelect;
 constexpr int kMaxStreamCtas = 1024;   // the stream kernel's grid at most (segment records: this + units)
 
 cudaError_t launch_prefill(const LayerArgs& a, int64_t rows_per_layer, cudaStream_t st);
@@ -30,6 +33,14 @@ cudaError_t launch_stage_in(void* d0, const void* s0, size_t b0, void* d1, const
 // Norms and rotation of the projection's heads: one token per sequence, or many into the cache.
 cudaError_t launch_rope_step(const RopeArgs& a, cudaStream_t st);
 cudaError_t launch_rope_prefill(const RopePrefillArgs& a, int sms, cudaStream_t st);
+// A cache in 8 bits: one token per sequence appended, tokens read back (from bf16 caches too), and attention over all
+// tokens or over a selection.
+cudaError_t launch_append8(const LayerArgs& a, const Kv8Args& kv8, cudaStream_t st);
+cudaError_t launch_read(const ReadArgs& a, cudaStream_t st);
+constexpr int kMaxAttend8Ctas = 160;
+inline size_t attend8_parts(int G, int d) { return (size_t)2 * kMaxAttend8Ctas * G * (d + 2) * 4; }
+cudaError_t prepare_attend8(int d);
+cudaError_t launch_attend8(const Attend8Args& a, cudaStream_t st);
 // Pages: copies between sequences, and listed blocks to the front of a sequence.
 // Blocks of one work item of a copy: 16, or 4 where that still leaves a multiprocessor two items at most (three
 // copies of 1025 tokens: 8.3 us with 16, 7.8 with 4).

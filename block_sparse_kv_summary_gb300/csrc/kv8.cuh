@@ -1,0 +1,120 @@
+// K and V in 8 bits.  A block's 16 tokens of one head are held as codes c and
+// one fp32 scale; with m the largest magnitude among its tokens and M the
+// type's largest value (127 for int8, 448 for e4m3),
+//
+//     scale = m / M,    c = nearest(x (M / m)), halfway cases to even,
+//
+// each operation rounded once, and everything zero where m < 2^-100: there the
+// quotients leave the normal numbers, and no logit or output notices.  A block
+// with an infinity or a NaN has that as its scale and codes of zero, so that
+// all of it reads as NaN.
+//
+// int8 spaces its values evenly below m, which suits coordinates of one size;
+// e4m3 keeps four bits of each value, which suits blocks whose coordinates
+// differ in size (channels some times wider than the others).
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "compkv_device.cuh"
+
+namespace compkv {
+
+template <int KV>
+struct Codes;
+template <>
+struct Codes<kKvInt8> {
+  static constexpr float most = 127.f;
+  // four values (|x| <= 127 up to a rounding, which the nearest integer swallows)
+  static __device__ __forceinline__ uint32_t pack(float a, float b, float c, float d) {
+    const uint32_t lo = __byte_perm(__float2int_rn(a), __float2int_rn(b), 0x0040);
+    const uint32_t hi = __byte_perm(__float2int_rn(c), __float2int_rn(d), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
+  }
+  static __device__ __forceinline__ float4 unpack(uint32_t w) {
+    const char4 c = *reinterpret_cast<const char4*>(&w);
+    return make_float4((float)c.x, (float)c.y, (float)c.z, (float)c.w);
+  }
+};
+template <>
+struct Codes<kKvE4m3> {
+  static constexpr float most = 448.f;
+  static __device__ __forceinline__ uint32_t pack(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | hi << 16;
+  }
+  static __device__ __forceinline__ float4 unpack(uint32_t w) {
+    const float2 a = __half22float2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3));
+    const float2 b = __half22float2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3));
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+};
+
+// A block's scale and the factor of its values, from the bits of its largest magnitude (an infinity or a NaN
+// is larger than any number).
+struct Scale {
+  float scale, inv;
+  template <int KV>
+  static __device__ __forceinline__ Scale of(uint32_t bits) {
+    const float m = __uint_as_float(bits);
+    Scale s = {__fdiv_rn(m, Codes<KV>::most), __fdiv_rn(Codes<KV>::most, m)};
+    if (m < 0x1p-100f) s = {0.f, 0.f};
+    if (bits >= 0x7f800000u) s.inv = 0.f;
+    return s;
+  }
+};
+
+// D / 32 consecutive coordinates of a token from a lane's registers.
+__device__ __forceinline__ void load_words(const __nv_bfloat16* p, uint32_t (&w)[2]) {
+  const uint2 x = __ldcg(reinterpret_cast<const uint2*>(p));
+  w[0] = x.x;
+  w[1] = x.y;
+}
+__device__ __forceinline__ void load_words(const __nv_bfloat16* p, uint32_t (&w)[1]) {
+  w[0] = __ldcg(reinterpret_cast<const uint32_t*>(p));
+}
+
+// A block's codes and scale from its tokens, by one warp; lane l holds the
+// coordinates [l D / 32, (l + 1) D / 32) of every token as bf16 pairs, zero
+// where the block has no token.
+template <int D, int KV>
+__device__ __forceinline__ void quantise_block(const uint32_t (&t)[kBlock][D / 64], uint8_t* codes, float* scale, int lane) {
+  constexpr int W = D / 64;
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < kBlock; ++j)
+#pragma unroll
+    for (int i = 0; i < W; ++i) m = max(m, max(t[j][i] << 16 & 0x7fffffffu, t[j][i] & 0x7fff0000u));
+  m = __reduce_max_sync(0xffffffffu, m);
+  const Scale s = Scale::of<KV>(m);
+  // (an infinity times zero is a NaN: codes of such a block are set, not computed)
+  const uint32_t live = m < 0x7f800000u ? 0xffffffffu : 0u;
+#pragma unroll
+  for (int j = 0; j < kBlock; ++j) {
+    float x[2 * W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      x[2 * i] = __uint_as_float((t[j][i] & live) << 16) * s.inv;
+      x[2 * i + 1] = __uint_as_float(t[j][i] & live & 0xffff0000u) * s.inv;
+    }
+    if constexpr (W == 2)
+      reinterpret_cast<uint32_t*>(codes + j * D)[lane] = Codes<KV>::pack(x[0], x[1], x[2], x[3]);
+    else
+      reinterpret_cast<uint16_t*>(codes + j * D)[lane] = (uint16_t)Codes<KV>::pack(x[0], x[1], 0.f, 0.f);
+  }
+  if (lane == 0) *scale = s.scale;
+}
+
+// The tail's tokens of block b of a unit, if it holds at least the first `lo` of them: K, with V behind it; else null.
+template <int D>
+__device__ __forceinline__ __nv_bfloat16* tail_of(const Kv8Args& c, int unit, int b, int lo) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int len = __ldcg(c.tail_len + 2 * unit + i);
+    if (len > b * kBlock && len <= (b + 1) * kBlock && len - b * kBlock >= lo) return c.tail + (int64_t)(2 * unit + i) * 2 * kBlock * D;
+  }
+  return nullptr;
+}
+
+}  // namespace compkv

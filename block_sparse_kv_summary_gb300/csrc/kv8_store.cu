@@ -1,0 +1,205 @@
+// A cache in 8 bits: one token per sequence appended, and tokens read back
+// (also from a cache in bf16).  Many tokens are written by rope_kernels.cu.
+#include "block_summary.cuh"
+#include "compkv_launch.h"
+#include "kv8.cuh"
+
+namespace compkv {
+
+namespace {
+
+// One CTA per sequence, a warp per KV head at a time.  Token L (L = seq_len)
+// joins the tokens of its block, which the tail holds in bf16; the block's
+// summary and codes are formed again from all of them, so that a block's
+// contents do not depend on how its tokens arrived.  Where the sequence was
+// cut back into an older block, the tokens in front come from their codes.
+// Bound by latency: length, tail and codes in a row.
+template <int D, int KV>
+__global__ void __launch_bounds__(256) append8_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ Kv8Args c) {
+  constexpr int V = D / 32, W = D / 64;
+  const int s = blockIdx.x, lane = threadIdx.x & 31;
+  const int L = __ldcg(a.seq_len + s);
+  const bool fits = L >= 0 && L < a.cap_blocks[s] * kBlock;
+  const int b = L / kBlock, slot = L % kBlock;
+  for (int h = threadIdx.x >> 5; fits && h < a.Hkv; h += blockDim.x >> 5) {
+    const int64_t row = row_of(a, s, h, b);
+    const int unit = s * a.Hkv + h;
+    const __nv_bfloat16* from = tail_of<D>(c, unit, b, slot);
+    __nv_bfloat16* to = c.tail + (int64_t)unit * 4 * kBlock * D;
+    const int other = __ldcg(c.tail_len + 2 * unit + 1);
+    __syncwarp();  // every lane has read the tail's lengths
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      __nv_bfloat16* tail = to + kv * kBlock * D + lane * V;
+      uint8_t* codes = (kv ? c.v : c.k) + row * kBlock * D;
+      float* scale = (kv ? c.vscale : c.kscale) + row;
+      const __nv_bfloat16* token = (kv ? a.v_new : a.k_new) + (int64_t)unit * D + lane * V;
+      const float old = __ldcg(scale);
+      uint32_t t[kBlock][W];
+#pragma unroll
+      for (int j = 0; j < kBlock; ++j) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) t[j][i] = 0;
+        if (j > slot) continue;
+        if (j == slot) {
+          load_words(token, t[j]);
+        } else if (from) {
+          load_words(from + (kv * kBlock + j) * D + lane * V, t[j]);
+          if (from == to) continue;
+        } else {
+          const uint8_t* p = codes + j * D + lane * V;
+          const float4 x = Codes<KV>::unpack(W == 2 ? __ldcg(reinterpret_cast<const uint32_t*>(p)) : __ldcg(reinterpret_cast<const uint16_t*>(p)));
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            const __nv_bfloat162 y = i ? __floats2bfloat162_rn(x.z * old, x.w * old) : __floats2bfloat162_rn(x.x * old, x.y * old);
+            t[j][i] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) reinterpret_cast<uint32_t*>(tail + j * D)[i] = t[j][i];
+      }
+      quantise_block<D, KV>(t, codes, scale, lane);
+    }
+    if (lane == 0) {
+      c.tail_len[2 * unit] = L + 1;
+      if (other > b * kBlock) c.tail_len[2 * unit + 1] = 0;  // of this block, or behind it
+    }
+    // (each lane reads back what it wrote itself)
+    warp_block_summary<D>(to, to + kBlock * D, slot + 1, nullptr, nullptr, a.kbar + row * D, a.vbar + row * D, a.dbar + row * a.r, a.r, lane);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    if (fits) a.seq_len[s] = L + 1;
+    else set_error(a.status, kDevCapacity, s, -1, 1);
+  }
+}
+
+// 16 values of one token from their codes, or as they stand in bf16.
+struct Sixteen {
+  float x[16];
+};
+template <int KV>
+__device__ __forceinline__ void values(const uint4 (&w)[KV == kKvBf16 ? 2 : 1], float scale, Sixteen& y) {
+  if constexpr (KV == kKvBf16) {
+    const uint32_t v[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      y.x[2 * i] = __uint_as_float(v[i] << 16);
+      y.x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+    }
+  } else {
+    const uint32_t v[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 f = Codes<KV>::unpack(v[i]);
+      y.x[4 * i] = f.x * scale;
+      y.x[4 * i + 1] = f.y * scale;
+      y.x[4 * i + 2] = f.z * scale;
+      y.x[4 * i + 3] = f.w * scale;
+    }
+  }
+}
+// 32 bytes in one store: a whole sector, whatever the lanes beside write.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// A warp per block, head and one of K and V: a lane takes 16 values of a token
+// at a time, its loads of the whole block in flight together.  Heads follow one
+// another, then blocks, so that the rows of a token come out close in time.
+template <int D, int KV, bool F32>
+__global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadArgs a) {
+  constexpr int CH = D / 16, N = kBlock * CH / 32, L = KV == kKvBf16 ? 2 : 1;  // chunks of a token; of a lane; their loads
+  const int lane = threadIdx.x & 31;
+  const int64_t item = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int per = 2 * a.Hkv;
+  const int64_t at = item / per;
+  if (at >= a.item0[a.B]) return;
+  const int kv = (int)(item % per) / a.Hkv, h = (int)(item % per) % a.Hkv;
+  int s = 0;
+  while (s + 1 < a.B && a.item0[s + 1] <= at) ++s;
+  const int b = a.starts[s] / kBlock + (int)(at - a.item0[s]);
+  const int have = __ldcg(a.seq_len + s), end = min(a.starts[s] + a.counts[s], have);
+  if (a.starts[s] + a.counts[s] > have && lane == 0 && item == (int64_t)a.item0[s] * per) set_error(a.status, kDevInvalidArg, s, -1, 3);
+  const int64_t row = a.seq_row0[s] + (int64_t)h * a.cap_blocks[s] + b;
+  uint4 w[N][L];
+  float scale = 1.f;
+  if constexpr (KV != kKvBf16) scale = __ldg((kv ? a.kv8.vscale : a.kv8.kscale) + row);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int x = i * 32 + lane, tok = b * kBlock + x / CH;  // chunk x of the block
+    const char* p = KV == kKvBf16 ? reinterpret_cast<const char*>((kv ? a.bv : a.bk) + row * kBlock * D) + x * 32
+                                  : reinterpret_cast<const char*>((kv ? a.kv8.v : a.kv8.k) + row * kBlock * D) + x * 16;
+#pragma unroll
+    for (int l = 0; l < L; ++l) w[i][l] = tok < end && tok >= a.starts[s] ? __ldcs(reinterpret_cast<const uint4*>(p) + l) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int x = i * 32 + lane, tok = b * kBlock + x / CH;
+    if (tok >= end || tok < a.starts[s]) continue;
+    Sixteen y;
+    values<KV>(w[i], scale, y);
+    const int64_t o = (((int64_t)a.token0[s] + tok - a.starts[s]) * a.Hkv + h) * D + x % CH * 16;
+    uint32_t z[8];
+    if constexpr (F32) {
+      float* out = reinterpret_cast<float*>(kv ? a.v : a.k) + o;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = __float_as_uint(y.x[8 * k + e]);
+        store32(out + 8 * k, z);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(y.x[2 * e], y.x[2 * e + 1]);
+        z[e] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+      store32(reinterpret_cast<__nv_bfloat16*>(kv ? a.v : a.k) + o, z);
+    }
+  }
+}
+
+template <int D, int KV>
+cudaError_t read_as(const ReadArgs& a, cudaStream_t st) {
+  const int64_t warps = (int64_t)a.item0[a.B] * 2 * a.Hkv;
+  const unsigned grid = (unsigned)((warps + 7) / 8);
+  if (a.out_f32) read_kernel<D, KV, true><<<grid, 256, 0, st>>>(a);
+  else read_kernel<D, KV, false><<<grid, 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_append8(const LayerArgs& a, const Kv8Args& c, cudaStream_t st) {
+  const int threads = 32 * (a.Hkv < 8 ? a.Hkv : 8);
+  const bool i8 = c.type == kKvInt8;
+  if (a.d == 128) {
+    if (i8) append8_kernel<128, kKvInt8><<<a.B, threads, 0, st>>>(a, c);
+    else append8_kernel<128, kKvE4m3><<<a.B, threads, 0, st>>>(a, c);
+  } else {
+    if (i8) append8_kernel<64, kKvInt8><<<a.B, threads, 0, st>>>(a, c);
+    else append8_kernel<64, kKvE4m3><<<a.B, threads, 0, st>>>(a, c);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_read(const ReadArgs& a, cudaStream_t st) {
+  if (!a.item0[a.B]) return cudaSuccess;
+  if (a.d == 128) {
+    switch (a.kv8.type) {
+      case kKvInt8: return read_as<128, kKvInt8>(a, st);
+      case kKvE4m3: return read_as<128, kKvE4m3>(a, st);
+      default: return read_as<128, kKvBf16>(a, st);
+    }
+  }
+  switch (a.kv8.type) {
+    case kKvInt8: return read_as<64, kKvInt8>(a, st);
+    case kKvE4m3: return read_as<64, kKvE4m3>(a, st);
+    default: return read_as<64, kKvBf16>(a, st);
+  }
+}
+
+}  // namespace compkv

@@ -22,6 +22,7 @@
 #include <type_traits>
 
 #include "compkv_launch.h"
+#include "kv8.cuh"
 
 namespace compkv {
 
@@ -410,6 +411,35 @@ __device__ __forceinline__ void tile_summary(const __nv_bfloat16* tile, int n, f
   }
 }
 
+// Codes and scale of a block from its tokens in shared memory (zero behind the last one), by one warp; the tokens also
+// go to `tail`, unless it is null.
+template <int D, int KV>
+__device__ __forceinline__ void tile_quantise(const __nv_bfloat16* tile, int n, uint8_t* codes, float* scale, __nv_bfloat16* tail, int lane) {
+  constexpr int W = D / 64;
+  uint32_t t[kBlock][W];
+#pragma unroll
+  for (int j = 0; j < kBlock; ++j)
+#pragma unroll
+    for (int i = 0; i < W; ++i) t[j][i] = reinterpret_cast<const uint32_t*>(tile + j * D)[lane * W + i];
+  quantise_block<D, KV>(t, codes, scale, lane);
+  if (!tail) return;
+#pragma unroll
+  for (int j = 0; j < kBlock; ++j) {
+    if (j >= n) break;
+#pragma unroll
+    for (int i = 0; i < W; ++i) reinterpret_cast<uint32_t*>(tail + j * D)[lane * W + i] = t[j][i];
+  }
+}
+
+// Eight coordinates of a token from a block's codes, rounded to bf16.
+template <int KV>
+__device__ __forceinline__ uint4 dequantised(const uint8_t* p, const Place& at, float scale) {
+  const float4 x = Codes<KV>::unpack(__ldcg(reinterpret_cast<const uint32_t*>(p + at.a)));
+  const float4 y = Codes<KV>::unpack(__ldcg(reinterpret_cast<const uint32_t*>(p + at.b)));
+  return make_uint4(round2(x.x * scale, x.y * scale), round2(x.z * scale, x.w * scale), round2(y.x * scale, y.y * scale),
+                    round2(y.z * scale, y.w * scale));
+}
+
 // One CTA per 16-token cache block that receives tokens and `hc` KV heads with
 // their query heads.  A warp has 32 / (D/8) tokens and goes through the heads,
 // kBatch of them in flight, so that a token's factors are formed once and stay
@@ -419,7 +449,7 @@ __device__ __forceinline__ void tile_summary(const __nv_bfloat16* tile, int n, f
 // heads of 128 move 0.84 GB in 166 us, 0.74 of the copy rate (1.24 GB from an fp32
 // projection in 231 us, 0.79); 4096 tokens take 31 us, 0.51.
 constexpr int kBatch = 4;
-template <int D, typename T, bool INTER>
+template <int D, typename T, bool INTER, int KV>
 __global__ void __launch_bounds__(256, 3) rope_prefill_kernel(const __grid_constant__ RopePrefillArgs g, int hc, bool ahead) {
   const RopeArgs& a = g.rope;
   constexpr int LPH = D / 8, TPW = 32 / LPH, WT = kBlock / TPW, TEAMS = 8 / WT;
@@ -427,83 +457,122 @@ __global__ void __launch_bounds__(256, 3) rope_prefill_kernel(const __grid_const
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int s = 0;
   while (s + 1 < a.B && g.item0[s + 1] <= (int)blockIdx.x) ++s;
-  const int b = g.starts[s] / kBlock + ((int)blockIdx.x - g.item0[s]);
-  const int lo = max(g.starts[s] - b * kBlock, 0);                     // slots of this block that receive tokens:
-  const int hi = min(g.starts[s] + g.counts[s] - b * kBlock, kBlock);  // [lo, hi)
+  int b = g.starts[s] / kBlock + ((int)blockIdx.x - g.item0[s]);
   const int kv0 = blockIdx.y * hc, kvn = min(hc, a.Hkv - kv0);
   if ((int)blockIdx.x == g.item0[s] && blockIdx.y == 0 && threadIdx.x == 0) a.seq_len[s] = g.starts[s] + g.counts[s];
+  const int last = (g.starts[s] + g.counts[s] - 1) / kBlock;
+  // In 8 bits, the tail that the first block's earlier tokens come from is the one that the last block's tokens
+  // replace: one CTA then does both, one after the other.
+  const bool both = KV != kKvBf16 && g.starts[s] % kBlock && last != g.starts[s] / kBlock;
+  if (both && b == last) return;
 
-  const int j = warp % WT * TPW + lane / LPH, team = warp / WT;  // this lane's token; warps of a team share heads
-  const bool live = j >= lo && j < hi;
-  const int64_t tok = (int64_t)g.token0[s] + b * kBlock - g.starts[s] + j;
-  const int pos = !live ? 0 : a.positions ? __ldg(a.positions + tok) : b * kBlock + j;
-  const float* row = table_row(a, pos, s, live && blockIdx.y == 0 && team == 0 && (lane & (LPH - 1)) == 0);
-  const Place at = place<D, INTER>(lane & (LPH - 1), a.rot);
-  const T* src = reinterpret_cast<const T*>(a.qkv) + tok * a.stride;
-  // the token's heads start on their way to L2 together; the batches below then wait for L2 alone
-  if (ahead && live && (lane & (LPH - 1)) == 0 && team == 0) {
-    const int G = a.Hq / a.Hkv;
-    prefetch_l2(src + (a.Hq + kv0) * D, kvn * D * sizeof(T));
-    prefetch_l2(src + (a.Hq + a.Hkv + kv0) * D, kvn * D * sizeof(T));
-    prefetch_l2(src + kv0 * G * D, kvn * G * D * sizeof(T));
-  }
+#pragma unroll 1
+  for (;;) {
+    const int lo = max(g.starts[s] - b * kBlock, 0);                     // slots of this block that receive tokens:
+    const int hi = min(g.starts[s] + g.counts[s] - b * kBlock, kBlock);  // [lo, hi)
+    const int j = warp % WT * TPW + lane / LPH, team = warp / WT;  // this lane's token; warps of a team share heads
+    const bool live = j >= lo && j < hi;
+    const int64_t tok = (int64_t)g.token0[s] + b * kBlock - g.starts[s] + j;
+    const int pos = !live ? 0 : a.positions ? __ldg(a.positions + tok) : b * kBlock + j;
+    const float* row = table_row(a, pos, s, live && blockIdx.y == 0 && team == 0 && (lane & (LPH - 1)) == 0);
+    const Place at = place<D, INTER>(lane & (LPH - 1), a.rot);
+    const T* src = reinterpret_cast<const T*>(a.qkv) + tok * a.stride;
+    // the token's heads start on their way to L2 together; the batches below then wait for L2 alone
+    if (ahead && live && (lane & (LPH - 1)) == 0 && team == 0) {
+      const int G = a.Hq / a.Hkv;
+      prefetch_l2(src + (a.Hq + kv0) * D, kvn * D * sizeof(T));
+      prefetch_l2(src + (a.Hq + a.Hkv + kv0) * D, kvn * D * sizeof(T));
+      prefetch_l2(src + kv0 * G * D, kvn * G * D * sizeof(T));
+    }
 
-  {
-    const int G = a.Hq / a.Hkv, nq = kvn * G;
-    const T* q = src + kv0 * G * D;
-    const int64_t out = (tok * a.Hq + kv0 * G) * D;
-    const Factors f = factors(weights<INTER>(a.q_weight, at), angles(row, a.rot, at));
-    for (int i0 = team; i0 < nq; i0 += kBatch * TEAMS) {
-      Raw<T> raw[kBatch];
+    {
+      const int G = a.Hq / a.Hkv, nq = kvn * G;
+      const T* q = src + kv0 * G * D;
+      const int64_t out = (tok * a.Hq + kv0 * G) * D;
+      const Factors f = factors(weights<INTER>(a.q_weight, at), angles(row, a.rot, at));
+      for (int i0 = team; i0 < nq; i0 += kBatch * TEAMS) {
+        Raw<T> raw[kBatch];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) raw[u].load(q + (i0 + u * TEAMS) * D, at, live && i0 + u * TEAMS < nq);
+        for (int u = 0; u < kBatch; ++u) raw[u].load(q + (i0 + u * TEAMS) * D, at, live && i0 + u * TEAMS < nq);
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (i0 + u * TEAMS >= nq) break;
-        Pairs y;
-        turn_head<D>(raw[u].template pairs<INTER>(), f, a.q_weight != nullptr, a.eps, y);
-        if (live) put_query<INTER>(a, out + (i0 + u * TEAMS) * D, at, y);
+        for (int u = 0; u < kBatch; ++u) {
+          if (i0 + u * TEAMS >= nq) break;
+          Pairs y;
+          turn_head<D>(raw[u].template pairs<INTER>(), f, a.q_weight != nullptr, a.eps, y);
+          if (live) put_query<INTER>(a, out + (i0 + u * TEAMS) * D, at, y);
+        }
       }
     }
-  }
-  {
-    const T* k = src + (a.Hq + kv0) * D;
-    const T* v = k + a.Hkv * D;
-    const Factors f = factors(weights<INTER>(a.k_weight, at), angles(row, a.rot, at));
-    const int64_t first = (g.seq_row0[s] + (int64_t)kv0 * g.cap_blocks[s] + b) * kBlock + j, step = (int64_t)g.cap_blocks[s] * kBlock;
+    {
+      const T* k = src + (a.Hq + kv0) * D;
+      const T* v = k + a.Hkv * D;
+      const Factors f = factors(weights<INTER>(a.k_weight, at), angles(row, a.rot, at));
+      const int64_t first = (g.seq_row0[s] + (int64_t)kv0 * g.cap_blocks[s] + b) * kBlock + j, step = (int64_t)g.cap_blocks[s] * kBlock;
 #pragma unroll 1
-    for (int h = team; h < kvn; h += TEAMS) {
-      Raw<T> rk, rv;
-      rk.load(k + h * D, at, live);
-      rv.load(v + h * D, at, live);
-      __nv_bfloat16* kd = a.k + (first + h * step) * D;
-      __nv_bfloat16* vd = a.v + (first + h * step) * D;
-      uint4 x = make_uint4(0, 0, 0, 0), y = x;
-      if (j < lo) {
-        const uint2 xa = __ldcg(reinterpret_cast<const uint2*>(kd + at.a)), xb = __ldcg(reinterpret_cast<const uint2*>(kd + at.b));
-        const uint2 ya = __ldcg(reinterpret_cast<const uint2*>(vd + at.a)), yb = __ldcg(reinterpret_cast<const uint2*>(vd + at.b));
-        x = make_uint4(xa.x, xa.y, xb.x, xb.y);
-        y = make_uint4(ya.x, ya.y, yb.x, yb.y);
+      for (int h = team; h < kvn; h += TEAMS) {
+        Raw<T> rk, rv;
+        rk.load(k + h * D, at, live);
+        rv.load(v + h * D, at, live);
+        uint4 x = make_uint4(0, 0, 0, 0), y = x;
+        const int64_t slot = (first + h * step) * D;
+        if constexpr (KV == kKvBf16) {
+          if (j < lo) {
+            const __nv_bfloat16 *kd = a.k + slot, *vd = a.v + slot;
+            const uint2 xa = __ldcg(reinterpret_cast<const uint2*>(kd + at.a)), xb = __ldcg(reinterpret_cast<const uint2*>(kd + at.b));
+            const uint2 ya = __ldcg(reinterpret_cast<const uint2*>(vd + at.a)), yb = __ldcg(reinterpret_cast<const uint2*>(vd + at.b));
+            x = make_uint4(xa.x, xa.y, xb.x, xb.y);
+            y = make_uint4(ya.x, ya.y, yb.x, yb.y);
+          }
+        } else if (j < lo) {
+          if (const __nv_bfloat16* kd = tail_of<D>(g.kv8, s * a.Hkv + kv0 + h, b, lo)) {
+            kd += j * D;
+            const __nv_bfloat16* vd = kd + kBlock * D;
+            const uint2 xa = __ldcg(reinterpret_cast<const uint2*>(kd + at.a)), xb = __ldcg(reinterpret_cast<const uint2*>(kd + at.b));
+            const uint2 ya = __ldcg(reinterpret_cast<const uint2*>(vd + at.a)), yb = __ldcg(reinterpret_cast<const uint2*>(vd + at.b));
+            x = make_uint4(xa.x, xa.y, xb.x, xb.y);
+            y = make_uint4(ya.x, ya.y, yb.x, yb.y);
+          } else {
+            x = dequantised<KV>(g.kv8.k + slot, at, __ldcg(g.kv8.kscale + slot / (kBlock * D)));
+            y = dequantised<KV>(g.kv8.v + slot, at, __ldcg(g.kv8.vscale + slot / (kBlock * D)));
+          }
+        }
+        const uint4 z = turn_key<D, INTER>(rk.template pairs<INTER>(), f, row, a, at);
+        if (live) {
+          x = z;
+          y = rv.bf16();
+          if constexpr (KV == kKvBf16) {
+            put(a.k + slot, at, x);
+            put(a.v + slot, at, y);
+          }
+        }
+        put(tiles + (h * kBlock + j) * D, at, x);
+        put(tiles + ((hc + h) * kBlock + j) * D, at, y);
       }
-      const uint4 z = turn_key<D, INTER>(rk.template pairs<INTER>(), f, row, a, at);
-      if (live) {
-        x = z;
-        y = rv.bf16();
-        put(kd, at, x);
-        put(vd, at, y);
-      }
-      put(tiles + (h * kBlock + j) * D, at, x);
-      put(tiles + ((hc + h) * kBlock + j) * D, at, y);
     }
-  }
-  __syncthreads();
+    __syncthreads();
 #pragma unroll 1
-  for (int i = warp; i < 2 * kvn; i += 8) {
-    const bool is_k = i < kvn;
-    const int h = is_k ? i : i - kvn;
-    const int64_t r = g.seq_row0[s] + (int64_t)(kv0 + h) * g.cap_blocks[s] + b;
-    tile_summary<D>(tiles + ((is_k ? 0 : hc) + h) * kBlock * D, hi, (is_k ? a.kbar : a.vbar) + r * D,
-                    is_k ? a.dbar + r * a.r : nullptr, a.r, lane);
+    for (int i = warp; i < 2 * kvn; i += 8) {
+      const bool is_k = i < kvn;
+      const int h = is_k ? i : i - kvn;
+      const int64_t r = g.seq_row0[s] + (int64_t)(kv0 + h) * g.cap_blocks[s] + b;
+      const __nv_bfloat16* tile = tiles + ((is_k ? 0 : hc) + h) * kBlock * D;
+      tile_summary<D>(tile, hi, (is_k ? a.kbar : a.vbar) + r * D, is_k ? a.dbar + r * a.r : nullptr, a.r, lane);
+      if constexpr (KV != kKvBf16) {
+        // the tail takes the last block, and the first one where the call begins inside it
+        const int place = 2 * (s * a.Hkv + kv0 + h) + (b != last);
+        const bool kept = b == last || lo > 0;
+        tile_quantise<D, KV>(tile, hi, (is_k ? g.kv8.k : g.kv8.v) + r * kBlock * D, (is_k ? g.kv8.kscale : g.kv8.vscale) + r,
+                             kept ? g.kv8.tail + (int64_t)(2 * place + !is_k) * kBlock * D : nullptr, lane);
+        if (is_k && lane == 0) {
+          if (kept) g.kv8.tail_len[place] = b * kBlock + hi;
+          // what else stands there of this block or behind it has been replaced
+          if (b == g.starts[s] / kBlock && !both && g.kv8.tail_len[place | 1] > b * kBlock) g.kv8.tail_len[place | 1] = 0;
+        }
+      }
+    }
+    if (KV == kKvBf16 || !both || b == last) break;
+    b = last;
+    __syncthreads();  // the tiles are read
   }
 }
 
@@ -543,7 +612,14 @@ cudaError_t launch_rope_prefill(const RopePrefillArgs& g, int sms, cudaStream_t 
   // all (200 tokens 5.7 -> 6.3 us)
   const bool ahead = (int64_t)grid.x * grid.y > 8 * sms;
   return form(a, [&](auto d, auto t, auto inter) {
-    rope_prefill_kernel<decltype(d)::value, decltype(t), decltype(inter)::value><<<grid, 256, smem, st>>>(g, hc, ahead);
+    constexpr int D = decltype(d)::value;
+    constexpr bool I = decltype(inter)::value;
+    using T = decltype(t);
+    switch (g.kv8.type) {
+      case kKvInt8: rope_prefill_kernel<D, T, I, kKvInt8><<<grid, 256, smem, st>>>(g, hc, ahead); break;
+      case kKvE4m3: rope_prefill_kernel<D, T, I, kKvE4m3><<<grid, 256, smem, st>>>(g, hc, ahead); break;
+      default: rope_prefill_kernel<D, T, I, kKvBf16><<<grid, 256, smem, st>>>(g, hc, ahead);
+    }
     return cudaGetLastError();
   });
 }

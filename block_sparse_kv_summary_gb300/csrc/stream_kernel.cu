@@ -707,7 +707,8 @@ static const void* stream_fn_t(int r) {
 }
 template <int D, int G, int MODE>
 static const void* stream_fn(int r, bool trace = false) {
-  return trace ? stream_fn_t<D, G, MODE, true>(r) : stream_fn_t<D, G, MODE, false>(r);
+  if constexpr (MODE == kStreamDecode8) return stream_fn_t<D, G, MODE, false>(r);  // caches in 8 bits are not traced
+  else return trace ? stream_fn_t<D, G, MODE, true>(r) : stream_fn_t<D, G, MODE, false>(r);
 }
 
 template <int D, int G, int MODE>
@@ -765,6 +766,7 @@ static cudaError_t launch_stream_dg(const LayerArgs& a, int mode, cudaStream_t s
     case kFusedDecode: return launch_stream_mode<D, G, kFusedDecode>(a, st, pdl);
     case kFusedScoreSelect: return launch_stream_mode<D, G, kFusedScoreSelect>(a, st, pdl);
     case kFusedAttend: return launch_stream_mode<D, G, kFusedAttend>(a, st, pdl);
+    case kStreamDecode8: return launch_stream_mode<D, G, kStreamDecode8>(a, st, pdl);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -803,6 +805,7 @@ static cudaError_t prepare_stream_dg(int r) {
   cudaError_t e = prepare_stream_mode<D, G, kFusedDecode>(r);
   if (e == cudaSuccess) e = prepare_stream_mode<D, G, kFusedScoreSelect>(r);
   if (e == cudaSuccess) e = prepare_stream_mode<D, G, kFusedAttend>(r);
+  if (e == cudaSuccess) e = prepare_stream_mode<D, G, kStreamDecode8>(r);
   return e;
 }
 

@@ -242,8 +242,8 @@ compkv_status compkv_decode_static(const compkv_config *cfg, const compkv_buffer
  * between decode steps.  The CompKV page has no counterpart to these calls.
  * ------------------------------------------------------------------------- */
 
-/* Element types of the calls below. */
-enum { COMPKV_BF16 = 0, COMPKV_F32 = 1 };
+/* Element types of the calls below, and of K and V in a cache of 8 bits. */
+enum { COMPKV_BF16 = 0, COMPKV_F32 = 1, COMPKV_INT8 = 2, COMPKV_E4M3 = 3 };
 
 /* Norms and position rotation of a projection's heads (compkv_rope and
  * compkv_prefill_qkv).  Per head x of d coordinates:
@@ -353,6 +353,78 @@ compkv_status compkv_attend_shared(compkv_ctx *ctx, int layer, const void *q, in
                                    const int *prefix_len, void *out, void *workspace, size_t workspace_bytes,
                                    void *stream);
 
+/* ---------------------------------------------------------------------------
+ * K and V in 8 bits: half the memory of a token and half the bytes of a read.
+ * The CompKV page has no counterpart to these calls either.
+ *
+ * A row's K, and its V, are 16 x d codes c and one fp32 scale: the block's
+ * values are c * scale.  With m the largest magnitude among the block's tokens
+ * and M the type's largest value (127 for COMPKV_INT8, 448 for COMPKV_E4M3),
+ *     scale = m / M,   c = nearest(x * (M / m))   (halfway cases to even),
+ * every operation rounded once in fp32; both are zero where m < 2^-100.  int8
+ * puts its values evenly below m; e4m3 keeps four significant bits of each, which
+ * suits channels of very different size.  A block with an infinity or a NaN
+ * among its tokens reads as NaN altogether.
+ *
+ * The tokens of two blocks of each sequence are kept in bf16 too (the tail): of its
+ * last block, and of the block that the last compkv_prefill_qkv began in the
+ * middle of.  A token that joins tokens of such a block quantises it afresh from
+ * these, so that its codes are those of its tokens however they arrived, and
+ * also after the sequence was cut back to where that call began.  Where tokens
+ * are written behind a place in another block (compkv_prefill_qkv with such a
+ * start, or an append after the caller set seq_len back), the tokens in front of
+ * them in that block come from their codes, rounded to bf16.  Summaries are
+ * those of the tokens in bf16.  Codes, scales and tail are written by these
+ * calls; a caller that fills codes and scales itself (with kbar, vbar, dbar and
+ * seq_len) does so before any call wrote to the sequence, and with codes that
+ * are numbers (the two NaN codes of e4m3 are never written and mean nothing
+ * here).
+ *
+ * A context of such a cache takes compkv_rope, compkv_prefill_qkv,
+ * compkv_append, compkv_score_select, compkv_attend, compkv_decode,
+ * compkv_decode_host, compkv_read and compkv_attend_all; compkv_prefill,
+ * compkv_fork, compkv_compact, compkv_attend_shared and compkv_trace give
+ * COMPKV_ERR_UNSUPPORTED_SHAPE, and compkv_profile_enable(2) times its calls
+ * as 1 does.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int type;                     /* COMPKV_INT8 or COMPKV_E4M3                        */
+  float *kscale;                /* fp32 [num_layers * rows_per_layer], 16-byte       */
+  float *vscale;                /* aligned                                           */
+  void  *tail;                  /* bf16 [num_layers][B][Hkv][2][2][16][d], 16-byte   */
+                                /* aligned: K and V of two blocks                    */
+  int   *tail_len;              /* int32 [num_layers][B][Hkv][2]: the tokens up to   */
+                                /* the last one there; zeroed by compkv_init_kv8     */
+} compkv_kv8;
+
+/* Bytes of device scratch of a context whose cache is in 8 bits; 0 on a bad config. */
+size_t compkv_scratch_bytes_kv8(const compkv_config *cfg);
+
+/* compkv_init for a cache in 8 bits: bufs->k and bufs->v are its codes, one byte
+ * each, [num_layers * rows_per_layer][16][d], and all of its buffers are device
+ * memory. */
+compkv_status compkv_init_kv8(const compkv_config *cfg, const compkv_buffers *bufs, const compkv_kv8 *kv8,
+                              compkv_ctx **out);
+
+/* Tokens read back, packed sequence after sequence: slots [starts[s], starts[s]
+ * + counts[s]) of sequence s (host int32 [B]; starts NULL: from slot 0) become k, v:
+ * device [tokens][Hkv][d] of `type` (COMPKV_BF16 or COMPKV_F32), 32-byte aligned.
+ * Codes times scale, rounded once to fp32 and from there to bf16.  Slots behind
+ * a sequence's tokens raise COMPKV_ERR_INVALID_ARG in the device status, and
+ * their rows of k and v are left as they were.  Takes caches in bf16 too, in
+ * either placement. */
+compkv_status compkv_read(compkv_ctx *ctx, int layer, const int *starts, const int *counts, int type, void *k, void *v,
+                          void *stream);
+
+/* Exact attention of every sequence's query token over all tokens that the
+ * sequence holds, in a cache of 8 bits:
+ *     out = sum_j e^(z_j) v_j / sum_j e^(z_j),   z_j = q . k_j / sqrt(d).
+ * q and out: device [B][Hq][d], both of `type` (COMPKV_BF16 or COMPKV_F32).
+ * Queries and softmax weights enter the products to 22 bits, sums are fp32.  The
+ * rows of a sequence without tokens are zero.  (In bf16, compkv_attend_shared
+ * without a prefix is the same attention.) */
+compkv_status compkv_attend_all(compkv_ctx *ctx, int layer, const void *q, int type, void *out, void *stream);
+
 /* Synchronise `stream`, read and clear the device status word.  Returns
  * COMPKV_OK or the first device-side error since the last call. */
 compkv_status compkv_device_status(compkv_ctx *ctx, void *stream);
@@ -377,7 +449,7 @@ int64_t compkv_launch_count(const compkv_ctx *ctx);
  * last read (then resets them).  Families COMPKV_KERNEL_PREFILL, _APPEND,
  * _SCORE, _ATTEND and _DECODE time whole API calls (compkv_prefill,
  * compkv_append, compkv_score_select, compkv_attend, compkv_decode), and so do
- * _ROPE, _PREFILL_QKV, _FORK, _COMPACT and _ATTEND_SHARED.  A
+ * _ROPE, _PREFILL_QKV, _FORK, _COMPACT, _ATTEND_SHARED, _READ and _ATTEND_ALL.  A
  * score/select, attend or decode call launches two kernels, each timed on its
  * own (enable = 2) under COMPKV_KERNEL_K_STREAM (append, and the stream over
  * every block summary: zbar, sigma2, the logsumexp parts and the compensation
@@ -398,7 +470,9 @@ enum {
   COMPKV_KERNEL_FORK = 10,
   COMPKV_KERNEL_COMPACT = 11,
   COMPKV_KERNEL_ATTEND_SHARED = 12,
-  COMPKV_KERNEL_FAMILIES = 13
+  COMPKV_KERNEL_READ = 13,
+  COMPKV_KERNEL_ATTEND_ALL = 14,
+  COMPKV_KERNEL_FAMILIES = 15
 };
 compkv_status compkv_profile_enable(compkv_ctx *ctx, int enable);
 
