@@ -120,7 +120,7 @@ compkv_status make_layout(const compkv_config* c, Layout* L) {
   region(&L->off_hout, (size_t)L->units * G * d * sizeof(float));
   L->total = off;
   region(&L->off_arrive8, (size_t)L->units * sizeof(int));
-  region(&L->off_parts8, attend8_parts(G, d));
+  region(&L->off_parts8, (size_t)attend8_parts() * G * (d + 2) * sizeof(float));
   L->total8 = off;
   return COMPKV_OK;
 }
@@ -450,7 +450,7 @@ Attend8Args attend8_args(const compkv_ctx* c, int layer, const void* q, bool q_b
   a.q = q;
   a.out = out;
   a.acc = reinterpret_cast<float*>(sc + c->lay.off_parts8);
-  a.ml = reinterpret_cast<float2*>(a.acc + (size_t)2 * kMaxAttend8Ctas * c->cfg.group_size * c->cfg.head_dim);
+  a.ml = reinterpret_cast<float2*>(a.acc + attend8_parts() * c->cfg.group_size * c->cfg.head_dim);
   a.arrive = reinterpret_cast<int*>(sc + c->lay.off_arrive8);
   a.status = reinterpret_cast<int*>(sc + c->lay.off_status);
   a.q_bf16 = q_bf16;

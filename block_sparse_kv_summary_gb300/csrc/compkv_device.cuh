@@ -160,9 +160,9 @@ struct Attend8Args {
   const int* seq_len;          // [B] of this layer
   const void* q;               // [B][Hq][d] fp32, or bf16 where q_bf16
   void* out;                   // the same type
-  float* acc;                  // partial outputs [2 P][G][d], two of every CTA
+  float* acc;                  // segments' outputs [2 P][G][d]: the first and the last of every CTA
   float2* ml;                  // [2 P][G]: reference of their weights (log2 units) and the weights' sum
-  int* arrive;                 // [units] CTAs that have left their parts of a unit (zero between calls)
+  int* arrive;                 // [units] segments of a unit that have been left (zero between calls)
   int* status;
   int q_bf16;
   int B, Hkv, G, d;

@@ -38,7 +38,7 @@ cudaError_t launch_rope_prefill(const RopePrefillArgs& a, int sms, cudaStream_t 
 cudaError_t launch_append8(const LayerArgs& a, const Kv8Args& kv8, cudaStream_t st);
 cudaError_t launch_read(const ReadArgs& a, cudaStream_t st);
 constexpr int kMaxAttend8Ctas = 160;
-inline size_t attend8_parts(int G, int d) { return (size_t)2 * kMaxAttend8Ctas * G * (d + 2) * 4; }
+inline int64_t attend8_parts() { return (int64_t)2 * kMaxAttend8Ctas; }
 cudaError_t prepare_attend8(int d);
 cudaError_t launch_attend8(const Attend8Args& a, cudaStream_t st);
 // Pages: copies between sequences, and listed blocks to the front of a sequence.

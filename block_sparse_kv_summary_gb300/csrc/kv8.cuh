@@ -6,8 +6,8 @@
 //
 // each operation rounded once, and everything zero where m < 2^-100: there the
 // quotients leave the normal numbers, and no logit or output notices.  A block
-// with an infinity or a NaN has that as its scale and codes of zero, so that
-// all of it reads as NaN.
+// with an infinity or a NaN has a scale of NaN and codes of zero, so that all of
+// it reads as NaN.
 //
 // int8 spaces its values evenly below m, which suits coordinates of one size;
 // e4m3 keeps four bits of each value, which suits blocks whose coordinates
@@ -60,7 +60,7 @@ struct Scale {
     const float m = __uint_as_float(bits);
     Scale s = {__fdiv_rn(m, Codes<KV>::most), __fdiv_rn(Codes<KV>::most, m)};
     if (m < 0x1p-100f) s = {0.f, 0.f};
-    if (bits >= 0x7f800000u) s.inv = 0.f;
+    if (bits >= 0x7f800000u) s = {__uint_as_float(0x7fffffffu), 0.f};
     return s;
   }
 };

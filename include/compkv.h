@@ -376,9 +376,7 @@ compkv_status compkv_attend_shared(compkv_ctx *ctx, int layer, const void *q, in
  * them in that block come from their codes, rounded to bf16.  Summaries are
  * those of the tokens in bf16.  Codes, scales and tail are written by these
  * calls; a caller that fills codes and scales itself (with kbar, vbar, dbar and
- * seq_len) does so before any call wrote to the sequence, and with codes that
- * are numbers (the two NaN codes of e4m3 are never written and mean nothing
- * here).
+ * seq_len) does so before any call wrote to the sequence.
  *
  * A context of such a cache takes compkv_rope, compkv_prefill_qkv,
  * compkv_append, compkv_score_select, compkv_attend, compkv_decode,
@@ -420,7 +418,9 @@ compkv_status compkv_read(compkv_ctx *ctx, int layer, const int *starts, const i
  * sequence holds, in a cache of 8 bits:
  *     out = sum_j e^(z_j) v_j / sum_j e^(z_j),   z_j = q . k_j / sqrt(d).
  * q and out: device [B][Hq][d], both of `type` (COMPKV_BF16 or COMPKV_F32).
- * Queries and softmax weights enter the products to 22 bits, sums are fp32.  The
+ * Queries and softmax weights enter the products to 22 bits, sums are fp32.
+ * Logits, and a query's largest coordinate times a block's largest one, are
+ * below 2^100 (so too in compkv_attend and compkv_decode on such a cache).  The
  * rows of a sequence without tokens are zero.  (In bf16, compkv_attend_shared
  * without a prefix is the same attention.) */
 compkv_status compkv_attend_all(compkv_ctx *ctx, int layer, const void *q, int type, void *out, void *stream);
