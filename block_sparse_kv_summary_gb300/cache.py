@@ -83,8 +83,8 @@ class CompKVCache:
             units = num_layers * batch * num_kv_heads
             self.kscale = torch.zeros((total,), dtype=torch.float32, device=dev)
             self.vscale = torch.zeros((total,), dtype=torch.float32, device=dev)
-            self.tail = torch.zeros((units, 2, 2, BLOCK, head_dim), dtype=torch.bfloat16, device=dev)
-            self.tail_len = torch.zeros((units, 2), dtype=torch.int32, device=dev)
+            self.tail = torch.zeros((units, 3, 2, BLOCK, head_dim), dtype=torch.bfloat16, device=dev)
+            self.tail_len = torch.zeros((units, 3), dtype=torch.int32, device=dev)
             kv8 = C.compkv_kv8(_KV8_TYPES[kv_dtype], self.kscale.data_ptr(), self.vscale.data_ptr(), self.tail.data_ptr(),
                                self.tail_len.data_ptr())
         nbytes = C.compkv_scratch_bytes(self.cfg) if kv8 is None else C.compkv_scratch_bytes_kv8(self.cfg)

@@ -337,8 +337,8 @@ Kv8Args kv8_args(const compkv_ctx* c, int layer) {
   a.v = reinterpret_cast<uint8_t*>(c->buf.v) + rows * block;
   a.kscale = c->kv8.kscale + rows;
   a.vscale = c->kv8.vscale + rows;
-  a.tail = reinterpret_cast<__nv_bfloat16*>(c->kv8.tail) + units * 4 * block;
-  a.tail_len = c->kv8.tail_len + units * 2;
+  a.tail = reinterpret_cast<__nv_bfloat16*>(c->kv8.tail) + units * 6 * block;
+  a.tail_len = c->kv8.tail_len + units * 3;
   return a;
 }
 
@@ -675,7 +675,7 @@ compkv_status init_context(const compkv_config* cfg, const compkv_buffers* bufs,
     return cuda_status(e, "setting the kernels' attributes");
   }
   e = cudaMemsetAsync(bufs->scratch, 0, scratch, 0);
-  if (kv8 && e == cudaSuccess) e = cudaMemsetAsync(kv8->tail_len, 0, (size_t)cfg->num_layers * L.units * 2 * sizeof(int), 0);
+  if (kv8 && e == cudaSuccess) e = cudaMemsetAsync(kv8->tail_len, 0, (size_t)cfg->num_layers * L.units * 3 * sizeof(int), 0);
   if (e == cudaSuccess) e = cudaStreamSynchronize(0);
   if (e != cudaSuccess) {
     delete c;

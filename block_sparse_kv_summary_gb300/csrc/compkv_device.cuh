@@ -95,9 +95,9 @@ struct Kv8Args {
   uint8_t* v;
   float* kscale;               // [rows]
   float* vscale;
-  __nv_bfloat16* tail;         // [B][Hkv][2][K, V][16][d]: tokens of two blocks of each sequence as they came: the last
-                               // one, and the one that its last call of many tokens began in the middle of
-  int* tail_len;               // [B][Hkv][2]: the tokens up to the last one there (0: nothing is)
+  __nv_bfloat16* tail;         // [B][Hkv][3][K, V][16][d]: tokens of blocks of each sequence as they came: the last one
+                               // in place 0 or 2, the one that its last call of many tokens began inside in place 1
+  int* tail_len;               // [B][Hkv][3]: the tokens up to the last one there (0: nothing is)
   int type;                    // KvType
 };
 

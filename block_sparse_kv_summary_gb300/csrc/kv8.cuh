@@ -77,44 +77,47 @@ __device__ __forceinline__ void load_words(const __nv_bfloat16* p, uint32_t (&w)
 
 // A block's codes and scale from its tokens, by one warp; lane l holds the
 // coordinates [l D / 32, (l + 1) D / 32) of every token as bf16 pairs, zero
-// where the block has no token.
+// where the block has no token: first every token's part in the largest
+// magnitude, then its codes.
+template <int W>
+__device__ __forceinline__ uint32_t larger(uint32_t m, const uint32_t (&t)[W]) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) m = max(m, max(t[i] << 16 & 0x7fffffffu, t[i] & 0x7fff0000u));
+  return m;
+}
 template <int D, int KV>
-__device__ __forceinline__ void quantise_block(const uint32_t (&t)[kBlock][D / 64], uint8_t* codes, float* scale, int lane) {
+__device__ __forceinline__ void put_codes(uint8_t* row, const uint32_t (&t)[D / 64], Scale s, int lane) {
   constexpr int W = D / 64;
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < kBlock; ++j)
-#pragma unroll
-    for (int i = 0; i < W; ++i) m = max(m, max(t[j][i] << 16 & 0x7fffffffu, t[j][i] & 0x7fff0000u));
-  m = __reduce_max_sync(0xffffffffu, m);
-  const Scale s = Scale::of<KV>(m);
   // (an infinity times zero is a NaN: codes of such a block are set, not computed)
-  const uint32_t live = m < 0x7f800000u ? 0xffffffffu : 0u;
+  const uint32_t live = isnan(s.scale) ? 0u : 0xffffffffu;
+  float x[2 * W];
 #pragma unroll
-  for (int j = 0; j < kBlock; ++j) {
-    float x[2 * W];
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      x[2 * i] = __uint_as_float((t[j][i] & live) << 16) * s.inv;
-      x[2 * i + 1] = __uint_as_float(t[j][i] & live & 0xffff0000u) * s.inv;
-    }
-    if constexpr (W == 2)
-      reinterpret_cast<uint32_t*>(codes + j * D)[lane] = Codes<KV>::pack(x[0], x[1], x[2], x[3]);
-    else
-      reinterpret_cast<uint16_t*>(codes + j * D)[lane] = (uint16_t)Codes<KV>::pack(x[0], x[1], 0.f, 0.f);
+  for (int i = 0; i < W; ++i) {
+    x[2 * i] = __uint_as_float((t[i] & live) << 16) * s.inv;
+    x[2 * i + 1] = __uint_as_float(t[i] & live & 0xffff0000u) * s.inv;
   }
-  if (lane == 0) *scale = s.scale;
+  if constexpr (W == 2) reinterpret_cast<uint32_t*>(row)[lane] = Codes<KV>::pack(x[0], x[1], x[2], x[3]);
+  else reinterpret_cast<uint16_t*>(row)[lane] = (uint16_t)Codes<KV>::pack(x[0], x[1], 0.f, 0.f);
 }
 
-// The tail's tokens of block b of a unit, if it holds at least the first `lo` of them: K, with V behind it; else null.
-template <int D>
-__device__ __forceinline__ __nv_bfloat16* tail_of(const Kv8Args& c, int unit, int b, int lo) {
+// The tail.  A place that holds tokens of block b or of a later one goes out of date when block b is written; the writer
+// empties it.
+constexpr int kTails = 3;
+__device__ __forceinline__ bool tail_in(int len, int b) { return len > b * kBlock && len <= (b + 1) * kBlock; }  // the place is block b's
+// The place that holds at least the first `lo` tokens of block b of a unit (-1: none).
+__device__ __forceinline__ int tail_place(const Kv8Args& c, int unit, int b, int lo) {
+  int place = -1;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int len = __ldcg(c.tail_len + 2 * unit + i);
-    if (len > b * kBlock && len <= (b + 1) * kBlock && len - b * kBlock >= lo) return c.tail + (int64_t)(2 * unit + i) * 2 * kBlock * D;
+  for (int i = 0; i < kTails; ++i) {
+    const int len = __ldcg(c.tail_len + kTails * unit + i);
+    if (tail_in(len, b) && len - b * kBlock >= lo) place = i;
   }
-  return nullptr;
+  return place;
+}
+// The keys there; the values stand behind them.
+template <int D>
+__device__ __forceinline__ __nv_bfloat16* tail_at(const Kv8Args& c, int unit, int place) {
+  return c.tail + (int64_t)(kTails * unit + place) * 2 * kBlock * D;
 }
 
 }  // namespace compkv

@@ -24,9 +24,9 @@ __global__ void __launch_bounds__(256) append8_kernel(const __grid_constant__ La
   for (int h = threadIdx.x >> 5; fits && h < a.Hkv; h += blockDim.x >> 5) {
     const int64_t row = row_of(a, s, h, b);
     const int unit = s * a.Hkv + h;
-    const __nv_bfloat16* from = tail_of<D>(c, unit, b, slot);
-    __nv_bfloat16* to = c.tail + (int64_t)unit * 4 * kBlock * D;
-    const int other = __ldcg(c.tail_len + 2 * unit + 1);
+    const int place = tail_place(c, unit, b, slot), last = place == 2 ? 2 : 0;
+    const __nv_bfloat16* from = place < 0 ? nullptr : tail_at<D>(c, unit, place);
+    __nv_bfloat16* to = tail_at<D>(c, unit, last);
     __syncwarp();  // every lane has read the tail's lengths
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
@@ -58,11 +58,18 @@ __global__ void __launch_bounds__(256) append8_kernel(const __grid_constant__ La
 #pragma unroll
         for (int i = 0; i < W; ++i) reinterpret_cast<uint32_t*>(tail + j * D)[i] = t[j][i];
       }
-      quantise_block<D, KV>(t, codes, scale, lane);
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < kBlock; ++j) m = larger(m, t[j]);
+      const Scale q = Scale::of<KV>(__reduce_max_sync(0xffffffffu, m));
+#pragma unroll
+      for (int j = 0; j < kBlock; ++j) put_codes<D, KV>(codes + j * D, t[j], q, lane);
+      if (lane == 0) *scale = q.scale;
     }
-    if (lane == 0) {
-      c.tail_len[2 * unit] = L + 1;
-      if (other > b * kBlock) c.tail_len[2 * unit + 1] = 0;  // of this block, or behind it
+    if (lane < kTails) {
+      int* len = c.tail_len + kTails * unit + lane;
+      if (lane == last) *len = L + 1;
+      else if (*len > b * kBlock) *len = 0;
     }
     // (each lane reads back what it wrote itself)
     warp_block_summary<D>(to, to + kBlock * D, slot + 1, nullptr, nullptr, a.kbar + row * D, a.vbar + row * D, a.dbar + row * a.r, a.r, lane);

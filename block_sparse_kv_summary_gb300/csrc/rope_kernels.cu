@@ -412,22 +412,36 @@ __device__ __forceinline__ void tile_summary(const __nv_bfloat16* tile, int n, f
 }
 
 // Codes and scale of a block from its tokens in shared memory (zero behind the last one), by one warp; the tokens also
-// go to `tail`, unless it is null.
+// go to `tail`, unless it is null.  They are read twice: the registers hold four at a time beside the rest of the kernel.
 template <int D, int KV>
 __device__ __forceinline__ void tile_quantise(const __nv_bfloat16* tile, int n, uint8_t* codes, float* scale, __nv_bfloat16* tail, int lane) {
   constexpr int W = D / 64;
-  uint32_t t[kBlock][W];
+  auto token = [&](int j, uint32_t (&t)[W]) {
 #pragma unroll
-  for (int j = 0; j < kBlock; ++j)
-#pragma unroll
-    for (int i = 0; i < W; ++i) t[j][i] = reinterpret_cast<const uint32_t*>(tile + j * D)[lane * W + i];
-  quantise_block<D, KV>(t, codes, scale, lane);
-  if (!tail) return;
-#pragma unroll
+    for (int i = 0; i < W; ++i) t[i] = reinterpret_cast<const uint32_t*>(tile + j * D)[lane * W + i];
+  };
+  uint32_t m = 0;
+#pragma unroll 4
   for (int j = 0; j < kBlock; ++j) {
-    if (j >= n) break;
+    uint32_t t[W];
+    token(j, t);
+    m = larger(m, t);
+  }
+  const Scale s = Scale::of<KV>(__reduce_max_sync(0xffffffffu, m));
+#pragma unroll 4
+  for (int j = 0; j < kBlock; ++j) {
+    uint32_t t[W];
+    token(j, t);
+    put_codes<D, KV>(codes + j * D, t, s, lane);
+  }
+  if (lane == 0) *scale = s.scale;
+  if (!tail) return;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    uint32_t t[W];
+    token(j, t);
 #pragma unroll
-    for (int i = 0; i < W; ++i) reinterpret_cast<uint32_t*>(tail + j * D)[lane * W + i] = t[j][i];
+    for (int i = 0; i < W; ++i) reinterpret_cast<uint32_t*>(tail + j * D)[lane * W + i] = t[i];
   }
 }
 
@@ -457,122 +471,125 @@ __global__ void __launch_bounds__(256, 3) rope_prefill_kernel(const __grid_const
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int s = 0;
   while (s + 1 < a.B && g.item0[s + 1] <= (int)blockIdx.x) ++s;
-  int b = g.starts[s] / kBlock + ((int)blockIdx.x - g.item0[s]);
+  const int b = g.starts[s] / kBlock + ((int)blockIdx.x - g.item0[s]);
+  const int lo = max(g.starts[s] - b * kBlock, 0);                     // slots of this block that receive tokens:
+  const int hi = min(g.starts[s] + g.counts[s] - b * kBlock, kBlock);  // [lo, hi)
   const int kv0 = blockIdx.y * hc, kvn = min(hc, a.Hkv - kv0);
   if ((int)blockIdx.x == g.item0[s] && blockIdx.y == 0 && threadIdx.x == 0) a.seq_len[s] = g.starts[s] + g.counts[s];
-  const int last = (g.starts[s] + g.counts[s] - 1) / kBlock;
-  // In 8 bits, the tail that the first block's earlier tokens come from is the one that the last block's tokens
-  // replace: one CTA then does both, one after the other.
-  const bool both = KV != kKvBf16 && g.starts[s] % kBlock && last != g.starts[s] / kBlock;
-  if (both && b == last) return;
 
-#pragma unroll 1
-  for (;;) {
-    const int lo = max(g.starts[s] - b * kBlock, 0);                     // slots of this block that receive tokens:
-    const int hi = min(g.starts[s] + g.counts[s] - b * kBlock, kBlock);  // [lo, hi)
-    const int j = warp % WT * TPW + lane / LPH, team = warp / WT;  // this lane's token; warps of a team share heads
-    const bool live = j >= lo && j < hi;
-    const int64_t tok = (int64_t)g.token0[s] + b * kBlock - g.starts[s] + j;
-    const int pos = !live ? 0 : a.positions ? __ldg(a.positions + tok) : b * kBlock + j;
-    const float* row = table_row(a, pos, s, live && blockIdx.y == 0 && team == 0 && (lane & (LPH - 1)) == 0);
-    const Place at = place<D, INTER>(lane & (LPH - 1), a.rot);
-    const T* src = reinterpret_cast<const T*>(a.qkv) + tok * a.stride;
-    // the token's heads start on their way to L2 together; the batches below then wait for L2 alone
-    if (ahead && live && (lane & (LPH - 1)) == 0 && team == 0) {
-      const int G = a.Hq / a.Hkv;
-      prefetch_l2(src + (a.Hq + kv0) * D, kvn * D * sizeof(T));
-      prefetch_l2(src + (a.Hq + a.Hkv + kv0) * D, kvn * D * sizeof(T));
-      prefetch_l2(src + kv0 * G * D, kvn * G * D * sizeof(T));
-    }
+  const int j = warp % WT * TPW + lane / LPH, team = warp / WT;  // this lane's token; warps of a team share heads
+  const bool live = j >= lo && j < hi;
+  const int64_t tok = (int64_t)g.token0[s] + b * kBlock - g.starts[s] + j;
+  const int pos = !live ? 0 : a.positions ? __ldg(a.positions + tok) : b * kBlock + j;
+  const float* row = table_row(a, pos, s, live && blockIdx.y == 0 && team == 0 && (lane & (LPH - 1)) == 0);
+  const Place at = place<D, INTER>(lane & (LPH - 1), a.rot);
+  const T* src = reinterpret_cast<const T*>(a.qkv) + tok * a.stride;
+  // the token's heads start on their way to L2 together; the batches below then wait for L2 alone
+  if (ahead && live && (lane & (LPH - 1)) == 0 && team == 0) {
+    const int G = a.Hq / a.Hkv;
+    prefetch_l2(src + (a.Hq + kv0) * D, kvn * D * sizeof(T));
+    prefetch_l2(src + (a.Hq + a.Hkv + kv0) * D, kvn * D * sizeof(T));
+    prefetch_l2(src + kv0 * G * D, kvn * G * D * sizeof(T));
+  }
 
-    {
-      const int G = a.Hq / a.Hkv, nq = kvn * G;
-      const T* q = src + kv0 * G * D;
-      const int64_t out = (tok * a.Hq + kv0 * G) * D;
-      const Factors f = factors(weights<INTER>(a.q_weight, at), angles(row, a.rot, at));
-      for (int i0 = team; i0 < nq; i0 += kBatch * TEAMS) {
-        Raw<T> raw[kBatch];
+  {
+    const int G = a.Hq / a.Hkv, nq = kvn * G;
+    const T* q = src + kv0 * G * D;
+    const int64_t out = (tok * a.Hq + kv0 * G) * D;
+    const Factors f = factors(weights<INTER>(a.q_weight, at), angles(row, a.rot, at));
+    for (int i0 = team; i0 < nq; i0 += kBatch * TEAMS) {
+      Raw<T> raw[kBatch];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) raw[u].load(q + (i0 + u * TEAMS) * D, at, live && i0 + u * TEAMS < nq);
+      for (int u = 0; u < kBatch; ++u) raw[u].load(q + (i0 + u * TEAMS) * D, at, live && i0 + u * TEAMS < nq);
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          if (i0 + u * TEAMS >= nq) break;
-          Pairs y;
-          turn_head<D>(raw[u].template pairs<INTER>(), f, a.q_weight != nullptr, a.eps, y);
-          if (live) put_query<INTER>(a, out + (i0 + u * TEAMS) * D, at, y);
-        }
+      for (int u = 0; u < kBatch; ++u) {
+        if (i0 + u * TEAMS >= nq) break;
+        Pairs y;
+        turn_head<D>(raw[u].template pairs<INTER>(), f, a.q_weight != nullptr, a.eps, y);
+        if (live) put_query<INTER>(a, out + (i0 + u * TEAMS) * D, at, y);
       }
     }
-    {
-      const T* k = src + (a.Hq + kv0) * D;
-      const T* v = k + a.Hkv * D;
-      const Factors f = factors(weights<INTER>(a.k_weight, at), angles(row, a.rot, at));
-      const int64_t first = (g.seq_row0[s] + (int64_t)kv0 * g.cap_blocks[s] + b) * kBlock + j, step = (int64_t)g.cap_blocks[s] * kBlock;
+  }
+  {
+    const T* k = src + (a.Hq + kv0) * D;
+    const T* v = k + a.Hkv * D;
+    const Factors f = factors(weights<INTER>(a.k_weight, at), angles(row, a.rot, at));
+    const int64_t first = (g.seq_row0[s] + (int64_t)kv0 * g.cap_blocks[s] + b) * kBlock + j, step = (int64_t)g.cap_blocks[s] * kBlock;
 #pragma unroll 1
-      for (int h = team; h < kvn; h += TEAMS) {
-        Raw<T> rk, rv;
-        rk.load(k + h * D, at, live);
-        rv.load(v + h * D, at, live);
-        uint4 x = make_uint4(0, 0, 0, 0), y = x;
-        const int64_t slot = (first + h * step) * D;
+    for (int h = team; h < kvn; h += TEAMS) {
+      Raw<T> rk, rv;
+      rk.load(k + h * D, at, live);
+      rv.load(v + h * D, at, live);
+      uint4 x = make_uint4(0, 0, 0, 0), y = x;
+      const int64_t slot = (first + h * step) * D;
+      if constexpr (KV == kKvBf16) {
+        if (j < lo) {
+          const __nv_bfloat16 *kd = a.k + slot, *vd = a.v + slot;
+          const uint2 xa = __ldcg(reinterpret_cast<const uint2*>(kd + at.a)), xb = __ldcg(reinterpret_cast<const uint2*>(kd + at.b));
+          const uint2 ya = __ldcg(reinterpret_cast<const uint2*>(vd + at.a)), yb = __ldcg(reinterpret_cast<const uint2*>(vd + at.b));
+          x = make_uint4(xa.x, xa.y, xb.x, xb.y);
+          y = make_uint4(ya.x, ya.y, yb.x, yb.y);
+        }
+      } else if (j < lo) {
+        const int unit = s * a.Hkv + kv0 + h, place = tail_place(g.kv8, unit, b, lo);
+        if (place >= 0) {
+          const __nv_bfloat16 *kd = tail_at<D>(g.kv8, unit, place) + j * D, *vd = kd + kBlock * D;
+          const uint2 xa = __ldcg(reinterpret_cast<const uint2*>(kd + at.a)), xb = __ldcg(reinterpret_cast<const uint2*>(kd + at.b));
+          const uint2 ya = __ldcg(reinterpret_cast<const uint2*>(vd + at.a)), yb = __ldcg(reinterpret_cast<const uint2*>(vd + at.b));
+          x = make_uint4(xa.x, xa.y, xb.x, xb.y);
+          y = make_uint4(ya.x, ya.y, yb.x, yb.y);
+        } else {
+          x = dequantised<KV>(g.kv8.k + slot, at, __ldcg(g.kv8.kscale + slot / (kBlock * D)));
+          y = dequantised<KV>(g.kv8.v + slot, at, __ldcg(g.kv8.vscale + slot / (kBlock * D)));
+        }
+      }
+      const uint4 z = turn_key<D, INTER>(rk.template pairs<INTER>(), f, row, a, at);
+      if (live) {
+        x = z;
+        y = rv.bf16();
         if constexpr (KV == kKvBf16) {
-          if (j < lo) {
-            const __nv_bfloat16 *kd = a.k + slot, *vd = a.v + slot;
-            const uint2 xa = __ldcg(reinterpret_cast<const uint2*>(kd + at.a)), xb = __ldcg(reinterpret_cast<const uint2*>(kd + at.b));
-            const uint2 ya = __ldcg(reinterpret_cast<const uint2*>(vd + at.a)), yb = __ldcg(reinterpret_cast<const uint2*>(vd + at.b));
-            x = make_uint4(xa.x, xa.y, xb.x, xb.y);
-            y = make_uint4(ya.x, ya.y, yb.x, yb.y);
-          }
-        } else if (j < lo) {
-          if (const __nv_bfloat16* kd = tail_of<D>(g.kv8, s * a.Hkv + kv0 + h, b, lo)) {
-            kd += j * D;
-            const __nv_bfloat16* vd = kd + kBlock * D;
-            const uint2 xa = __ldcg(reinterpret_cast<const uint2*>(kd + at.a)), xb = __ldcg(reinterpret_cast<const uint2*>(kd + at.b));
-            const uint2 ya = __ldcg(reinterpret_cast<const uint2*>(vd + at.a)), yb = __ldcg(reinterpret_cast<const uint2*>(vd + at.b));
-            x = make_uint4(xa.x, xa.y, xb.x, xb.y);
-            y = make_uint4(ya.x, ya.y, yb.x, yb.y);
-          } else {
-            x = dequantised<KV>(g.kv8.k + slot, at, __ldcg(g.kv8.kscale + slot / (kBlock * D)));
-            y = dequantised<KV>(g.kv8.v + slot, at, __ldcg(g.kv8.vscale + slot / (kBlock * D)));
-          }
+          put(a.k + slot, at, x);
+          put(a.v + slot, at, y);
         }
-        const uint4 z = turn_key<D, INTER>(rk.template pairs<INTER>(), f, row, a, at);
-        if (live) {
-          x = z;
-          y = rv.bf16();
-          if constexpr (KV == kKvBf16) {
-            put(a.k + slot, at, x);
-            put(a.v + slot, at, y);
-          }
-        }
-        put(tiles + (h * kBlock + j) * D, at, x);
-        put(tiles + ((hc + h) * kBlock + j) * D, at, y);
       }
+      put(tiles + (h * kBlock + j) * D, at, x);
+      put(tiles + ((hc + h) * kBlock + j) * D, at, y);
     }
-    __syncthreads();
+  }
+  // The tail's place for this block's tokens.  The CTA of the call's last block takes 0 -- or 2, where the CTA of its first
+  // block may be reading 0, or the block already stands there -- and empties the other one if it holds a block behind the
+  // first; the CTA of the first block puts it into 1 if the call begins inside it, and empties what else holds it.
+  __shared__ int keep[4];
+  const int begin = g.starts[s] / kBlock, last = (g.starts[s] + g.counts[s] - 1) / kBlock;
+  int* len = KV == kKvBf16 ? nullptr : g.kv8.tail_len + kTails * (s * a.Hkv + kv0 + (int)threadIdx.x);
+  if (KV != kKvBf16 && threadIdx.x < kvn) {
+    const bool two = begin == last ? tail_in(__ldcg(len + 2), b) : tail_in(__ldcg(len), begin);
+    keep[threadIdx.x] = b == last ? (two ? 2 : 0) : b == begin && lo > 0 ? 1 : -1;
+  }
+  __syncthreads();
+  if (KV != kKvBf16 && threadIdx.x < kvn && (b == begin || b == last)) {
+    const int to = keep[threadIdx.x];
+#pragma unroll
+    for (int i = 0; i < kTails; ++i) {
+      const int had = __ldcg(len + i);
+      const bool gone = begin == last ? had > b * kBlock : b == last ? i == 2 - to && had > (begin + 1) * kBlock
+                                                         : i == 1 ? had > b * kBlock : tail_in(had, b);
+      if (i == to) len[i] = b * kBlock + hi;
+      else if (gone) len[i] = 0;
+    }
+  }
 #pragma unroll 1
-    for (int i = warp; i < 2 * kvn; i += 8) {
-      const bool is_k = i < kvn;
-      const int h = is_k ? i : i - kvn;
-      const int64_t r = g.seq_row0[s] + (int64_t)(kv0 + h) * g.cap_blocks[s] + b;
-      const __nv_bfloat16* tile = tiles + ((is_k ? 0 : hc) + h) * kBlock * D;
-      tile_summary<D>(tile, hi, (is_k ? a.kbar : a.vbar) + r * D, is_k ? a.dbar + r * a.r : nullptr, a.r, lane);
-      if constexpr (KV != kKvBf16) {
-        // the tail takes the last block, and the first one where the call begins inside it
-        const int place = 2 * (s * a.Hkv + kv0 + h) + (b != last);
-        const bool kept = b == last || lo > 0;
-        tile_quantise<D, KV>(tile, hi, (is_k ? g.kv8.k : g.kv8.v) + r * kBlock * D, (is_k ? g.kv8.kscale : g.kv8.vscale) + r,
-                             kept ? g.kv8.tail + (int64_t)(2 * place + !is_k) * kBlock * D : nullptr, lane);
-        if (is_k && lane == 0) {
-          if (kept) g.kv8.tail_len[place] = b * kBlock + hi;
-          // what else stands there of this block or behind it has been replaced
-          if (b == g.starts[s] / kBlock && !both && g.kv8.tail_len[place | 1] > b * kBlock) g.kv8.tail_len[place | 1] = 0;
-        }
-      }
+  for (int i = warp; i < 2 * kvn; i += 8) {
+    const bool is_k = i < kvn;
+    const int h = is_k ? i : i - kvn;
+    const int64_t r = g.seq_row0[s] + (int64_t)(kv0 + h) * g.cap_blocks[s] + b;
+    const __nv_bfloat16* tile = tiles + ((is_k ? 0 : hc) + h) * kBlock * D;
+    tile_summary<D>(tile, hi, (is_k ? a.kbar : a.vbar) + r * D, is_k ? a.dbar + r * a.r : nullptr, a.r, lane);
+    if constexpr (KV != kKvBf16) {
+      const int to = keep[h], unit = s * a.Hkv + kv0 + h;
+      tile_quantise<D, KV>(tile, hi, (is_k ? g.kv8.k : g.kv8.v) + r * kBlock * D, (is_k ? g.kv8.kscale : g.kv8.vscale) + r,
+                           to < 0 ? nullptr : tail_at<D>(g.kv8, unit, to) + (is_k ? 0 : kBlock * D), lane);
     }
-    if (KV == kKvBf16 || !both || b == last) break;
-    b = last;
-    __syncthreads();  // the tiles are read
   }
 }
 

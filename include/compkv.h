@@ -366,7 +366,7 @@ compkv_status compkv_attend_shared(compkv_ctx *ctx, int layer, const void *q, in
  * suits channels of very different size.  A block with an infinity or a NaN
  * among its tokens reads as NaN altogether.
  *
- * The tokens of two blocks of each sequence are kept in bf16 too (the tail): of its
+ * The tokens of some blocks of each sequence are kept in bf16 too (the tail): of its
  * last block, and of the block that the last compkv_prefill_qkv began in the
  * middle of.  A token that joins tokens of such a block quantises it afresh from
  * these, so that its codes are those of its tokens however they arrived, and
@@ -389,9 +389,9 @@ typedef struct {
   int type;                     /* COMPKV_INT8 or COMPKV_E4M3                        */
   float *kscale;                /* fp32 [num_layers * rows_per_layer], 16-byte       */
   float *vscale;                /* aligned                                           */
-  void  *tail;                  /* bf16 [num_layers][B][Hkv][2][2][16][d], 16-byte   */
-                                /* aligned: K and V of two blocks                    */
-  int   *tail_len;              /* int32 [num_layers][B][Hkv][2]: the tokens up to   */
+  void  *tail;                  /* bf16 [num_layers][B][Hkv][3][2][16][d], 16-byte   */
+                                /* aligned: K and V of three blocks                  */
+  int   *tail_len;              /* int32 [num_layers][B][Hkv][3]: the tokens up to   */
                                 /* the last one there; zeroed by compkv_init_kv8     */
 } compkv_kv8;
 

@@ -248,8 +248,11 @@ def test_a_cut_into_an_older_block_goes_on_from_its_codes(kv, append):
     write(c, [(cut, cut + 4)], 8, hkv, 4, d)
     tail = c.tail.clone()
     write(c, [(cut + 2, cut + 4)], 9, hkv, 4, d)
-    assert torch.equal(c.tail[:, 0, :, :cut - 14], tail[:, 0, :, :cut - 14])
-    assert not torch.equal(c.tail[:, 0, :, cut - 14:cut - 12], tail[:, 0, :, cut - 14:cut - 12])
+    unit = torch.arange(hkv, device="cuda")
+    place = (c.tail_len == cut + 4).int().argmax(1)
+    assert (c.tail_len[unit, place] == cut + 4).all()
+    assert torch.equal(c.tail[unit, place][:, :, :cut - 14], tail[unit, place][:, :, :cut - 14])
+    assert not torch.equal(c.tail[unit, place][:, :, cut - 14:cut - 12], tail[unit, place][:, :, cut - 14:cut - 12])
 
 
 @pytest.mark.parametrize("kv", KV8)
@@ -280,7 +283,46 @@ def test_cuts_into_blocks_that_the_tail_holds(kv, append):
     both(70, 71, 9)     # block 4 goes on with other tokens
     both(71, 100, 10)
     both(64, 120, 11)   # block 4 from its start, with others again: what the tail had of it is gone
-    assert not (c8.tail_len[:, 1] > 64).any()
+    assert (c8.tail_len > 64).sum().item() == hkv and (c8.tail_len == 120).sum().item() == hkv
+    both(120, 121, 12)  # the last block goes on, wherever it stands
+    both(121, 127, 13)
+    both(127, 150, 14)  # from inside the last block into the next two
+    both(127, 160, 15)  # and again, longer
+    both(125, 126, 16)  # back into the block that the call began inside
+    both(16, 17, 17)    # far back, at a block's start
+
+
+def test_many_writes_keep_the_tail_in_order():
+    # random cuts and writes of two sequences: wherever the tail has the tokens in front, codes are those of the tokens in
+    # bf16; elsewhere the bf16 cache first takes over what the codes stand for
+    import random
+    rng = random.Random(5)
+    hkv, d, cap = 5, 64, 192
+    c8, c16 = make_cache([cap, cap], torch.int8, hkv=hkv, d=d), make_cache([cap, cap], torch.bfloat16, hkv=hkv, d=d)
+    lens = [0, 0]
+    for step in range(60):
+        span = []
+        for s in range(2):
+            a = lens[s] if rng.random() < 0.5 else rng.randrange(max(0, lens[s] - 40), lens[s] + 1)
+            span.append((a, min(cap, a + rng.choice([0, 1, 3, 16, 30, 50]))))
+        for s, (a, b) in enumerate(span):
+            if b > a and a % BLOCK:
+                held = c8.tail_len[s * hkv].tolist()
+                if not any(BLOCK * (a // BLOCK) < x <= BLOCK * (a // BLOCK + 1) and x >= a for x in held):
+                    vk, vv = values(c8)
+                    for h in range(hkv):
+                        r = c8.rows(0, s, h)[0] + a // BLOCK
+                        for t, x in ((c16.k, vk), (c16.v, vv)):
+                            t[r, :a % BLOCK] = x[r, :a % BLOCK].float().bfloat16()
+        for c in (c8, c16):
+            write(c, span, 1000 + step, hkv, 4, d)
+        lens = [b if b > a else n for (a, b), n in zip(span, lens)]
+        # (a block behind the end of a shorter write may be out of date in either cache: the first `lens` tokens count)
+        check_stored(c8, c16, lens)
+        if max(lens) > cap - 20:
+            for c in (c8, c16):
+                c.seq_len.fill_(0)
+            lens = [0, 0]
 
 
 @pytest.mark.parametrize("kv", KV8)
@@ -291,7 +333,8 @@ def test_a_call_again_stores_the_same(kv):
     held = None
     for _ in range(3):
         write(c, [(20, 41), (77, 300), (33, 40)], 2, hkv, 4, d)
-        now = [bits(t).clone() for t in (c.k, c.v, c.kscale, c.vscale, c.kbar, c.vbar, c.dbar, c.tail, c.tail_len)]
+        now = [bits(t).clone() for t in (c.k, c.v, c.kscale, c.vscale, c.kbar, c.vbar, c.dbar)]
+        now.append(c.tail_len.sort(1).values)  # (which place of the tail holds which block may change)
         assert held is None or all(torch.equal(a, b) for a, b in zip(held, now))
         held = now
 
