@@ -356,8 +356,18 @@ __global__ void __launch_bounds__(128) rope_step_kernel(const __grid_constant__ 
 // the first n tokens and, for keys, the grouped mean of the population
 // variances, both in two passes over registers and in the order of
 // warp_block_summary, with the same results.
-template <int D>
-__device__ __forceinline__ void tile_summary(const __nv_bfloat16* tile, int n, float* bar, float* dbar, int r, int lane) {
+// In 8 bits, the block's codes and scale too, from the same registers.
+struct TileCodes {
+  uint8_t* codes;
+  float* scale;
+};
+__device__ __forceinline__ float max_nan(float a, float b) {  // a NaN where either is one
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+template <int D, int KV>
+__device__ __forceinline__ void tile_summary(const __nv_bfloat16* tile, int n, float* bar, float* dbar, int r, TileCodes out, int lane) {
   constexpr int V = D / 32;
   float2 t[kBlock][V / 2], mean[V / 2] = {};
 #pragma unroll
@@ -376,6 +386,25 @@ __device__ __forceinline__ void tile_summary(const __nv_bfloat16* tile, int n, f
   for (int i = 0; i < V / 2; ++i) {
     mean[i] = make_float2(over(mean[i].x), over(mean[i].y));
     reinterpret_cast<float2*>(bar + lane * V)[i] = mean[i];
+  }
+  if constexpr (KV != kKvBf16) {
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < kBlock; ++j) {
+      if (j >= n) break;
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) m = max_nan(max_nan(fabsf(t[j][i].x), fabsf(t[j][i].y)), m);
+    }
+    const Scale s = Scale::of<KV>(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+    const bool live = !isnan(s.scale);  // (an infinity times zero is a NaN: codes of such a block are set, not computed)
+#pragma unroll
+    for (int j = 0; j < kBlock; ++j) {
+      uint32_t c = 0;
+      if (j < n && live) c = Codes<KV>::pack(t[j][0].x * s.inv, t[j][0].y * s.inv, V == 4 ? t[j][V / 2 - 1].x * s.inv : 0.f, V == 4 ? t[j][V / 2 - 1].y * s.inv : 0.f);
+      if constexpr (V == 4) reinterpret_cast<uint32_t*>(out.codes + j * D)[lane] = c;
+      else reinterpret_cast<uint16_t*>(out.codes + j * D)[lane] = (uint16_t)c;
+    }
+    if (lane == 0) *out.scale = s.scale;
   }
   if (!dbar) return;
   float2 v2[V / 2] = {};
@@ -408,40 +437,6 @@ __device__ __forceinline__ void tile_summary(const __nv_bfloat16* tile, int n, f
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) dbar[lane * V + i] = var[i];
-  }
-}
-
-// Codes and scale of a block from its tokens in shared memory (zero behind the last one), by one warp; the tokens also
-// go to `tail`, unless it is null.  They are read twice: the registers hold four at a time beside the rest of the kernel.
-template <int D, int KV>
-__device__ __forceinline__ void tile_quantise(const __nv_bfloat16* tile, int n, uint8_t* codes, float* scale, __nv_bfloat16* tail, int lane) {
-  constexpr int W = D / 64;
-  auto token = [&](int j, uint32_t (&t)[W]) {
-#pragma unroll
-    for (int i = 0; i < W; ++i) t[i] = reinterpret_cast<const uint32_t*>(tile + j * D)[lane * W + i];
-  };
-  uint32_t m = 0;
-#pragma unroll 4
-  for (int j = 0; j < kBlock; ++j) {
-    uint32_t t[W];
-    token(j, t);
-    m = larger(m, t);
-  }
-  const Scale s = Scale::of<KV>(__reduce_max_sync(0xffffffffu, m));
-#pragma unroll 4
-  for (int j = 0; j < kBlock; ++j) {
-    uint32_t t[W];
-    token(j, t);
-    put_codes<D, KV>(codes + j * D, t, s, lane);
-  }
-  if (lane == 0) *scale = s.scale;
-  if (!tail) return;
-#pragma unroll 1
-  for (int j = 0; j < n; ++j) {
-    uint32_t t[W];
-    token(j, t);
-#pragma unroll
-    for (int i = 0; i < W; ++i) reinterpret_cast<uint32_t*>(tail + j * D)[lane * W + i] = t[i];
   }
 }
 
@@ -584,11 +579,12 @@ __global__ void __launch_bounds__(256, 3) rope_prefill_kernel(const __grid_const
     const int h = is_k ? i : i - kvn;
     const int64_t r = g.seq_row0[s] + (int64_t)(kv0 + h) * g.cap_blocks[s] + b;
     const __nv_bfloat16* tile = tiles + ((is_k ? 0 : hc) + h) * kBlock * D;
-    tile_summary<D>(tile, hi, (is_k ? a.kbar : a.vbar) + r * D, is_k ? a.dbar + r * a.r : nullptr, a.r, lane);
-    if constexpr (KV != kKvBf16) {
-      const int to = keep[h], unit = s * a.Hkv + kv0 + h;
-      tile_quantise<D, KV>(tile, hi, (is_k ? g.kv8.k : g.kv8.v) + r * kBlock * D, (is_k ? g.kv8.kscale : g.kv8.vscale) + r,
-                           to < 0 ? nullptr : tail_at<D>(g.kv8, unit, to) + (is_k ? 0 : kBlock * D), lane);
+    tile_summary<D, KV>(tile, hi, (is_k ? a.kbar : a.vbar) + r * D, is_k ? a.dbar + r * a.r : nullptr, a.r,
+                        {(is_k ? g.kv8.k : g.kv8.v) + r * kBlock * D, (is_k ? g.kv8.kscale : g.kv8.vscale) + r}, lane);
+    if (KV != kKvBf16 && keep[h] >= 0) {
+      uint32_t* to = reinterpret_cast<uint32_t*>(tail_at<D>(g.kv8, s * a.Hkv + kv0 + h, keep[h]) + (is_k ? 0 : kBlock * D));
+#pragma unroll 4
+      for (int x = lane; x < hi * (D / 2); x += 32) to[x] = reinterpret_cast<const uint32_t*>(tile)[x];
     }
   }
 }
