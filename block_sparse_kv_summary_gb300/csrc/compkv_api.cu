@@ -670,6 +670,7 @@ compkv_status init_context(const compkv_config* cfg, const compkv_buffers* bufs,
   if (e == cudaSuccess) e = prepare_post(cfg->head_dim, cfg->group_size, L.C, L.bpc_max, L.K);
   if (e == cudaSuccess) e = prepare_pages(cfg->head_dim);
   if (e == cudaSuccess) e = kv8 ? prepare_attend8(cfg->head_dim) : prepare_shared(cfg->head_dim);
+  if (kv8 && e == cudaSuccess) e = prepare_append8(cfg->head_dim);
   if (e != cudaSuccess) {
     delete c;
     return cuda_status(e, "setting the kernels' attributes");

@@ -35,6 +35,7 @@ cudaError_t launch_rope_step(const RopeArgs& a, cudaStream_t st);
 cudaError_t launch_rope_prefill(const RopePrefillArgs& a, int sms, cudaStream_t st);
 // A cache in 8 bits: one token per sequence appended, tokens read back (from bf16 caches too), and attention over all
 // tokens or over a selection.
+cudaError_t prepare_append8(int d);
 cudaError_t launch_append8(const LayerArgs& a, const Kv8Args& kv8, cudaStream_t st);
 cudaError_t launch_read(const ReadArgs& a, cudaStream_t st);
 constexpr int kMaxAttend8Ctas = 160;

@@ -65,41 +65,6 @@ struct Scale {
   }
 };
 
-// D / 32 consecutive coordinates of a token from a lane's registers.
-__device__ __forceinline__ void load_words(const __nv_bfloat16* p, uint32_t (&w)[2]) {
-  const uint2 x = __ldcg(reinterpret_cast<const uint2*>(p));
-  w[0] = x.x;
-  w[1] = x.y;
-}
-__device__ __forceinline__ void load_words(const __nv_bfloat16* p, uint32_t (&w)[1]) {
-  w[0] = __ldcg(reinterpret_cast<const uint32_t*>(p));
-}
-
-// A block's codes and scale from its tokens, by one warp; lane l holds the
-// coordinates [l D / 32, (l + 1) D / 32) of every token as bf16 pairs, zero
-// where the block has no token: first every token's part in the largest
-// magnitude, then its codes.
-template <int W>
-__device__ __forceinline__ uint32_t larger(uint32_t m, const uint32_t (&t)[W]) {
-#pragma unroll
-  for (int i = 0; i < W; ++i) m = max(m, max(t[i] << 16 & 0x7fffffffu, t[i] & 0x7fff0000u));
-  return m;
-}
-template <int D, int KV>
-__device__ __forceinline__ void put_codes(uint8_t* row, const uint32_t (&t)[D / 64], Scale s, int lane) {
-  constexpr int W = D / 64;
-  // (an infinity times zero is a NaN: codes of such a block are set, not computed)
-  const uint32_t live = isnan(s.scale) ? 0u : 0xffffffffu;
-  float x[2 * W];
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    x[2 * i] = __uint_as_float((t[i] & live) << 16) * s.inv;
-    x[2 * i + 1] = __uint_as_float(t[i] & live & 0xffff0000u) * s.inv;
-  }
-  if constexpr (W == 2) reinterpret_cast<uint32_t*>(row)[lane] = Codes<KV>::pack(x[0], x[1], x[2], x[3]);
-  else reinterpret_cast<uint16_t*>(row)[lane] = (uint16_t)Codes<KV>::pack(x[0], x[1], 0.f, 0.f);
-}
-
 // The tail.  A place that holds tokens of block b or of a later one goes out of date when block b is written; the writer
 // empties it.
 constexpr int kTails = 3;

@@ -509,7 +509,10 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
   // stream of a given selection, all of these are older than the stream, which waited for them before it let this
   // kernel start: only its records have to be waited for, and copies and queries come first.
   const bool early = SPARSE && !a.selects;
-  if (!early) pdl_wait();
+  if (!early) {
+    pdl_wait();
+    pdl_trigger();  // the next call's kernels may launch (they wait for this grid before reading)
+  }
   if (warp == 0) {
     // the row of stages, from the lengths; in a short row every unit begins a run of its own
     int st[kMaxBatch / 32], sum = 0, padded = 0;
@@ -664,7 +667,10 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
       valid = __reduce_add_sync(0xffffffffu, valid);
       if (lane == 0 && valid) atomicAdd(&sm.valid, valid);
       if (__any_sync(0xffffffffu, wrong) && lane == 0 && (int)blockIdx.x == c0) set_error(a.status, kDevBadSelection, s, h, 61);
-      if (!waited) pdl_wait();
+      if (!waited) {
+        pdl_wait();
+        pdl_trigger();
+      }
       waited = true;
       if (!a.no_comp) {
         const int nseg = (sm.streamed[s] + sm.seg - 1) / sm.seg;

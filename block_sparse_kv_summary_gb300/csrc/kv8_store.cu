@@ -1,78 +1,92 @@
 // A cache in 8 bits: one token per sequence appended, and tokens read back
 // (also from a cache in bf16).  Many tokens are written by rope_kernels.cu.
-#include "block_summary.cuh"
 #include "compkv_launch.h"
 #include "kv8.cuh"
+#include "tile_summary.cuh"
 
 namespace compkv {
 
 namespace {
 
-// One CTA per sequence, a warp per KV head at a time.  Token L (L = seq_len)
-// joins the tokens of its block, which the tail holds in bf16; the block's
-// summary and codes are formed again from all of them, so that a block's
-// contents do not depend on how its tokens arrived.  Where the sequence was
-// cut back into an older block, the tokens in front come from their codes.
-// Bound by latency: length, tail and codes in a row.
+// One CTA per sequence, a warp for K and one for V of eight heads at a time.
+// Token L (L = seq_len) joins the tokens of its block, which the tail holds in
+// bf16; the block's summary and codes are formed again from all of them, so that
+// a block's contents do not depend on how its tokens arrived.  Where the
+// sequence was cut back into an older block, the tokens in front come from their
+// codes.  Bound by latency: length, tail, and the block's arithmetic in a row.
+constexpr int kAppendHeads = 8;
+constexpr int append8_smem(int d, int heads) { return heads * 2 * kBlock * d * 2; }
 template <int D, int KV>
-__global__ void __launch_bounds__(256) append8_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ Kv8Args c) {
-  constexpr int V = D / 32, W = D / 64;
-  const int s = blockIdx.x, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(64 * kAppendHeads) append8_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ Kv8Args c) {
+  constexpr int V = D / 32, W = D / 64, CH = D / 8;  // coordinates of a lane, their words; 16-byte chunks of a token
+  extern __shared__ __align__(16) __nv_bfloat16 tiles[];  // [head][K, V][16][D]
+  pdl_wait();     // what came before on the stream may have written the cache and the token
+  pdl_trigger();  // the kernels of this step may launch (they wait for this grid before reading)
+  const int s = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kv = warp & 1;
   const int L = __ldcg(a.seq_len + s);
   const bool fits = L >= 0 && L < a.cap_blocks[s] * kBlock;
   const int b = L / kBlock, slot = L % kBlock;
-  for (int h = threadIdx.x >> 5; fits && h < a.Hkv; h += blockDim.x >> 5) {
-    const int64_t row = row_of(a, s, h, b);
-    const int unit = s * a.Hkv + h;
+  __nv_bfloat16* tile = tiles + warp * kBlock * D;
+  for (int h0 = 0; fits && h0 < a.Hkv; h0 += kAppendHeads) {
+    const int h = h0 + (warp >> 1);
+    const bool mine = h < a.Hkv;
+    const int64_t row = row_of(a, s, mine ? h : 0, b);
+    const int unit = s * a.Hkv + (mine ? h : 0);
     const int place = tail_place(c, unit, b, slot), last = place == 2 ? 2 : 0;
-    const __nv_bfloat16* from = place < 0 ? nullptr : tail_at<D>(c, unit, place);
-    __nv_bfloat16* to = tail_at<D>(c, unit, last);
-    __syncwarp();  // every lane has read the tail's lengths
+    uint8_t* codes = (kv ? c.v : c.k) + row * kBlock * D;
+    float* scale = (kv ? c.vscale : c.kscale) + row;
+    __nv_bfloat16* to = tail_at<D>(c, unit, last) + kv * kBlock * D;
+    if (mine) {
+      const __nv_bfloat16* token = (kv ? a.v_new : a.k_new) + (int64_t)unit * D;
+      if (slot == 0 || place >= 0) {
+        const uint4* from = reinterpret_cast<const uint4*>(tail_at<D>(c, unit, place < 0 ? 0 : place) + kv * kBlock * D);
+        uint4 x[CH / 2];
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      __nv_bfloat16* tail = to + kv * kBlock * D + lane * V;
-      uint8_t* codes = (kv ? c.v : c.k) + row * kBlock * D;
-      float* scale = (kv ? c.vscale : c.kscale) + row;
-      const __nv_bfloat16* token = (kv ? a.v_new : a.k_new) + (int64_t)unit * D + lane * V;
-      const float old = __ldcg(scale);
-      uint32_t t[kBlock][W];
-#pragma unroll
-      for (int j = 0; j < kBlock; ++j) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) t[j][i] = 0;
-        if (j > slot) continue;
-        if (j == slot) {
-          load_words(token, t[j]);
-        } else if (from) {
-          load_words(from + (kv * kBlock + j) * D + lane * V, t[j]);
-          if (from == to) continue;
-        } else {
-          const uint8_t* p = codes + j * D + lane * V;
-          const float4 x = Codes<KV>::unpack(W == 2 ? __ldcg(reinterpret_cast<const uint32_t*>(p)) : __ldcg(reinterpret_cast<const uint16_t*>(p)));
-#pragma unroll
-          for (int i = 0; i < W; ++i) {
-            const __nv_bfloat162 y = i ? __floats2bfloat162_rn(x.z * old, x.w * old) : __floats2bfloat162_rn(x.x * old, x.y * old);
-            t[j][i] = *reinterpret_cast<const uint32_t*>(&y);
-          }
+        for (int i = 0; i < CH / 2; ++i) {
+          const int at = i * 32 + lane, j = at / CH;  // chunk `at` of the block belongs to token j
+          x[i] = j > slot ? make_uint4(0, 0, 0, 0) : __ldcg(j == slot ? reinterpret_cast<const uint4*>(token) + at % CH : from + at);
         }
 #pragma unroll
-        for (int i = 0; i < W; ++i) reinterpret_cast<uint32_t*>(tail + j * D)[i] = t[j][i];
+        for (int i = 0; i < CH / 2; ++i) {
+          const int at = i * 32 + lane, j = at / CH;
+          reinterpret_cast<uint4*>(tile)[at] = x[i];
+          if (j == slot || (j < slot && place != last)) reinterpret_cast<uint4*>(to)[at] = x[i];
+        }
+      } else {
+        const float old = __ldcg(scale);
+#pragma unroll 1
+        for (int j = 0; j < kBlock; ++j) {
+          uint32_t t[W] = {};
+          if (j == slot) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) t[i] = __ldcg(reinterpret_cast<const uint32_t*>(token + lane * V) + i);
+          } else if (j < slot) {
+            const uint8_t* p = codes + j * D + lane * V;
+            const float4 x = Codes<KV>::unpack(W == 2 ? __ldcg(reinterpret_cast<const uint32_t*>(p)) : __ldcg(reinterpret_cast<const uint16_t*>(p)));
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+              const __nv_bfloat162 y = i ? __floats2bfloat162_rn(x.z * old, x.w * old) : __floats2bfloat162_rn(x.x * old, x.y * old);
+              t[i] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            reinterpret_cast<uint32_t*>(tile + j * D + lane * V)[i] = t[i];
+            if (j <= slot) reinterpret_cast<uint32_t*>(to + j * D + lane * V)[i] = t[i];
+          }
+        }
       }
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 0; j < kBlock; ++j) m = larger(m, t[j]);
-      const Scale q = Scale::of<KV>(__reduce_max_sync(0xffffffffu, m));
-#pragma unroll
-      for (int j = 0; j < kBlock; ++j) put_codes<D, KV>(codes + j * D, t[j], q, lane);
-      if (lane == 0) *scale = q.scale;
     }
-    if (lane < kTails) {
-      int* len = c.tail_len + kTails * unit + lane;
-      if (lane == last) *len = L + 1;
-      else if (*len > b * kBlock) *len = 0;
+    __syncthreads();  // every warp has read the tail's lengths
+    if (mine) {
+      tile_summary<D, KV>(tile, slot + 1, (kv ? a.vbar : a.kbar) + row * D, kv ? nullptr : a.dbar + row * a.r, a.r, {codes, scale}, lane);
+      if (!kv && lane < kTails) {
+        int* len = c.tail_len + kTails * unit + lane;
+        if (lane == last) *len = L + 1;
+        else if (*len > b * kBlock) *len = 0;
+      }
     }
-    // (each lane reads back what it wrote itself)
-    warp_block_summary<D>(to, to + kBlock * D, slot + 1, nullptr, nullptr, a.kbar + row * D, a.vbar + row * D, a.dbar + row * a.r, a.r, lane);
+    __syncthreads();  // (and the tiles are read)
   }
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -180,17 +194,37 @@ cudaError_t read_as(const ReadArgs& a, cudaStream_t st) {
 
 }  // namespace
 
+template <int D, int KV>
+static cudaError_t append8_as(const LayerArgs& a, const Kv8Args& c, cudaStream_t st) {
+  LayerArgs args = a;
+  Kv8Args codes = c;
+  void* argv[] = {&args, &codes};
+  const int heads = a.Hkv < kAppendHeads ? a.Hkv : kAppendHeads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.B);
+  cfg.blockDim = dim3(64 * heads);
+  cfg.dynamicSmemBytes = append8_smem(D, heads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&append8_kernel<D, KV>), argv);
+}
+
 cudaError_t launch_append8(const LayerArgs& a, const Kv8Args& c, cudaStream_t st) {
-  const int threads = 32 * (a.Hkv < 8 ? a.Hkv : 8);
   const bool i8 = c.type == kKvInt8;
-  if (a.d == 128) {
-    if (i8) append8_kernel<128, kKvInt8><<<a.B, threads, 0, st>>>(a, c);
-    else append8_kernel<128, kKvE4m3><<<a.B, threads, 0, st>>>(a, c);
-  } else {
-    if (i8) append8_kernel<64, kKvInt8><<<a.B, threads, 0, st>>>(a, c);
-    else append8_kernel<64, kKvE4m3><<<a.B, threads, 0, st>>>(a, c);
-  }
-  return cudaGetLastError();
+  if (a.d == 128) return i8 ? append8_as<128, kKvInt8>(a, c, st) : append8_as<128, kKvE4m3>(a, c, st);
+  return i8 ? append8_as<64, kKvInt8>(a, c, st) : append8_as<64, kKvE4m3>(a, c, st);
+}
+
+cudaError_t prepare_append8(int d) {
+  const int smem = append8_smem(d, kAppendHeads);
+  const void* fn[2] = {d == 128 ? reinterpret_cast<const void*>(&append8_kernel<128, kKvInt8>) : reinterpret_cast<const void*>(&append8_kernel<64, kKvInt8>),
+                       d == 128 ? reinterpret_cast<const void*>(&append8_kernel<128, kKvE4m3>) : reinterpret_cast<const void*>(&append8_kernel<64, kKvE4m3>)};
+  const cudaError_t e = raise_smem_limit(fn[0], smem);
+  return e == cudaSuccess ? raise_smem_limit(fn[1], smem) : e;
 }
 
 cudaError_t launch_read(const ReadArgs& a, cudaStream_t st) {
