@@ -25,10 +25,15 @@ struct Codes;
 template <>
 struct Codes<kKvInt8> {
   static constexpr float most = 127.f;
-  // four values (|x| <= 127 up to a rounding, which the nearest integer swallows)
-  static __device__ __forceinline__ uint32_t pack(float a, float b, float c, float d) {
-    const uint32_t lo = __byte_perm(__float2int_rn(a), __float2int_rn(b), 0x0040);
-    const uint32_t hi = __byte_perm(__float2int_rn(c), __float2int_rn(d), 0x0040);
+  // four values (|x| <= 127 up to a rounding, which the nearest integer swallows): added to 3 * 2^22, a value is rounded
+  // to the nearest integer, halfway cases to even, and stands in the low bits.  One by one: as pairs, ptxas makes one
+  // instruction of the addition and the product in front of it, which then rounds once where the definition rounds twice.
+  static __device__ __forceinline__ uint32_t pack(float2 a, float2 b) {
+    constexpr float magic = 12582912.f;
+    a = make_float2(__fadd_rn(a.x, magic), __fadd_rn(a.y, magic));
+    b = make_float2(__fadd_rn(b.x, magic), __fadd_rn(b.y, magic));
+    const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
     return __byte_perm(lo, hi, 0x5410);
   }
   static __device__ __forceinline__ float4 unpack(uint32_t w) {
@@ -39,9 +44,9 @@ struct Codes<kKvInt8> {
 template <>
 struct Codes<kKvE4m3> {
   static constexpr float most = 448.f;
-  static __device__ __forceinline__ uint32_t pack(float a, float b, float c, float d) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  static __device__ __forceinline__ uint32_t pack(float2 a, float2 b) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
     return lo | hi << 16;
   }
   static __device__ __forceinline__ float4 unpack(uint32_t w) {

@@ -454,11 +454,11 @@ __device__ __forceinline__ void join_segments(Smem8<D, SPARSE>& sm, const Attend
     float M = -INFINITY, S = 0.f;
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int k0 = group; k0 < C; k0 += 8 * groups) {
-      float2 e[8];
-      float4 v[8];
+    for (int k0 = group; k0 < C; k0 += 4 * groups) {
+      float2 e[4];
+      float4 v[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 4; ++j) {
         const int k = k0 + j * groups;
         const int64_t at = (int64_t)(2 * (c0 + k) + (k == 0 && tail)) * a.G + g;
         e[j] = k < C ? __ldcg(a.ml + at) : make_float2(-INFINITY, 0.f);
@@ -466,12 +466,12 @@ __device__ __forceinline__ void join_segments(Smem8<D, SPARSE>& sm, const Attend
       }
       float mn = M;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) mn = fmaxf(mn, e[j].x);
+      for (int j = 0; j < 4; ++j) mn = fmaxf(mn, e[j].x);
       const float fo = part_factor(M, mn);
       A = make_float4(A.x * fo, A.y * fo, A.z * fo, A.w * fo);
       S *= fo;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) add_part(A, S, v[j], e[j].y, part_factor(e[j].x, mn));
+      for (int j = 0; j < 4; ++j) add_part(A, S, v[j], e[j].y, part_factor(e[j].x, mn));
       M = mn;
     }
     if (groups == 1) {
@@ -511,7 +511,6 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
   const bool early = SPARSE && !a.selects;
   if (!early) {
     pdl_wait();
-    pdl_trigger();  // the next call's kernels may launch (they wait for this grid before reading)
   }
   if (warp == 0) {
     // the row of stages, from the lengths; in a short row every unit begins a run of its own
@@ -524,7 +523,6 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
         bool fits;
         const int L = call_tokens(__ldcg(a.seq_len + s), a.cap_blocks[s], false, &fits), n = ceil_blocks(L);
         sm.tokens[s] = L;
-        if (SPARSE) sm.streamed[s] = streamed_blocks(L, false, a.selects, a.K, false);
         st[k] = ((SPARSE ? min(n, a.K) : n) + kPair - 1) / kPair;
         sm.stages[s] = st[k];
       }
@@ -551,10 +549,14 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
       at += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) sm.first[a.B] = at;
-    if (SPARSE) {
-      __syncwarp();
-      plan_warp(sm.streamed, a.B, a.Hkv, a.stream_P, stage_blocks(a.r, a.G), sm.soff, &sm.seg, lane);
+  } else if (SPARSE && warp == 1) {
+    // the stream's plan
+    for (int s = lane; s < a.B; s += 32) {
+      bool fits;
+      sm.streamed[s] = streamed_blocks(call_tokens(__ldcg(a.seq_len + s), a.cap_blocks[s], false, &fits), false, a.selects, a.K, false);
     }
+    __syncwarp();
+    plan_warp(sm.streamed, a.B, a.Hkv, a.stream_P, stage_blocks(a.r, a.G), sm.soff, &sm.seg, lane);
   }
   __syncthreads();
   const int total = sm.first[a.B], per = run_stages(total, (int)gridDim.x, W);
@@ -669,7 +671,6 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
       if (__any_sync(0xffffffffu, wrong) && lane == 0 && (int)blockIdx.x == c0) set_error(a.status, kDevBadSelection, s, h, 61);
       if (!waited) {
         pdl_wait();
-        pdl_trigger();
       }
       waited = true;
       if (!a.no_comp) {
@@ -765,15 +766,14 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
     }
     if (C == 1) continue;
     // ---- whoever leaves the unit's last segment joins them
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
+    if (tid == 0) {  // (the barrier above orders the CTA's stores before this thread's fence)
+      __threadfence();
       sm.last = atomicAdd(a.arrive + unit, 1) == C - 1;
       if (sm.last) a.arrive[unit] = 0;
+      __threadfence();
     }
     __syncthreads();
     if (!sm.last) continue;
-    __threadfence();
     join_segments<D, KV>(sm, a, unit, c0, C, tail, tid);
   }
   if (!waited) pdl_wait();

@@ -15,15 +15,11 @@ struct TileCodes {
   uint8_t* codes;
   float* scale;
 };
-__device__ __forceinline__ float max_nan(float a, float b) {  // a NaN where either is one
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
 template <int D, int KV>
 __device__ __forceinline__ void tile_summary(const __nv_bfloat16* tile, int n, float* bar, float* dbar, int r, TileCodes out, int lane) {
   constexpr int V = D / 32;
   float2 t[kBlock][V / 2], mean[V / 2] = {};
+  __nv_bfloat162 most = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
   for (int j = 0; j < kBlock; ++j) {
     if (j >= n) break;
@@ -31,6 +27,7 @@ __device__ __forceinline__ void tile_summary(const __nv_bfloat16* tile, int n, f
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) {
       t[j][i] = make_float2(__uint_as_float(p[i] << 16), __uint_as_float(p[i] & 0xffff0000u));
+      if (KV != kKvBf16) most = __hmax2_nan(most, __habs2(*reinterpret_cast<const __nv_bfloat162*>(p + i)));
       mean[i] = __fadd2_rn(mean[i], t[j][i]);
     }
   }
@@ -42,19 +39,17 @@ __device__ __forceinline__ void tile_summary(const __nv_bfloat16* tile, int n, f
     reinterpret_cast<float2*>(bar + lane * V)[i] = mean[i];
   }
   if constexpr (KV != kKvBf16) {
-    float m = 0.f;
-#pragma unroll
-    for (int j = 0; j < kBlock; ++j) {
-      if (j >= n) break;
-#pragma unroll
-      for (int i = 0; i < V / 2; ++i) m = max_nan(max_nan(fabsf(t[j][i].x), fabsf(t[j][i].y)), m);
-    }
-    const Scale s = Scale::of<KV>(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+    const uint32_t m = *reinterpret_cast<const uint32_t*>(&most);  // (a NaN has the largest bits)
+    const Scale s = Scale::of<KV>(__reduce_max_sync(0xffffffffu, max(m << 16, m & 0xffff0000u)));
     const bool live = !isnan(s.scale);  // (an infinity times zero is a NaN: codes of such a block are set, not computed)
 #pragma unroll
     for (int j = 0; j < kBlock; ++j) {
       uint32_t c = 0;
-      if (j < n && live) c = Codes<KV>::pack(t[j][0].x * s.inv, t[j][0].y * s.inv, V == 4 ? t[j][V / 2 - 1].x * s.inv : 0.f, V == 4 ? t[j][V / 2 - 1].y * s.inv : 0.f);
+      if (j < n && live) {
+        const float2 x = t[j][0], y = t[j][V / 2 - 1];
+        c = Codes<KV>::pack(make_float2(__fmul_rn(x.x, s.inv), __fmul_rn(x.y, s.inv)),
+                            V == 4 ? make_float2(__fmul_rn(y.x, s.inv), __fmul_rn(y.y, s.inv)) : make_float2(0.f, 0.f));
+      }
       if constexpr (V == 4) reinterpret_cast<uint32_t*>(out.codes + j * D)[lane] = c;
       else reinterpret_cast<uint16_t*>(out.codes + j * D)[lane] = (uint16_t)c;
     }
