@@ -695,3 +695,55 @@ def test_a_conversation(kv):
     q = randn(99, 3, hkv * g, d)
     check(c, c.attend_all(1, q), 1, q, [20, 137, 50])
     assert c.seq_len[1].tolist() == [20, 137, 50] and c.device_status() == 0
+
+
+@pytest.mark.parametrize("kv", KV8)
+def test_far_into_a_large_cache(kv):
+    # the codes of the last layer start behind 4 GB: every call gives what it gives in a small cache
+    hkv, g, d, layers = 8, 4, 128, 34
+    big, small = make_cache([131072], kv, layers=layers, hkv=hkv, g=g, d=d), make_cache([1024], kv, hkv=hkv, g=g, d=d)
+    assert big.rows(layers - 1, 0, 0)[0] * BLOCK * d > 2 ** 32
+    got = []
+    for c, layer in ((big, layers - 1), (small, 0)):
+        q = write(c, [(0, 700)], 1, hkv, g, d, layer)
+        c.append(layer, *(randn(5 + i, 1, hkv, d, dtype=torch.bfloat16) for i in range(2)))
+        write(c, [(701, 760)], 2, hkv, g, d, layer)
+        q = randn(9, 1, hkv * g, d)
+        sel = c.new_sel()
+        out = c.decode(layer, q, *(randn(7 + i, 1, hkv, d, dtype=torch.bfloat16) for i in range(2)), sel=sel)
+        got.append([out, sel, *c.read(layer, None, [761]), c.attend_all(layer, q), c.attend(layer, q, sel)])
+        assert c.device_status() == 0
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert not big.k[:big.rows_per_layer].view(torch.int8).any()
+
+
+def test_wide_batches():
+    # 64 sequences of 32 heads: more units than CTAs, several heads of a sequence in one run, units without tokens
+    lens = [(s * 37) % 90 for s in range(64)]
+    c = make_cache([96] * 64, torch.int8, hkv=32, g=1, d=64)
+    fill(c, 4, lens)
+    q = randn(5, 64, 32, 64)
+    check(c, c.attend_all(0, q), 0, q, lens)
+    sel = selection(6, c, lens, 8)
+    sel[::3, :, 4:] = -1
+    check(c, c.attend(0, q, sel), 0, q, lens, sel)
+    assert c.device_status() == 0
+
+
+def test_queries_from_another_stream():
+    # queries written on another stream are waited for by the caller's events, as for any call
+    c = make_cache([2048], torch.float8_e4m3fn, hkv=4, d=128)
+    fill(c, 3, [2000])
+    side = torch.cuda.Stream()
+    q = randn(1, 1, 16, 128)
+    want = c.attend_all(0, q)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(side):
+            x = q.clone()
+            ready = side.record_event()
+        torch.cuda.current_stream().wait_event(ready)
+        assert torch.equal(c.attend_all(0, x), want)
+    with pytest.raises(ValueError):
+        c.attend_all(0, torch.stack([q, q], -1)[..., 0])
