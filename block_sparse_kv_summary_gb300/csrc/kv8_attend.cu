@@ -17,19 +17,17 @@
 // A stage.  Each warp has a ring of stages filled by tensor copies that it starts
 // itself, the scales of its blocks beside them, so that 192 KB are on their way
 // to a multiprocessor while another segment's queries are read or its parts
-// joined.  Codes become fp16, which holds them all: an int8 byte is
-// put behind the exponent of 1024 and 1152 taken off; e4m3 has an instruction
-// (16 x 64K tokens of 8 heads: 198 us; its bits shifted into place, 263).
+// joined.
 //
-// Scores are S = Q K^T on mma.sync (m16n8k16): rows 0..7 are the query heads'
-// high fp16 parts, rows 8..15 their low parts, so that one product has both;
-// the sum of rows r and r + 8 is q . c to the 22 bits of the two parts.  The 16
-// columns of a block share one scale.  Outputs are O^T = V^T P (rows:
-// coordinates, columns: heads), with the weights in high and low parts too:
-// weights are e^(z - m + 14 ln 2), which keeps their low parts normal numbers.
-// A block's product starts from zero and is added to the running output with the
-// block's scale in fp32: the tensor cores' accumulator truncates, and the scale
-// has to be applied anyway.
+// Products.  Codes become fp16, which holds them all.  Scores are S = Q K^T on
+// mma.sync (m16n8k16): rows 0..7 are the query heads' high fp16 parts, rows
+// 8..15 their low parts, so that one product has both; the sum of rows r and
+// r + 8 is q . c to the 22 bits of the two parts.  The 16 columns of a block
+// share one scale.  Outputs are O^T = V^T P (rows: coordinates, columns: heads),
+// with the weights in high and low parts too: weights are e^(z - m + 14 ln 2),
+// which keeps their low parts normal numbers.  A block's product is added to the
+// running output with the block's scale in fp32: the tensor cores' accumulator
+// truncates, and the scale has to be applied anyway.
 //
 // Which coordinate stands where inside a product is free, as long as both sides
 // agree: lane (r, c) = (lane / 4, lane % 4) takes the D / 4 coordinates from
@@ -38,6 +36,15 @@
 // conflicts.  mma.sync and not tcgen05: with at most 8 query rows a tile of 128
 // would be 1/16 full, and codes would have to go back to shared memory as fp16
 // between their copy and the product.
+//
+// Bound by DRAM for long rows, with the instructions that widen the codes close
+// behind: 64 sequences of up to 64K tokens of 8 heads, d 128 (4.4 GB of codes), 612
+// us, 7.2 TB/s; one of 128K 49 us, of which 5 pass before the first stage is there
+// and 8 between the first and the last CTA's end (some multiprocessors get a tenth
+// less of the memory's rate) and in the join; 1025 tokens of 2 heads 7 us.  Twelve
+// warps of two stages: with eight of three 707 us on the 64 sequences, with ten,
+// which leave two of the four schedulers a warp short, 787, with sixteen of single
+// blocks 706.
 #include <cuda_fp16.h>
 
 #include "compkv_launch.h"
@@ -60,13 +67,13 @@ struct Smem8 {
   static constexpr int kSlots = D == 128 ? 2 : 4;                // stages of a warp's ring
   static constexpr int kStage = 2 * kPair * kBlock * D;          // K blocks, then V blocks
   alignas(1024) uint8_t ring[kWarps][kSlots][kStage];
-  float vbar[SPARSE ? kWarps : 1][kSlots][kPair][D];  // mean values of a stage's blocks
+  float vbar[SPARSE ? kWarps : 1][kSlots][kPair][D];  // mean values of a stage's blocks (selections only)
   uint4 q[D / 16][32];                // A fragments of the queries (high, low, high, low)
-  float part[kWarps][kHeads][D];     // the warps' outputs of two heads; parts of a join
+  float part[kWarps][kHeads][D];      // the warps' outputs of two heads; parts of a join
   float comp[SPARSE ? kMaxG : 1][D];  // this segment's share of the compensation sums
   float scale[kWarps][kSlots][2 * kPair];
   int block[kWarps][kSlots][kPair];   // a stage's blocks (selections only)
-  float ref[kWarps + 1][kMaxG];      // references (log2) and sums of the parts; the last: compensation
+  float ref[kWarps + 1][kMaxG];       // references (log2) and sums of the parts; the last: compensation
   float sum[kWarps + 1][kMaxG];
   float qs[kMaxG];                    // factor of a head's scores
   float2 qb[kMaxG];                   // what the scores of its two parts start from
@@ -118,7 +125,9 @@ __device__ __forceinline__ void split_f16(float x, float y, uint32_t& hi, uint32
 
 // Four codes as two pairs of fp16, in units of kUnit and kBias too large: coordinates 0 and 1, then 2 and 3 (e4m3), or 0
 // and 2, then 1 and 3 (int8).  A byte on its own is a subnormal fp16 number, byte * 2^-24, so an int8 code takes no more
-// than being made unsigned and put in place; products start from what the bias of 128 makes of them.
+// than being made unsigned and put in place; products start from what the bias of 128 makes of them (64 sequences of up to
+// 64K tokens: 617 us; with the bias taken off each pair of codes by a subtraction, 675).  e4m3 has an instruction (16 x
+// 64K: 198 us; its bits shifted into place, 263).
 template <int KV>
 struct Wide {
   static constexpr float kUnit = KV == kKvInt8 ? 0x1p-24f : 1.f, kBias = KV == kKvInt8 ? 128.f : 0.f;

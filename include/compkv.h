@@ -364,7 +364,8 @@ compkv_status compkv_attend_shared(compkv_ctx *ctx, int layer, const void *q, in
  * every operation rounded once in fp32; both are zero where m < 2^-100.  int8
  * puts its values evenly below m; e4m3 keeps four significant bits of each, which
  * suits channels of very different size.  A block with an infinity or a NaN
- * among its tokens reads as NaN altogether.
+ * among its tokens reads as NaN altogether.  Codes behind the last token of a
+ * block that is written become zero.
  *
  * The tokens of some blocks of each sequence are kept in bf16 too (the tail): of its
  * last block, and of the block that the last compkv_prefill_qkv began in the
