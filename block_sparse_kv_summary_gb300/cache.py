@@ -96,6 +96,7 @@ class CompKVCache:
         self._shared_ws = None
         # shapes of a call's outputs, and of the rows of the projection that it reads
         self._q_shape, self._kv_shape = (batch, num_kv_heads * group_size, head_dim), (batch, num_kv_heads, head_dim)
+        self._sel_shape = (batch, num_kv_heads, self.K)
         self._width = (group_size + 2) * num_kv_heads * head_dim
         with torch.cuda.device(dev):
             self.ctx = C.compkv_init(self.cfg, self.bufs) if kv8 is None else C.compkv_init_kv8(self.cfg, self.bufs, kv8)
@@ -116,23 +117,25 @@ class CompKVCache:
         return self.kbar[r0:r0 + cap], self.dbar[r0:r0 + cap], self.vbar[r0:r0 + cap]
 
     # ------------------------------------------------------------------ checks
+    # (calls take microseconds, so their checks are written out for speed)
     def _t(self, t, name, dtype, shape):
-        if t.device != self.device or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        """Address of a contiguous tensor of this type and shape on the cache's device."""
+        if t.dtype is not dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
             raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {self.device}, "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
         return t.data_ptr()
 
     def _q(self, q):
-        return self._t(q, "q", torch.float32, (self.batch, self.Hkv * self.G, self.d))
+        return self._t(q, "q", torch.float32, self._q_shape)
 
     def _kv(self, t, name):
-        return self._t(t, name, torch.bfloat16, (self.batch, self.Hkv, self.d))
+        return self._t(t, name, torch.bfloat16, self._kv_shape)
 
     def new_sel(self):
-        return torch.empty((self.batch, self.Hkv, self.K), dtype=torch.int32, device=self.device)
+        return torch.empty(self._sel_shape, dtype=torch.int32, device=self.device)
 
     def new_out(self):
-        return torch.empty((self.batch, self.Hkv * self.G, self.d), dtype=torch.float32, device=self.device)
+        return torch.empty(self._q_shape, dtype=torch.float32, device=self.device)
 
     # ------------------------------------------------------------------ calls
     def prefill(self, layer, lens):
@@ -148,23 +151,23 @@ class CompKVCache:
         if scores is not None:
             sp = self._t(scores, "scores", torch.float32, (self.batch, self.Hkv, self.max_cap_blocks))
         C.compkv_score_select(self.ctx, layer, self._q(q),
-                              self._t(sel, "sel", torch.int32, (self.batch, self.Hkv, self.K)),
+                              self._t(sel, "sel", torch.int32, self._sel_shape),
                               sp, _stream(self.device))
         return sel
 
     def attend(self, layer, q, sel, out=None):
         out = self.new_out() if out is None else out
         C.compkv_attend(self.ctx, layer, self._q(q),
-                        self._t(sel, "sel", torch.int32, (self.batch, self.Hkv, self.K)),
-                        self._t(out, "out", torch.float32, (self.batch, self.Hkv * self.G, self.d)),
+                        self._t(sel, "sel", torch.int32, self._sel_shape),
+                        self._t(out, "out", torch.float32, self._q_shape),
                         _stream(self.device))
         return out
 
     def decode(self, layer, q, k_new, v_new, out=None, sel=None):
         out = self.new_out() if out is None else out
-        sp = 0 if sel is None else self._t(sel, "sel", torch.int32, (self.batch, self.Hkv, self.K))
+        sp = 0 if sel is None else self._t(sel, "sel", torch.int32, self._sel_shape)
         C.compkv_decode(self.ctx, layer, self._q(q), self._kv(k_new, "k_new"), self._kv(v_new, "v_new"),
-                        self._t(out, "out", torch.float32, (self.batch, self.Hkv * self.G, self.d)),
+                        self._t(out, "out", torch.float32, self._q_shape),
                         sp, _stream(self.device))
         return out
 
@@ -187,7 +190,6 @@ class CompKVCache:
         return out
 
     # ------------------------------------------------------------------ around the decode step
-    # (these calls take microseconds, so their checks are written out for speed)
     def _call(self, fn, *args):
         """A library call with the cache's device as the current one."""
         index = self._index
@@ -196,12 +198,6 @@ class CompKVCache:
         else:
             with torch.cuda.device(index):
                 fn(self.ctx, *args, _raw_stream(index))
-
-    def _is(self, t, name, dtype, shape):
-        """Address of a contiguous tensor of this type and shape."""
-        if t.dtype is not dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
-            self._t(t, name, dtype, shape)
-        return t.data_ptr()
 
     def _rope_args(self, qkv, tokens, table, q_weight, k_weight, eps, positions, interleaved, q_dtype):
         width, dev, d = self._width, self.device, (self.d,)
@@ -219,9 +215,9 @@ class CompKVCache:
             self._t(table, "table", torch.float32, table.shape)
         return C.compkv_rope_args(
             qkv.data_ptr(), _TYPES[qkv.dtype], stride[0] if tokens > 1 else width, table.data_ptr(), positions_rows, rot,
-            1 if interleaved else 0, None if q_weight is None else self._is(q_weight, "q_weight", torch.float32, d),
-            None if k_weight is None else self._is(k_weight, "k_weight", torch.float32, d), eps,
-            None if positions is None else self._is(positions, "positions", torch.int32, (tokens,)), _TYPES[q_dtype])
+            1 if interleaved else 0, None if q_weight is None else self._t(q_weight, "q_weight", torch.float32, d),
+            None if k_weight is None else self._t(k_weight, "k_weight", torch.float32, d), eps,
+            None if positions is None else self._t(positions, "positions", torch.int32, (tokens,)), _TYPES[q_dtype])
 
     def rope(self, layer, qkv, table, *, q_weight=None, k_weight=None, eps=1e-6, positions=None, interleaved=False,
              q_dtype=torch.float32, q=None, k_new=None, v_new=None):
@@ -234,15 +230,15 @@ class CompKVCache:
         if q is None:
             q = torch.empty(self._q_shape, dtype=q_dtype, device=self.device)
         else:
-            self._is(q, "q", q_dtype, self._q_shape)
+            self._t(q, "q", q_dtype, self._q_shape)
         if k_new is None:
             k_new = torch.empty(self._kv_shape, dtype=torch.bfloat16, device=self.device)
         else:
-            self._is(k_new, "k_new", torch.bfloat16, self._kv_shape)
+            self._t(k_new, "k_new", torch.bfloat16, self._kv_shape)
         if v_new is None:
             v_new = torch.empty_like(k_new)
         else:
-            self._is(v_new, "v_new", torch.bfloat16, self._kv_shape)
+            self._t(v_new, "v_new", torch.bfloat16, self._kv_shape)
         self._call(C.compkv_rope, layer, a, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr())
         return q, k_new, v_new
 
@@ -263,7 +259,7 @@ class CompKVCache:
         if q is None:
             q = torch.empty(shape, dtype=q_dtype, device=self.device)
         else:
-            self._is(q, "q", q_dtype, shape)
+            self._t(q, "q", q_dtype, shape)
         if tokens:
             self._call(C.compkv_prefill_qkv, layer, a, starts, counts, q.data_ptr())
         return q
@@ -296,7 +292,7 @@ class CompKVCache:
         src, dst, layer0, n = self._pairs(range(self.batch) if src is None else src, dst, layers)
         if keep.dim() != 4:
             raise ValueError(f"keep must be [layers, pairs, Hkv, blocks], got {tuple(keep.shape)}")
-        kp = self._is(keep, "keep", torch.int32, (n, len(src), self.Hkv, keep.shape[3]))
+        kp = self._t(keep, "keep", torch.int32, (n, len(src), self.Hkv, keep.shape[3]))
         self._call(C.compkv_compact, layer0, n, src, dst, kp, keep.shape[3])
 
     def shared_workspace(self):
@@ -319,11 +315,11 @@ class CompKVCache:
         dtype, shape = q.dtype, self._q_shape
         if dtype not in _TYPES:
             raise ValueError(f"q must be torch.float32 or torch.bfloat16, got {dtype}")
-        qp = self._is(q, "q", dtype, shape)
+        qp = self._t(q, "q", dtype, shape)
         if out is None:
             out = torch.empty_like(q)
         else:
-            self._is(out, "out", dtype, shape)
+            self._t(out, "out", dtype, shape)
         ws = self.shared_workspace()
         self._call(C.compkv_attend_shared, layer, qp, _TYPES[dtype], prefix_seq, prefix_len, out.data_ptr(),
                    ws.data_ptr(), ws.numel())
@@ -344,11 +340,11 @@ class CompKVCache:
         if k is None:
             k = torch.empty(shape, dtype=dtype, device=self.device)
         else:
-            self._is(k, "k", dtype, shape)
+            self._t(k, "k", dtype, shape)
         if v is None:
             v = torch.empty(shape, dtype=dtype, device=self.device)
         else:
-            self._is(v, "v", dtype, shape)
+            self._t(v, "v", dtype, shape)
         if shape[0]:
             self._call(C.compkv_read, layer, starts, counts, _TYPES[dtype], k.data_ptr(), v.data_ptr())
         return k, v
@@ -359,11 +355,11 @@ class CompKVCache:
         dtype, shape = q.dtype, self._q_shape
         if dtype not in _TYPES:
             raise ValueError(f"q must be torch.float32 or torch.bfloat16, got {dtype}")
-        qp = self._is(q, "q", dtype, shape)
+        qp = self._t(q, "q", dtype, shape)
         if out is None:
             out = torch.empty_like(q)
         else:
-            self._is(out, "out", dtype, shape)
+            self._t(out, "out", dtype, shape)
         self._call(C.compkv_attend_all, layer, qp, _TYPES[dtype], out.data_ptr())
         return out
 

@@ -185,7 +185,9 @@ def compkv_score_select(ctx, layer, q, sel, scores, stream):
 
 
 def compkv_attend(ctx, layer, q, sel, out, stream):
-    _check(lib().compkv_attend(ctx, layer, q, sel, out, stream), "compkv_attend")
+    st = (_lib or lib()).compkv_attend(ctx, layer, q, sel, out, stream)
+    if st:
+        _check(st, "compkv_attend")
 
 
 def compkv_decode(ctx, layer, q, k_new, v_new, out, sel, stream):
