@@ -73,7 +73,8 @@ struct Scale {
 // The tail.  A place that holds tokens of block b or of a later one goes out of date when block b is written; the writer
 // empties it.
 constexpr int kTails = 3;
-__device__ __forceinline__ bool tail_in(int len, int b) { return len > b * kBlock && len <= (b + 1) * kBlock; }  // the place is block b's
+// Whether the place is block b's.
+__device__ __forceinline__ bool tail_in(int len, int b) { return len > b * kBlock && len <= (b + 1) * kBlock; }
 // The place that holds at least the first `lo` tokens of block b of a unit (-1: none).
 __device__ __forceinline__ int tail_place(const Kv8Args& c, int unit, int b, int lo) {
   int place = -1;

@@ -102,15 +102,16 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // d += A B, fp16 inputs
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
   asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // d = A B + C, where rows r of C are x in even and y in odd columns, and rows r + 8 are z and w
-__device__ __forceinline__ void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
-                                             float x, float y, float z, float w) {
+__device__ __forceinline__ void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1, float x, float y, float z, float w) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(x), "f"(y), "f"(z), "f"(w));
@@ -188,7 +189,10 @@ struct Places {
 #pragma unroll
     for (int x = 0; x < D / 64; ++x) k[x] = chunk_at<D>(token_of<D>(r), c * (D / 64) + x);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) v[j] = D == 128 ? chunk_at<D>(token_of<D>(2 * c + j), r) : chunk_at<D>(token_of<D>(2 * c + j), r >> 1) + (r & 1) * 8;
+    for (int j = 0; j < 2; ++j) {
+      const int t = token_of<D>(2 * c + j);
+      v[j] = D == 128 ? chunk_at<D>(t, r) : chunk_at<D>(t, r >> 1) + (r & 1) * 8;
+    }
   }
 };
 
@@ -282,7 +286,8 @@ __device__ __forceinline__ void attend_pair(State<D>& st, const uint8_t* stage, 
     if constexpr (SPARSE) {
       const float fn = blk[i].vbar ? ex2(e2[i] - low) : 0.f;
       if (c == 0) st.l -= fn;
-      off = make_float2(-Wd::kUnit * __shfl_sync(0xffffffffu, fn, 8 * c), -Wd::kUnit * __shfl_sync(0xffffffffu, fn, 8 * c + 4));
+      off.x = -Wd::kUnit * __shfl_sync(0xffffffffu, fn, 8 * c);
+      off.y = -Wd::kUnit * __shfl_sync(0xffffffffu, fn, 8 * c + 4);
     }
     uint32_t w[4][D / 32];  // values of this lane's four tokens: token_of(2c), token_of(2c + 1), and 8 further
 #pragma unroll
@@ -347,7 +352,8 @@ __device__ __forceinline__ float4 load_query(const Attend8Args& a, int64_t unit,
   const int64_t at = (unit * a.G + head) * D + 4 * lane;
   if (!a.q_bf16) return __ldcg(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.q) + at));
   const uint2 w = __ldcg(reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(a.q) + at));
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
 }
 template <int D, int KV, bool SPARSE>
 __device__ __forceinline__ void stage_query(Smem8<D, SPARSE>& sm, float4 x, int head, int lane) {
@@ -374,7 +380,8 @@ __device__ __forceinline__ void stage_query(Smem8<D, SPARSE>& sm, float4 x, int 
     const uint32_t part[2][2] = {{f.x, f.z}, {f.y, f.w}};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&part[k][0])), v = __half22float2(*reinterpret_cast<const __half2*>(&part[k][1]));
+      const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&part[k][0]));
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&part[k][1]));
       b[k].x = warp_sum((u.x + u.y) + (v.x + v.y)) * (-Wide<KV>::kBias * Wide<KV>::kUnit);
     }
     if (lane == 0) sm.qb[head] = make_float2(b[0].x, b[1].x);
@@ -387,7 +394,8 @@ __device__ __forceinline__ void stage_query(Smem8<D, SPARSE>& sm, float4 x, int 
 
 // This segment's share of the unit's compensation sums: the stream's records p, p + C, ... at their common reference.
 template <int D, bool SPARSE>
-__device__ __forceinline__ void stage_compensation(Smem8<D, SPARSE>& sm, const Attend8Args& a, int i0, int nseg, int p, int C, float unit, int tid) {
+__device__ __forceinline__ void stage_compensation(Smem8<D, SPARSE>& sm, const Attend8Args& a, int i0, int nseg, int p, int C,
+                                                   float unit, int tid) {
 #pragma unroll 1
   for (int item = tid; item < a.G * D / 4; item += Smem8<D, SPARSE>::kThreads) {
     const int g = item / (D / 4), col = 4 * (item % (D / 4));
@@ -450,10 +458,11 @@ __device__ __forceinline__ void add_part(float4& A, float& S, float4 v, float s,
   S = fmaf(s, f, S);
 }
 
-// The unit's segments joined: those of runs c0 .. c0 + C - 1, whose first may have come from another unit's stages.  Where the
-// rows have fewer items than there are threads, groups of threads take a share of the segments each.
+// The unit's segments joined: those of runs c0 .. c0 + C - 1, whose first may have come from another unit's stages.
+// Where the rows have fewer items than there are threads, groups of threads take a share of the segments each.
 template <int D, int KV, bool SPARSE>
-__device__ __forceinline__ void join_segments(Smem8<D, SPARSE>& sm, const Attend8Args& a, int64_t unit, int c0, int C, bool tail, int tid) {
+__device__ __forceinline__ void join_segments(Smem8<D, SPARSE>& sm, const Attend8Args& a, int64_t unit, int c0, int C, bool tail,
+                                              int tid) {
   const int items = a.G * D / 4, groups = max(1, min(Smem8<D, SPARSE>::kThreads, (int)sizeof(sm.part) / 24) / items);
   float4* accs = reinterpret_cast<float4*>(sm.part);                                   // [groups][items]
   float2* refs = reinterpret_cast<float2*>(accs + groups * items);
@@ -496,7 +505,10 @@ __device__ __forceinline__ void join_segments(Smem8<D, SPARSE>& sm, const Attend
     float M = -INFINITY, S = 0.f;
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = 0; k < groups; ++k) M = fmaxf(M, refs[k * items + tid].x);
-    for (int k = 0; k < groups; ++k) add_part(A, S, accs[k * items + tid], refs[k * items + tid].y, part_factor(refs[k * items + tid].x, M));
+    for (int k = 0; k < groups; ++k) {
+      const float2 e = refs[k * items + tid];
+      add_part(A, S, accs[k * items + tid], e.y, part_factor(e.x, M));
+    }
     put_out<D, KV>(a, unit, tid / (D / 4), 4 * (tid % (D / 4)), A, S);
   }
   __syncthreads();
@@ -562,7 +574,8 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
     // the stream's plan
     for (int s = lane; s < a.B; s += 32) {
       bool fits;
-      sm.streamed[s] = streamed_blocks(call_tokens(__ldcg(a.seq_len + s), a.cap_blocks[s], false, &fits), false, a.selects, a.K, false);
+      const int L = call_tokens(__ldcg(a.seq_len + s), a.cap_blocks[s], false, &fits);
+      sm.streamed[s] = streamed_blocks(L, false, a.selects, a.K, false);
     }
     __syncwarp();
     plan_warp(sm.streamed, a.B, a.Hkv, a.stream_P, stage_blocks(a.r, a.G), sm.soff, &sm.seg, lane);
@@ -576,7 +589,8 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
   int si = 0, unit_first = 0, unit_end = 0, stages_issue = 0, n_issue = 0, y_issue = 0;  // the unit of stage to_issue
   int64_t su = 0, row_issue = 0;
   const uint64_t pol = policy_evict_first();
-  auto entry = [&](int64_t unit, int i, int n) -> int {  // block of entry i of a unit's selection (-1: none, or not a valid one)
+  // block of entry i of a unit's selection (-1: none, or not a valid one)
+  auto entry = [&](int64_t unit, int i, int n) -> int {
     if (i >= min(n, a.K)) return -1;
     const int* sel = a.sel + unit * a.K;
     const int e = __ldcg(sel + i), prev = i > 0 ? __ldcg(sel + i - 1) : -1;
@@ -613,7 +627,8 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
         const int mine = lane & 1 ? b1 : b0;
         if (mine >= 0) {
           const float* src = (lane < kPair ? a.kv8.kscale : a.kv8.vscale) + row_issue + mine;
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&sm.scale[warp][issue_slot][lane])), "l"(src) : "memory");
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&sm.scale[warp][issue_slot][lane])), "l"(src)
+                       : "memory");
         }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
       }
@@ -677,7 +692,8 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
       }
       valid = __reduce_add_sync(0xffffffffu, valid);
       if (lane == 0 && valid) atomicAdd(&sm.valid, valid);
-      if (__any_sync(0xffffffffu, wrong) && lane == 0 && (int)blockIdx.x == c0) set_error(a.status, kDevBadSelection, s, h, 61);
+      if (__any_sync(0xffffffffu, wrong) && lane == 0 && (int)blockIdx.x == c0)
+        set_error(a.status, kDevBadSelection, s, h, 61);
       if (!waited) {
         pdl_wait();
       }
@@ -747,7 +763,10 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
         for (int e = 0; e < 2; ++e) {
           float2* to = reinterpret_cast<float2*>(&sm.part[warp][e][r * (D / 8)]);
 #pragma unroll
-          for (int mt = 0; mt < D / 16; ++mt) to[mt] = e ? make_float2(st.acc[mt][0].y, st.acc[mt][1].y) : make_float2(st.acc[mt][0].x, st.acc[mt][1].x);
+          for (int mt = 0; mt < D / 16; ++mt) {
+            const float2 u = st.acc[mt][0], v = st.acc[mt][1];
+            to[mt] = e ? make_float2(u.y, v.y) : make_float2(u.x, v.x);
+          }
         }
       }
       __syncthreads();
@@ -761,9 +780,11 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
         float S = 0.f;
 #pragma unroll
         for (int w = 0; w < W; ++w)
-          add_part(A, S, *reinterpret_cast<const float4*>(&sm.part[w][g - g0][col]), sm.sum[w][g], part_factor(sm.ref[w][g], M));
+          add_part(A, S, *reinterpret_cast<const float4*>(&sm.part[w][g - g0][col]), sm.sum[w][g],
+                   part_factor(sm.ref[w][g], M));
         if (comp)
-          add_part(A, S, *reinterpret_cast<const float4*>(&sm.comp[SPARSE ? g : 0][col]), sm.sum[W][g], part_factor(sm.ref[W][g], M));
+          add_part(A, S, *reinterpret_cast<const float4*>(&sm.comp[SPARSE ? g : 0][col]), sm.sum[W][g],
+                   part_factor(sm.ref[W][g], M));
         if (C == 1) {
           put_out<D, KV>(a, unit, g, col, A, S);
         } else {
@@ -794,7 +815,8 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
 #pragma unroll 1
   for (int u = blockIdx.x; u < a.B * a.Hkv; u += gridDim.x) {
     if (sm.stages[u / a.Hkv]) continue;
-    for (int i = tid; i < a.G * D / 4; i += T) put_out<D, KV>(a, u, i / (D / 4), 4 * (i % (D / 4)), make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
+    for (int i = tid; i < a.G * D / 4; i += T)
+      put_out<D, KV>(a, u, i / (D / 4), 4 * (i % (D / 4)), make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
   }
 }
 
@@ -822,7 +844,8 @@ cudaError_t attend8_d(const Attend8Args& a, cudaStream_t st) {
 template <int D, int KV, bool SPARSE>
 cudaError_t prepare_as() {
   static_assert(sizeof(Smem8<D, SPARSE>) + 1024 <= 232448, "shared memory of a CTA");
-  return raise_smem_limit(reinterpret_cast<const void*>(&attend8_kernel<D, KV, SPARSE>), (int)sizeof(Smem8<D, SPARSE>) + 1024);
+  return raise_smem_limit(reinterpret_cast<const void*>(&attend8_kernel<D, KV, SPARSE>),
+                          (int)sizeof(Smem8<D, SPARSE>) + 1024);
 }
 template <int D>
 cudaError_t prepare_d() {
@@ -835,6 +858,8 @@ cudaError_t prepare_d() {
 }  // namespace
 
 cudaError_t prepare_attend8(int d) { return d == 128 ? prepare_d<128>() : prepare_d<64>(); }
-cudaError_t launch_attend8(const Attend8Args& a, cudaStream_t st) { return a.d == 128 ? attend8_d<128>(a, st) : attend8_d<64>(a, st); }
+cudaError_t launch_attend8(const Attend8Args& a, cudaStream_t st) {
+  return a.d == 128 ? attend8_d<128>(a, st) : attend8_d<64>(a, st);
+}
 
 }  // namespace compkv

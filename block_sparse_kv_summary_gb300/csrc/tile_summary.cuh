@@ -16,7 +16,8 @@ struct TileCodes {
   float* scale;
 };
 template <int D, int KV>
-__device__ __forceinline__ void tile_summary(const __nv_bfloat16* tile, int n, float* bar, float* dbar, int r, TileCodes out, int lane) {
+__device__ __forceinline__ void tile_summary(const __nv_bfloat16* tile, int n, float* bar, float* dbar, int r, TileCodes out,
+                                             int lane) {
   constexpr int V = D / 32;
   float2 t[kBlock][V / 2], mean[V / 2] = {};
   __nv_bfloat162 most = __floats2bfloat162_rn(0.f, 0.f);
