@@ -93,6 +93,7 @@ class CompKVCache:
                                      self.vbar.data_ptr(), self.dbar.data_ptr(),
                                      self.seq_len.data_ptr(), self.scratch.data_ptr(), nbytes)
         self._index = self.device.index
+        self._lib = C.lib()
         self._shared_ws = None
         # shapes of a call's outputs, and of the rows of the projection that it reads
         self._q_shape, self._kv_shape = (batch, num_kv_heads * group_size, head_dim), (batch, num_kv_heads, head_dim)
@@ -199,6 +200,17 @@ class CompKVCache:
             with torch.cuda.device(index):
                 fn(self.ctx, *args, _raw_stream(index))
 
+    def _call_raw(self, name, *args):
+        """The same past the binding's function of that name, for arguments that are marshalled already."""
+        fn, index = getattr(self._lib, name), self._index
+        if _current_device() == index:
+            st = fn(self.ctx, *args, _raw_stream(index))
+        else:
+            with torch.cuda.device(index):
+                st = fn(self.ctx, *args, _raw_stream(index))
+        if st:
+            C._check(st, name)
+
     def _rope_args(self, qkv, tokens, table, q_weight, k_weight, eps, positions, interleaved, q_dtype):
         width, dev, d = self._width, self.device, (self.d,)
         if q_dtype not in _TYPES:
@@ -261,7 +273,7 @@ class CompKVCache:
         else:
             self._t(q, "q", q_dtype, shape)
         if tokens:
-            self._call(C.compkv_prefill_qkv, layer, a, starts, counts, q.data_ptr())
+            self._call_raw("compkv_prefill_qkv", layer, a, C._at(starts), C._at(counts), q.data_ptr())
         return q
 
     def _pairs(self, src, dst, layers):
@@ -346,7 +358,7 @@ class CompKVCache:
         else:
             self._t(v, "v", dtype, shape)
         if shape[0]:
-            self._call(C.compkv_read, layer, starts, counts, _TYPES[dtype], k.data_ptr(), v.data_ptr())
+            self._call_raw("compkv_read", layer, C._at(starts), C._at(counts), _TYPES[dtype], k.data_ptr(), v.data_ptr())
         return k, v
 
     def attend_all(self, layer, q, out=None):
@@ -360,7 +372,7 @@ class CompKVCache:
             out = torch.empty_like(q)
         else:
             self._t(out, "out", dtype, shape)
-        self._call(C.compkv_attend_all, layer, qp, _TYPES[dtype], out.data_ptr())
+        self._call_raw("compkv_attend_all", layer, qp, _TYPES[dtype], out.data_ptr())
         return out
 
     def device_status(self) -> int:
