@@ -747,3 +747,38 @@ def test_queries_from_another_stream():
         assert torch.equal(c.attend_all(0, x), want)
     with pytest.raises(ValueError):
         c.attend_all(0, torch.stack([q, q], -1)[..., 0])
+
+
+@pytest.mark.parametrize("kv", KV8)
+@pytest.mark.parametrize("d", [64, 128])
+def test_what_stands_behind_the_tokens_is_never_read_as_such(kv, d):
+    # codes of NaN behind the last token of a block, and rows of NaN behind the last block
+    hkv, g, lens, caps = 2, 4, [1, 17, 40, 0, 100, 31], [64, 64, 64, 16, 128, 32]
+    c = make_cache(caps, kv, hkv=hkv, g=g, d=d)
+    write(c, [(0, n) for n in lens], 3, hkv, g, d)
+    q = randn(4, len(lens), hkv * g, d)
+    sel = selection(5, c, lens, 8)
+    sel[4, :, 3:] = -1
+
+    def results():
+        return [c.attend_all(0, q), c.attend(0, q, sel), *c.read(0, None, lens, torch.float32)]
+
+    want = results()
+    for s, n in enumerate(lens):
+        for h in range(hkv):
+            r0, cap = c.rows(0, s, h)
+            N = (n + BLOCK - 1) // BLOCK
+            for t, x in ((c.k, c.kscale), (c.v, c.vscale)):
+                t[r0:r0 + cap].view(torch.int8).view(-1, d)[n:] = 127
+                x[r0 + N:r0 + cap] = float("nan")
+            for t in (c.kbar, c.vbar, c.dbar):
+                t[r0 + N:r0 + cap] = float("nan")
+    assert all(torch.equal(a, b) for a, b in zip(results(), want))
+    # and tokens that come later make blocks of their own
+    k, v = (randn(6 + i, len(lens), hkv, d, dtype=torch.bfloat16) for i in range(2))
+    twin = make_cache(caps, torch.bfloat16, hkv=hkv, g=g, d=d)
+    write(twin, [(0, n) for n in lens], 3, hkv, g, d)
+    for x in (c, twin):
+        x.append(0, k, v)
+    check_stored(c, twin, [n + 1 for n in lens])
+    assert c.attend_all(0, q).isfinite().all()
