@@ -376,8 +376,9 @@ compkv_status compkv_attend_shared(compkv_ctx *ctx, int layer, const void *q, in
  * start, or an append after the caller set seq_len back), the tokens in front of
  * them in that block come from their codes, rounded to bf16.  Summaries are
  * those of the tokens in bf16.  Codes, scales and tail are written by these
- * calls; a caller that fills codes and scales itself (with kbar, vbar, dbar and
- * seq_len) does so before any call wrote to the sequence.
+ * calls; a caller that fills a sequence's codes and scales itself, with its kbar,
+ * vbar, dbar and seq_len (a copy of another sequence's, say), sets its tail_len
+ * to 0.
  *
  * A context of such a cache takes compkv_rope, compkv_prefill_qkv,
  * compkv_append, compkv_score_select, compkv_attend, compkv_decode,

@@ -782,3 +782,30 @@ def test_what_stands_behind_the_tokens_is_never_read_as_such(kv, d):
         x.append(0, k, v)
     check_stored(c, twin, [n + 1 for n in lens])
     assert c.attend_all(0, q).isfinite().all()
+
+
+def test_a_sequence_copied_by_the_caller():
+    # rows, summaries and length of one sequence into another that held something else, its tail_len zeroed
+    hkv, d, n = 2, 64, 37
+    c = make_cache([64, 64], torch.float8_e4m3fn, hkv=hkv, d=d)
+    write(c, [(0, n), (0, 41)], 3, hkv, 4, d)
+    for h in range(hkv):
+        a, b = c.rows(0, 0, h)[0], c.rows(0, 1, h)[0]
+        for t in (c.k.view(torch.int8), c.v.view(torch.int8), c.kscale, c.vscale, c.kbar, c.vbar, c.dbar):
+            t[b:b + 4] = t[a:a + 4]
+    c.seq_len[0, 1] = n
+    c.tail_len.view(2, hkv, 3)[1] = 0
+    q = randn(4, 1, hkv * 4, d).expand(2, -1, -1).contiguous()
+    out = c.attend_all(0, q)
+    assert torch.equal(out[0], out[1])
+    before = values(c)
+    k, v = (randn(6 + i, 2, hkv, d, dtype=torch.bfloat16) for i in range(2))
+    c.append(0, k, v)
+    for h in range(hkv):
+        r = c.rows(0, 1, h)[0] + n // BLOCK
+        for x, codes, scale, y in zip(before, (c.k, c.v), (c.kscale, c.vscale), (k, v)):
+            block = torch.zeros(BLOCK, d, device="cuda")
+            block[:n % BLOCK] = x[r, :n % BLOCK].float().bfloat16().float()
+            block[n % BLOCK] = y[1, h].float()
+            want, s = quantised(block, c.kv_dtype)
+            assert torch.equal(bits(codes[r]), bits(want)) and scale[r] == s
