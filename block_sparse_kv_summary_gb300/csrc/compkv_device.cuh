@@ -95,8 +95,9 @@ struct Kv8Args {
   uint8_t* v;
   float* kscale;               // [rows]
   float* vscale;
-  __nv_bfloat16* tail;         // [B][Hkv][3][K, V][16][d]: tokens of blocks of each sequence as they came: the last one
-                               // in place 0 or 2, the one that its last call of many tokens began inside in place 1
+  __nv_bfloat16* tail;         // [B][Hkv][3][K, V][16][d]: tokens of blocks of each sequence as they came: the one that
+                               // its last call of many tokens began inside in place 1, or in 2 if it also ended there;
+                               // the last one there too, or in 0 or 2
   int* tail_len;               // [B][Hkv][3]: the tokens up to the last one there (0: nothing is)
   int type;                    // KvType
 };

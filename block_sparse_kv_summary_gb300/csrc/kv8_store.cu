@@ -11,9 +11,12 @@ namespace {
 // One CTA per sequence, a warp for K and one for V of eight heads at a time.
 // Token L (L = seq_len) joins the tokens of its block, which the tail holds in
 // bf16; the block's summary and codes are formed again from all of them, so that
-// a block's contents do not depend on how its tokens arrived.  Where the
-// sequence was cut back into an older block, the tokens in front come from their
-// codes.  Bound by latency: length, tail, and the block's arithmetic in a row; 5.6
+// a block's contents do not depend on how its tokens arrived.  A block goes on in
+// the place of the tail that it stands in, and a new one takes place 0, so that
+// the block that the last call of many tokens began inside (place 1 or 2) is
+// there when the sequence is cut back to that beginning.  Where it was cut back
+// into another older block, the tokens in front come from their codes.  Bound by
+// latency: length, tail, and the block's arithmetic in a row; 5.6
 // us for 8 heads of 128 (8.2 with one warp for K and V, which read their tokens
 // from global memory once more for the summary).
 constexpr int kAppendHeads = 8;
@@ -35,7 +38,7 @@ __global__ void __launch_bounds__(64 * kAppendHeads) append8_kernel(const __grid
     const bool mine = h < a.Hkv;
     const int64_t row = row_of(a, s, mine ? h : 0, b);
     const int unit = s * a.Hkv + (mine ? h : 0);
-    const int place = tail_place(c, unit, b, slot), last = place == 2 ? 2 : 0;
+    const int place = tail_place(c, unit, b, slot), last = max(place, 0);
     uint8_t* codes = (kv ? c.v : c.k) + row * kBlock * D;
     float* scale = (kv ? c.vscale : c.kscale) + row;
     __nv_bfloat16* to = tail_at<D>(c, unit, last) + kv * kBlock * D;
@@ -54,7 +57,7 @@ __global__ void __launch_bounds__(64 * kAppendHeads) append8_kernel(const __grid
         for (int i = 0; i < CH / 2; ++i) {
           const int at = i * 32 + lane, j = at / CH;
           reinterpret_cast<uint4*>(tile)[at] = x[i];
-          if (j == slot || (j < slot && place != last)) reinterpret_cast<uint4*>(to)[at] = x[i];
+          if (j == slot) reinterpret_cast<uint4*>(to)[at] = x[i];
         }
       } else {
         const float old = __ldcg(scale);

@@ -467,13 +467,16 @@ __global__ void __launch_bounds__(256, 3) rope_prefill_kernel(const __grid_const
   }
   // The tail's place for this block's tokens.  The CTA of the call's last block takes 0 -- or 2, where the CTA of its first
   // block may be reading 0, or the block already stands there -- and empties the other one if it holds a block behind the
-  // first; the CTA of the first block puts it into 1 if the call begins inside it, and empties what else holds it.
+  // first; the CTA of the first block puts it into 1 if the call begins inside it, and empties what else holds it.  A call
+  // that begins inside a block and ends there keeps it in 1 or takes 2: one token after another makes its new blocks in 0,
+  // and what an earlier call began inside stays in 1.
   __shared__ int keep[4];
   const int begin = g.starts[s] / kBlock, last = (g.starts[s] + g.counts[s] - 1) / kBlock;
   int* len = KV == kKvBf16 ? nullptr : g.kv8.tail_len + kTails * (s * a.Hkv + kv0 + (int)threadIdx.x);
   if (KV != kKvBf16 && threadIdx.x < kvn) {
-    const bool two = begin == last ? tail_in(__ldcg(len + 2), b) : tail_in(__ldcg(len), begin);
-    keep[threadIdx.x] = b == last ? (two ? 2 : 0) : b == begin && lo > 0 ? 1 : -1;
+    const bool two = begin == last ? lo > 0 || tail_in(__ldcg(len + 2), b) : tail_in(__ldcg(len), begin);
+    const bool one = b == begin && lo > 0 && (begin < last || tail_in(__ldcg(len + 1), b));
+    keep[threadIdx.x] = one ? 1 : b == last ? (two ? 2 : 0) : -1;
   }
   __syncthreads();
   if (KV != kKvBf16 && threadIdx.x < kvn && (b == begin || b == last)) {
