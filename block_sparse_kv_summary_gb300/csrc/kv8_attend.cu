@@ -59,6 +59,8 @@ constexpr int kPair = 2;     // blocks of a stage
 constexpr int kHeads = 2;    // heads joined at a time
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLift = 14.f;  // weights are kept below 2^14: fp16 ends at 2^16
+constexpr float kUnit = 0x1p-24f;  // of outputs until they are divided: with the lift, 2^-10 of the weighted sums, so that
+                                   // values up to the end of fp32 have room for 512 tokens and more
 
 // Shared memory, from a 1024-byte boundary on.
 template <int D, bool SPARSE>
@@ -124,14 +126,14 @@ __device__ __forceinline__ void split_f16(float x, float y, uint32_t& hi, uint32
   lo = as_u32(__floats2half2_rn(x - f.x, y - f.y));
 }
 
-// Four codes as two pairs of fp16, in units of kUnit and kBias too large: coordinates 0 and 1, then 2 and 3 (e4m3), or 0
+// Four codes as two pairs of fp16, in units of kCode and kBias too large: coordinates 0 and 1, then 2 and 3 (e4m3), or 0
 // and 2, then 1 and 3 (int8).  A byte on its own is a subnormal fp16 number, byte * 2^-24, so an int8 code takes no more
 // than being made unsigned and put in place; products start from what the bias of 128 makes of them (64 sequences of up to
 // 64K tokens: 617 us; with the bias taken off each pair of codes by a subtraction, 675).  e4m3 has an instruction (16 x
 // 64K: 198 us; its bits shifted into place, 263).
 template <int KV>
 struct Wide {
-  static constexpr float kUnit = KV == kKvInt8 ? 0x1p-24f : 1.f, kBias = KV == kKvInt8 ? 128.f : 0.f;
+  static constexpr float kCode = KV == kKvInt8 ? 0x1p-24f : 1.f, kBias = KV == kKvInt8 ? 128.f : 0.f;
   static __device__ __forceinline__ void pairs(uint32_t w, uint32_t& a, uint32_t& b) {
     if constexpr (KV == kKvInt8) {
       const uint32_t x = w ^ 0x80808080u;
@@ -175,7 +177,7 @@ struct State {
 // What a block of a stage is: its tokens (0: not there), its scales, and what comes off of the compensation sums.
 struct Block8 {
   int n;
-  float ks, vs;
+  float ks, vs;        // (vs brings a product to kUnit)
   float zb;            // zbar of head r, natural units
   const float* vbar;   // mean value; null: nothing comes off
 };
@@ -229,7 +231,7 @@ __device__ __forceinline__ void attend_pair(State<D>& st, const uint8_t* stage, 
   float z[kPair][4], bm = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kPair; ++i) {
-    const float f = qs * blk[i].ks * (1.f / Wd::kUnit);
+    const float f = qs * blk[i].ks * (1.f / Wd::kCode);
 #pragma unroll
     for (int e = 0; e < 4; ++e) z[i][e] = (s[i][e >> 1][e & 1] + s[i][e >> 1][2 + (e & 1)]) * f;
     if (blk[i].n < kBlock) {
@@ -277,8 +279,8 @@ __device__ __forceinline__ void attend_pair(State<D>& st, const uint8_t* stage, 
     if constexpr (Wd::kBias != 0.f) {
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      from.x = __shfl_sync(0xffffffffu, sum, 8 * c) * (-Wd::kBias * Wd::kUnit);
-      from.y = __shfl_sync(0xffffffffu, sum, 8 * c + 4) * (-Wd::kBias * Wd::kUnit);
+      from.x = __shfl_sync(0xffffffffu, sum, 8 * c) * (-Wd::kBias * Wd::kCode);
+      from.y = __shfl_sync(0xffffffffu, sum, 8 * c + 4) * (-Wd::kBias * Wd::kCode);
       sum = c == 0 ? sum : 0.f;
     }
     st.l += sum;  // this lane's part
@@ -286,8 +288,8 @@ __device__ __forceinline__ void attend_pair(State<D>& st, const uint8_t* stage, 
     if constexpr (SPARSE) {
       const float fn = blk[i].vbar ? ex2(e2[i] - low) : 0.f;
       if (c == 0) st.l -= fn;
-      off.x = -Wd::kUnit * __shfl_sync(0xffffffffu, fn, 8 * c);
-      off.y = -Wd::kUnit * __shfl_sync(0xffffffffu, fn, 8 * c + 4);
+      off.x = -kUnit * __shfl_sync(0xffffffffu, fn, 8 * c);
+      off.y = -kUnit * __shfl_sync(0xffffffffu, fn, 8 * c + 4);
     }
     uint32_t w[4][D / 32];  // values of this lane's four tokens: token_of(2c), token_of(2c + 1), and 8 further
 #pragma unroll
@@ -382,7 +384,7 @@ __device__ __forceinline__ void stage_query(Smem8<D, SPARSE>& sm, float4 x, int 
     for (int k = 0; k < 2; ++k) {
       const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&part[k][0]));
       const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&part[k][1]));
-      b[k].x = warp_sum((u.x + u.y) + (v.x + v.y)) * (-Wide<KV>::kBias * Wide<KV>::kUnit);
+      b[k].x = warp_sum((u.x + u.y) + (v.x + v.y)) * (-Wide<KV>::kBias * Wide<KV>::kCode);
     }
     if (lane == 0) sm.qb[head] = make_float2(b[0].x, b[1].x);
   } else if (lane == 0) {
@@ -395,7 +397,7 @@ __device__ __forceinline__ void stage_query(Smem8<D, SPARSE>& sm, float4 x, int 
 // This segment's share of the unit's compensation sums: the stream's records p, p + C, ... at their common reference.
 template <int D, bool SPARSE>
 __device__ __forceinline__ void stage_compensation(Smem8<D, SPARSE>& sm, const Attend8Args& a, int i0, int nseg, int p, int C,
-                                                   float unit, int tid) {
+                                                   int tid) {
 #pragma unroll 1
   for (int item = tid; item < a.G * D / 4; item += Smem8<D, SPARSE>::kThreads) {
     const int g = item / (D / 4), col = 4 * (item % (D / 4));
@@ -424,7 +426,7 @@ __device__ __forceinline__ void stage_compensation(Smem8<D, SPARSE>& sm, const A
         R = mn;
       }
     }
-    *reinterpret_cast<float4*>(&sm.comp[g][col]) = make_float4(A.x * unit, A.y * unit, A.z * unit, A.w * unit);
+    *reinterpret_cast<float4*>(&sm.comp[g][col]) = make_float4(A.x * kUnit, A.y * kUnit, A.z * kUnit, A.w * kUnit);
     if (col == 0) {
       sm.ref[Smem8<D, SPARSE>::kWarps][g] = R * kLog2e;
       sm.sum[Smem8<D, SPARSE>::kWarps][g] = W;
@@ -432,11 +434,11 @@ __device__ __forceinline__ void stage_compensation(Smem8<D, SPARSE>& sm, const A
   }
 }
 
-template <int D, int KV>
+template <int D>
 __device__ __forceinline__ void put_out(const Attend8Args& a, int64_t unit, int g, int col, float4 acc, float l) {
   // a row without tokens is zero; a sum that is NaN goes through
   const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
-  constexpr float one = 1.f / Wide<KV>::kUnit;
+  constexpr float one = 1.f / kUnit;
   const float4 y = make_float4(acc.x * inv * one, acc.y * inv * one, acc.z * inv * one, acc.w * inv * one);
   const int64_t at = (unit * a.G + g) * D + col;
   if (a.q_bf16) {
@@ -460,7 +462,7 @@ __device__ __forceinline__ void add_part(float4& A, float& S, float4 v, float s,
 
 // The unit's segments joined: those of runs c0 .. c0 + C - 1, whose first may have come from another unit's stages.
 // Where the rows have fewer items than there are threads, groups of threads take a share of the segments each.
-template <int D, int KV, bool SPARSE>
+template <int D, bool SPARSE>
 __device__ __forceinline__ void join_segments(Smem8<D, SPARSE>& sm, const Attend8Args& a, int64_t unit, int c0, int C, bool tail,
                                               int tid) {
   const int items = a.G * D / 4, groups = max(1, min(Smem8<D, SPARSE>::kThreads, (int)sizeof(sm.part) / 24) / items);
@@ -493,7 +495,7 @@ __device__ __forceinline__ void join_segments(Smem8<D, SPARSE>& sm, const Attend
       M = mn;
     }
     if (groups == 1) {
-      put_out<D, KV>(a, unit, g, col, A, S);
+      put_out<D>(a, unit, g, col, A, S);
     } else {
       accs[x] = A;
       refs[x] = make_float2(M, S);
@@ -509,7 +511,7 @@ __device__ __forceinline__ void join_segments(Smem8<D, SPARSE>& sm, const Attend
       const float2 e = refs[k * items + tid];
       add_part(A, S, accs[k * items + tid], e.y, part_factor(e.x, M));
     }
-    put_out<D, KV>(a, unit, tid / (D / 4), 4 * (tid % (D / 4)), A, S);
+    put_out<D>(a, unit, tid / (D / 4), 4 * (tid % (D / 4)), A, S);
   }
   __syncthreads();
 }
@@ -700,7 +702,7 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
       waited = true;
       if (!a.no_comp) {
         const int nseg = (sm.streamed[s] + sm.seg - 1) / sm.seg;
-        stage_compensation<D>(sm, a, sm.soff[s] + h * nseg, nseg, (int)blockIdx.x - c0, C, Wide<KV>::kUnit, tid);
+        stage_compensation<D>(sm, a, sm.soff[s] + h * nseg, nseg, (int)blockIdx.x - c0, C, tid);
       }
     }
     __syncthreads();
@@ -734,7 +736,7 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
 #pragma unroll
         for (int k = 0; k < kPair; ++k) {
           blk[k].ks = blk[k].n ? sm.scale[warp][slot][k] : 0.f;
-          blk[k].vs = blk[k].n ? sm.scale[warp][slot][kPair + k] : 0.f;
+          blk[k].vs = blk[k].n ? sm.scale[warp][slot][kPair + k] * (kUnit / Wide<KV>::kCode) : 0.f;
         }
         if (blk[0].n | blk[1].n) attend_pair<D, KV, SPARSE>(st, sm.ring[warp][slot], sm.q, qs, qb, blk, places, lane);
         --flying;
@@ -786,7 +788,7 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
           add_part(A, S, *reinterpret_cast<const float4*>(&sm.comp[SPARSE ? g : 0][col]), sm.sum[W][g],
                    part_factor(sm.ref[W][g], M));
         if (C == 1) {
-          put_out<D, KV>(a, unit, g, col, A, S);
+          put_out<D>(a, unit, g, col, A, S);
         } else {
           __stcg(reinterpret_cast<float4*>(a.acc + ((int64_t)place * a.G + g) * D + col), A);
           if (col == 0) __stcg(a.ml + (int64_t)place * a.G + g, make_float2(M, S));
@@ -804,7 +806,7 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
     }
     __syncthreads();
     if (!sm.last) continue;
-    join_segments<D, KV>(sm, a, unit, c0, C, tail, tid);
+    join_segments<D>(sm, a, unit, c0, C, tail, tid);
   }
   if (!waited) pdl_wait();
   if (!ok) {  // a wait ran out: let the copies in flight land before the CTA's memory goes
@@ -816,7 +818,7 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
   for (int u = blockIdx.x; u < a.B * a.Hkv; u += gridDim.x) {
     if (sm.stages[u / a.Hkv]) continue;
     for (int i = tid; i < a.G * D / 4; i += T)
-      put_out<D, KV>(a, u, i / (D / 4), 4 * (i % (D / 4)), make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
+      put_out<D>(a, u, i / (D / 4), 4 * (i % (D / 4)), make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
   }
 }
 

@@ -422,8 +422,10 @@ compkv_status compkv_read(compkv_ctx *ctx, int layer, const int *starts, const i
  * q and out: device [B][Hq][d], both of `type` (COMPKV_BF16 or COMPKV_F32).
  * Queries and softmax weights enter the products to 22 bits, sums are fp32.
  * Logits, and a query's largest coordinate times a block's largest one, are
- * below 2^100 (so too in compkv_attend and compkv_decode on such a cache).  The
- * rows of a sequence without tokens are zero.  (In bf16, compkv_attend_shared
+ * below 2^100 (so too in compkv_attend and compkv_decode on such a cache); a
+ * value's magnitude times the sequence's tokens is below 2^137 (there: 2^127),
+ * and blocks of e4m3 whose largest value is below 2^-93 enter with fewer bits.
+ * The rows of a sequence without tokens are zero.  (In bf16, compkv_attend_shared
  * without a prefix is the same attention.) */
 compkv_status compkv_attend_all(compkv_ctx *ctx, int layer, const void *q, int type, void *out, void *stream);
 

@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from test_gpu_kv8 import KV8, _built, check_stored, make_cache, randn, write  # noqa: F401
+from test_gpu_kv8 import KV8, MOST, _built, check, check_stored, fill, make_cache, randn, selection, values, write  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +50,43 @@ def test_the_block_that_a_call_began_inside_is_kept(kv, name):
         if op != "c":
             check_stored(c8, c16, [at])
     assert c8.device_status() == 0
+
+
+# ------------------------------------------------------------------ the range of values
+@pytest.mark.parametrize("kv", KV8)
+@pytest.mark.parametrize("d,hkv,g", [(64, 2, 4), (128, 1, 8)])
+def test_values_near_the_end_of_fp32(kv, d, hkv, g):
+    # keys of ordinary size, values up to bf16's largest: what the call sums up stays within fp32 where the result does
+    lens = [1, 17, 40, 300]
+    caps = [16, 32, 48, 304]
+    c = make_cache(caps, kv, hkv=hkv, g=g, d=d, budget=128)
+    for seed, size, sparse in ((1, 2.0 ** 127, False), (2, 2.0 ** 112, True)):
+        fill(c, seed, lens)
+        c.vscale.mul_(size / MOST[kv] / c.vscale.max())
+        v = values(c)[1]
+        assert size / 2 < v.abs().max() < size * 1.01
+        for s, n in enumerate(lens):
+            for h in range(hkv):
+                r0, _ = c.rows(0, s, h)
+                for b in range((n + 15) // 16):
+                    c.vbar[r0 + b] = v[r0 + b, :n - 16 * b].mean(0)
+        for dtype in (torch.float32, torch.bfloat16):
+            q = randn(seed + 7, len(lens), hkv * g, d, dtype=dtype)
+            out = c.attend_all(0, q)
+            assert out.isfinite().all()
+            check(c, out, 0, q, lens)
+        if sparse:  # (with Mean compensation the sums of a row's mean values are formed first, at their own size)
+            q = randn(seed + 9, len(lens), hkv * g, d)
+            sel = selection(3, c, lens, 8)
+            out = c.attend(0, q, sel)
+            assert out.isfinite().all()
+            check(c, out, 0, q, lens, sel)
+
+
+@pytest.mark.parametrize("kv", KV8)
+def test_values_near_the_least(kv):
+    c = make_cache([48], kv, hkv=1, g=4, d=64)
+    fill(c, 5, [40])
+    c.vscale.mul_(2.0 ** -80 / MOST[kv] / c.vscale.max())
+    q = randn(6, 1, 4, 64)
+    check(c, c.attend_all(0, q), 0, q, [40])
