@@ -22,8 +22,9 @@
 // Products.  Codes become fp16, which holds them all.  Scores are S = Q K^T on
 // mma.sync (m16n8k16): rows 0..7 are the query heads' high fp16 parts, rows
 // 8..15 their low parts, so that one product has both; the sum of rows r and
-// r + 8 is q . c to the 22 bits of the two parts.  The 16 columns of a block
-// share one scale.  Outputs are O^T = V^T P (rows: coordinates, columns: heads),
+// r + 8 is q . c.  (Two parts hold an fp32 number to 2^-23 of itself: what the
+// high part leaves is at most 2^12 units of its last place, of which the low part
+// holds 11 bits.)  The 16 columns of a block share one scale.  Outputs are O^T = V^T P (rows: coordinates, columns: heads),
 // with the weights in high and low parts too: weights are e^(z - m + 14 ln 2),
 // which keeps their low parts normal numbers.  A block's product is added to the
 // running output with the block's scale in fp32: the tensor cores' accumulator
@@ -38,13 +39,13 @@
 // between their copy and the product.
 //
 // Bound by DRAM for long rows, with the instructions that widen the codes close
-// behind: 64 sequences of up to 64K tokens of 8 heads, d 128 (4.4 GB of codes), 612
-// us, 7.2 TB/s; one of 128K 49 us, of which 5 pass before the first stage is there
+// behind: 64 sequences of up to 64K tokens of 8 heads, d 128 (4.4 GB of codes), 628
+// us, 7.0 TB/s; one of 128K 49 us, of which 5 pass before the first stage is there
 // and 8 between the first and the last CTA's end (some multiprocessors get a tenth
 // less of the memory's rate) and in the join; 1025 tokens of 2 heads 7 us.  Twelve
-// warps of two stages: with eight of three 707 us on the 64 sequences, with ten,
-// which leave two of the four schedulers a warp short, 787, with sixteen of single
-// blocks 706.
+// warps of two stages: where these took 617 us on the 64 sequences, eight of three
+// took 707, ten, which leave two of the four schedulers a warp short, 787, and
+// sixteen of single blocks 706.
 #include <cuda_fp16.h>
 
 #include "compkv_launch.h"
@@ -78,7 +79,6 @@ struct Smem8 {
   float ref[kWarps + 1][kMaxG];       // references (log2) and sums of the parts; the last: compensation
   float sum[kWarps + 1][kMaxG];
   float qs[kMaxG];                    // factor of a head's scores
-  float2 qb[kMaxG];                   // what the scores of its two parts start from
   uint64_t full[kWarps][kSlots];
   int tokens[kMaxBatch];              // of each sequence
   int stages[kMaxBatch];              // stages of each of its units
@@ -111,12 +111,12 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// d = A B + C, where rows r of C are x in even and y in odd columns, and rows r + 8 are z and w
-__device__ __forceinline__ void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                             uint32_t b1, float x, float y, float z, float w) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+// d = A B
+__device__ __forceinline__ void mma_f16_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(x), "f"(y), "f"(z), "f"(w));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ void split_f16(float x, float y, uint32_t& hi, uint32_t& lo) {
@@ -126,19 +126,22 @@ __device__ __forceinline__ void split_f16(float x, float y, uint32_t& hi, uint32
   lo = as_u32(__floats2half2_rn(x - f.x, y - f.y));
 }
 
-// Four codes as two pairs of fp16, in units of kCode and kBias too large: coordinates 0 and 1, then 2 and 3 (e4m3), or 0
-// and 2, then 1 and 3 (int8).  A byte on its own is a subnormal fp16 number, byte * 2^-24, so an int8 code takes no more
-// than being made unsigned and put in place; products start from what the bias of 128 makes of them (64 sequences of up to
-// 64K tokens: 617 us; with the bias taken off each pair of codes by a subtraction, 675).  e4m3 has an instruction (16 x
-// 64K: 198 us; its bits shifted into place, 263).
+// Four codes as two pairs of fp16, in units of kCode: coordinates 0 and 1, then 2 and 3 (e4m3), or 0 and 2, then 1 and 3
+// (int8).  A byte on its own is a subnormal fp16 number, byte * 2^-24, so an int8 code is made unsigned, put in place, and
+// the 128 taken off again: exactly, before the products, whose sums would otherwise carry 128 times the queries or the
+// weights through every step (64 sequences of up to 64K tokens 628 us; with products that start from -128 times these sums
+// 612, and errors two to four times as large, more where a block has wide channels).  e4m3 has an instruction (16 x 64K: 196
+// us; its bits shifted into place, 263).
 template <int KV>
 struct Wide {
-  static constexpr float kCode = KV == kKvInt8 ? 0x1p-24f : 1.f, kBias = KV == kKvInt8 ? 128.f : 0.f;
+  static constexpr float kCode = KV == kKvInt8 ? 0x1p-24f : 1.f;
   static __device__ __forceinline__ void pairs(uint32_t w, uint32_t& a, uint32_t& b) {
     if constexpr (KV == kKvInt8) {
-      const uint32_t x = w ^ 0x80808080u;
-      a = x & 0x00ff00ffu;
-      b = __byte_perm(x, 0u, 0x4341);
+      const uint32_t x = w ^ 0x80808080u, most = 0x00800080u;
+      const uint32_t lo = x & 0x00ff00ffu, hi = __byte_perm(x, 0u, 0x4341);
+      const __half2 bias = *reinterpret_cast<const __half2*>(&most);
+      a = as_u32(__hsub2(*reinterpret_cast<const __half2*>(&lo), bias));
+      b = as_u32(__hsub2(*reinterpret_cast<const __half2*>(&hi), bias));
     } else {
       const __half2_raw l = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w, __NV_E4M3);
       const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
@@ -199,7 +202,7 @@ struct Places {
 };
 
 template <int D, int KV, bool SPARSE>
-__device__ __forceinline__ void attend_pair(State<D>& st, const uint8_t* stage, const uint4 (*qf)[32], float qs, float2 qb,
+__device__ __forceinline__ void attend_pair(State<D>& st, const uint8_t* stage, const uint4 (*qf)[32], float qs,
                                             const Block8 (&blk)[kPair], const Places<D>& at, int lane) {
   constexpr int KS = D / 16, B8 = kBlock * D, HALF = 8 * D;  // steps; bytes of a block, and of eight of its tokens
   using Wd = Wide<KV>;
@@ -222,7 +225,7 @@ __device__ __forceinline__ void attend_pair(State<D>& st, const uint8_t* stage, 
         for (int t = 0; t < 2; ++t) {
           uint32_t b0, b1;
           Wd::pairs(y == 0 ? w[i][t].x : y == 1 ? w[i][t].y : y == 2 ? w[i][t].z : w[i][t].w, b0, b1);
-          if (x == 0 && y == 0) mma_f16_from(s[i][t], q.x, q.y, q.z, q.w, b0, b1, qb.x, qb.x, qb.y, qb.y);
+          if (x == 0 && y == 0) mma_f16_new(s[i][t], q.x, q.y, q.z, q.w, b0, b1);
           else mma_f16(s[i][t], q.x, q.y, q.z, q.w, b0, b1);
         }
     }
@@ -274,16 +277,7 @@ __device__ __forceinline__ void attend_pair(State<D>& st, const uint8_t* stage, 
     for (int e = 0; e < 4; ++e) p[e] = ex2(z[i][e] - low);
     split_f16(p[0], p[1], ph[0], pl[0]);
     split_f16(p[2], p[3], ph[1], pl[1]);
-    float sum = (p[0] + p[1]) + (p[2] + p[3]);
-    float2 from = make_float2(0.f, 0.f);  // what the products of heads 2c and 2c + 1 start from
-    if constexpr (Wd::kBias != 0.f) {
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      from.x = __shfl_sync(0xffffffffu, sum, 8 * c) * (-Wd::kBias * Wd::kCode);
-      from.y = __shfl_sync(0xffffffffu, sum, 8 * c + 4) * (-Wd::kBias * Wd::kCode);
-      sum = c == 0 ? sum : 0.f;
-    }
-    st.l += sum;  // this lane's part
+    st.l += (p[0] + p[1]) + (p[2] + p[3]);  // this lane's part
     float2 off = make_float2(0.f, 0.f);
     if constexpr (SPARSE) {
       const float fn = blk[i].vbar ? ex2(e2[i] - low) : 0.f;
@@ -327,7 +321,7 @@ __device__ __forceinline__ void attend_pair(State<D>& st, const uint8_t* stage, 
         Wd::pairs(__byte_perm(w[0][x], w[1][x], sel), a0, a1);
         Wd::pairs(__byte_perm(w[2][x], w[3][x], sel), a2, a3);
         float o[4];
-        mma_f16_from(o, a0, a1, a2, a3, ph[0], ph[1], from.x, from.y, from.x, from.y);
+        mma_f16_new(o, a0, a1, a2, a3, ph[0], ph[1]);
         mma_f16(o, a0, a1, a2, a3, pl[0], pl[1]);
         float2(&acc)[2] = st.acc[2 * x + y];
         acc[0] = __ffma2_rn(make_float2(o[0], o[1]), vs, acc[0]);
@@ -376,20 +370,6 @@ __device__ __forceinline__ void stage_query(Smem8<D, SPARSE>& sm, float4 x, int 
   split_f16(x.x * up, x.y * up, f.x, f.y);
   split_f16(x.z * up, x.w * up, f.z, f.w);
   if (lane < D / 4) sm.q[lane % KS][head * 4 + lane / KS] = f;
-  if constexpr (Wide<KV>::kBias != 0.f) {
-    // the bias times the sum of each part
-    float2 b[2];
-    const uint32_t part[2][2] = {{f.x, f.z}, {f.y, f.w}};
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&part[k][0]));
-      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&part[k][1]));
-      b[k].x = warp_sum((u.x + u.y) + (v.x + v.y)) * (-Wide<KV>::kBias * Wide<KV>::kCode);
-    }
-    if (lane == 0) sm.qb[head] = make_float2(b[0].x, b[1].x);
-  } else if (lane == 0) {
-    sm.qb[head] = make_float2(0.f, 0.f);
-  }
   const float root = D == 128 ? 0.08838834764831845f : 0.125f;
   if (lane == 0) sm.qs[head] = __uint_as_float((uint32_t)(e - 13 + 127) << 23) * (kLog2e * root);
 }
@@ -718,7 +698,6 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
     }
     const bool comp = SPARSE && !a.no_comp && sm.valid < n;
     const float qs = sm.qs[lane >> 2];
-    const float2 qb = sm.qb[lane >> 2];
     st.reset();
     for (int i = at + (warp - (at - lo) % W + W) % W; i < end; i += W) {
       Block8 blk[kPair];
@@ -738,7 +717,7 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
           blk[k].ks = blk[k].n ? sm.scale[warp][slot][k] : 0.f;
           blk[k].vs = blk[k].n ? sm.scale[warp][slot][kPair + k] * (kUnit / Wide<KV>::kCode) : 0.f;
         }
-        if (blk[0].n | blk[1].n) attend_pair<D, KV, SPARSE>(st, sm.ring[warp][slot], sm.q, qs, qb, blk, places, lane);
+        if (blk[0].n | blk[1].n) attend_pair<D, KV, SPARSE>(st, sm.ring[warp][slot], sm.q, qs, blk, places, lane);
         --flying;
         fill();
       }

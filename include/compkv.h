@@ -420,7 +420,9 @@ compkv_status compkv_read(compkv_ctx *ctx, int layer, const int *starts, const i
  * sequence holds, in a cache of 8 bits:
  *     out = sum_j e^(z_j) v_j / sum_j e^(z_j),   z_j = q . k_j / sqrt(d).
  * q and out: device [B][Hq][d], both of `type` (COMPKV_BF16 or COMPKV_F32).
- * Queries and softmax weights enter the products to 22 bits, sums are fp32.
+ * Queries and softmax weights enter the products to 2^-23 of themselves (as two
+ * fp16 parts; beside a head's largest coordinate to 2^-38 of that one), codes as
+ * they are; sums are fp32.
  * Logits, and a query's largest coordinate times a block's largest one, are
  * below 2^100 (so too in compkv_attend and compkv_decode on such a cache); a
  * value's magnitude times the sequence's tokens is below 2^137 (there: 2^127),

@@ -2,7 +2,8 @@
 import pytest
 import torch
 
-from test_gpu_kv8 import KV8, MOST, _built, check, check_stored, fill, make_cache, randn, selection, values, write  # noqa: F401
+from test_gpu_kv8 import (BLOCK, F32, KV8, MOST, _built, check, check_stored, fill, gen, make_cache, randn, selection,  # noqa: F401
+                          values, write)
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +91,63 @@ def test_values_near_the_least(kv):
     c.vscale.mul_(2.0 ** -80 / MOST[kv] / c.vscale.max())
     q = randn(6, 1, 4, 64)
     check(c, c.attend_all(0, q), 0, q, [40])
+
+
+# ------------------------------------------------------------------ channels of very different size
+@pytest.mark.parametrize("kv", KV8)
+@pytest.mark.parametrize("sparse", [False, True])
+def test_one_channel_far_wider_in_the_keys(kv, sparse):
+    # a channel that the queries do not look at takes the whole range of the codes; those that they look at, all with one
+    # sign, are codes of one unit
+    d, g, n = 128, 4, 64
+    c = make_cache([n], kv, hkv=1, g=g, d=d, budget=128)
+    fill(c, 1, [n], wide=False)
+    k = torch.randint(0, 2, c.k.shape, device="cuda", generator=gen(3)) * 2.0 - 1
+    k[..., 3] = 127.0
+    c.k.copy_(k.to(kv))
+    c.kscale.fill_(8.0)
+    q = randn(2, 1, g, d).abs()
+    q[..., 3] = 0
+    sel = torch.tensor([[[0, 1, 2, 3, -1, -1, -1, -1]]], dtype=torch.int32, device="cuda")
+    out = c.attend(0, q, sel) if sparse else c.attend_all(0, q)
+    kk, vv = values(c)
+    z = q[0].double() @ kk.view(n, d).T / d ** 0.5
+    p = torch.exp(z - z.amax(-1, keepdim=True))
+    want = p @ vv.view(n, d) / p.sum(-1, keepdim=True)
+    # Relative error of a weight: the two parts of a query's coordinate
+    # (2^-23), eight products in a row (2^-22 of the sum each, as they truncate), three factors and the distance from the
+    # reference (2^-24 each of up to |z| + 20 in log2 units, times log 2), the exponential and its two parts (2^-21); sums of
+    # 64 tokens, the block's products (three steps of 2^-22) and the join of up to 12 parts add 64 + 12 + 40 roundings.
+    size = 8 * q.sum(-1).max().item() / d ** 0.5
+    eps = (8 * 4 + 2) * F32 * size + 5 * F32 * (z.abs().max().item() + 20) + 8 * F32 + 116 * F32
+    tol = 2 * eps * (p @ vv.view(n, d).abs() / p.sum(-1, keepdim=True) + want.abs())
+    assert ((out[0].double() - want).abs() <= tol).all(), ((out[0].double() - want).abs() / tol).max()
+
+
+@pytest.mark.parametrize("kv", KV8)
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_channel_far_wider_in_the_values(kv, d):
+    # one block, logits of one product each, values of one unit beside a channel of the whole range
+    g, n = 4, 16
+    c = make_cache([n], kv, hkv=1, g=g, d=d)
+    fill(c, 1, [n], wide=False)
+    c.k.zero_()
+    c.k[0, :, 0] = torch.arange(-8, 8, device="cuda").to(kv)
+    c.kscale.fill_(0.25)
+    v = torch.randint(0, 2, (1, n, d), device="cuda", generator=gen(4)) * 2.0 - 1
+    v[..., 5] = 127.0
+    c.v.copy_(v.to(kv))
+    c.vscale.fill_(0.3)
+    q = torch.zeros(1, g, d, device="cuda")
+    q[0, :, 0] = torch.tensor([1.0, -1.7, 3.1, 0.3], device="cuda")
+    out = c.attend_all(0, q)
+    kk, vv = values(c)
+    z = q[0].double() @ kk[0].T / d ** 0.5
+    p = torch.exp(z - z.amax(-1, keepdim=True))
+    want = p @ vv[0] / p.sum(-1, keepdim=True)
+    # A logit (below 1) has five roundings of 2^-24; its distance from the reference, below 16 in log2 units, one of 2^-24
+    # of that; the exponential 2^-22, the weight's parts 2^-23; sums of 16 tokens 16 roundings, the block's products three
+    # truncations of 2^-22, joins and the division some 14 more.
+    eps = (5 + 16 + 4 + 2 + 16 + 12 + 14) * F32
+    tol = 2 * eps * (p @ vv[0].abs() / p.sum(-1, keepdim=True) + want.abs())
+    assert ((out[0].double() - want).abs() <= tol).all(), ((out[0].double() - want).abs() / tol).max()
