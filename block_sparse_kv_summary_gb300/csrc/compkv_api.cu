@@ -145,6 +145,7 @@ struct compkv_ctx {
   compkv_kv8 kv8;              // K and V in 8 bits (type COMPKV_BF16: they are not)
   CUtensorMap tmap8[4];        // the codes in boxes of 16 tokens (K, V) and of 32
   int kv_host = 0;             // K and V in page-locked host memory (no tensor maps)
+  int lost_stage = -1;         // Attend8Args::lost
   int64_t launches = 0;
   unsigned long long* trace = nullptr;
   int trace_cap = 0;
@@ -459,6 +460,7 @@ Attend8Args attend8_args(const compkv_ctx* c, int layer, const void* q, bool q_b
   a.G = c->cfg.group_size;
   a.d = c->cfg.head_dim;
   a.P = device_sms() < kMaxAttend8Ctas ? device_sms() : kMaxAttend8Ctas;
+  a.lost = c->lost_stage;
   a.layer_row0 = c->lay.rows_per_layer * (int64_t)layer;
   for (int s = 0; s < a.B; ++s) {
     a.seq_row0[s] = c->lay.seq_row0[s];
@@ -1234,6 +1236,10 @@ void compkv_destroy(compkv_ctx* c) { delete c; }
 compkv_status compkv_internal_fail(compkv_status st, const char* what, const char* detail) {
   return fail(st, "%s: %s", what, detail);
 }
+
+// From the next call on, the attention of a cache in 8 bits leaves out the copies of one stage (two blocks, in the order
+// of the kernel's row of stages; -1: of none), so that the wait for them runs out: for tests of what follows then.
+extern "C" void compkv_internal_lose_stage(compkv_ctx* c, int stage) { c->lost_stage = stage; }
 
 // Decode step with a scratch buffer supplied by the caller of this function
 // instead of by a context: used by the scratch-free entry point

@@ -594,6 +594,7 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
         y_issue = (int)((a.layer_row0 + row_issue) * kBlock);
       }
       const int j = to_issue - unit_first;
+      const bool made = to_issue != a.lost;
       to_issue += W;
       if (j >= stages_issue) continue;  // behind a unit's last stage
       uint64_t* bar = &sm.full[warp][issue_slot];
@@ -621,7 +622,7 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
           for (int i = 0; i < kPair; ++i) {
             const int b = i ? b1 : b0;
             sm.block[warp][issue_slot][i] = b;
-            if (b < 0) continue;
+            if (b < 0 || !made) continue;
             tma_2d(dst + i * B8, a.k16, 0, y_issue + b * kBlock, bar, pol);
             tma_2d(dst + (kPair + i) * B8, a.v16, 0, y_issue + b * kBlock, bar, pol);
             bulk_g2s(sm.vbar[warp][issue_slot][i], a.vbar + (row_issue + b) * D, D * 4, bar);
@@ -629,8 +630,10 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
         } else {
           // (a pair's second block may be another unit's, or lie behind the cache, which reads as zero: it is masked)
           mbar_arrive_expect_tx(bar, Smem::kStage);
-          tma_2d(dst, a.k32, 0, y_issue + b0 * kBlock, bar, pol);
-          tma_2d(dst + kPair * B8, a.v32, 0, y_issue + b0 * kBlock, bar, pol);
+          if (made) {
+            tma_2d(dst, a.k32, 0, y_issue + b0 * kBlock, bar, pol);
+            tma_2d(dst + kPair * B8, a.v32, 0, y_issue + b0 * kBlock, bar, pol);
+          }
         }
       }
       ++flying;
@@ -699,7 +702,9 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
     const bool comp = SPARSE && !a.no_comp && sm.valid < n;
     const float qs = sm.qs[lane >> 2];
     st.reset();
-    for (int i = at + (warp - (at - lo) % W + W) % W; i < end; i += W) {
+    // (a warp whose wait ran out reads no further stage: its ring is not filled again, and the block numbers there are those
+    // of other stages)
+    for (int i = at + (warp - (at - lo) % W + W) % W; ok && i < end; i += W) {
       Block8 blk[kPair];
       if (SPARSE) __syncwarp();  // the slot's block numbers are there
 #pragma unroll
@@ -710,7 +715,7 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
         blk[k].zb = comp && b >= 0 && lane >> 2 < a.G ? __ldcg(a.zs + (row0 + b) * pad_g(a.G) + (lane >> 2)) : 0.f;
         blk[k].vbar = comp && b >= 0 ? sm.vbar[SPARSE ? warp : 0][slot][k] : nullptr;
       }
-      ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&sm.full[warp][slot], phase, a.status, s, h, 71));
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm.full[warp][slot], phase, a.status, s, h, 71));
       if (ok) {
 #pragma unroll
         for (int k = 0; k < kPair; ++k) {

@@ -1,6 +1,11 @@
 """K and V in 8 bits at the edges of what the calls promise."""
+import ctypes
+
 import pytest
 import torch
+
+from block_sparse_kv_summary_gb300 import compkv as C
+from block_sparse_kv_summary_gb300 import lib
 
 from test_gpu_kv8 import (BLOCK, F32, KV8, MOST, _built, check, check_stored, fill, gen, make_cache, randn, selection,  # noqa: F401
                           values, write)
@@ -151,3 +156,64 @@ def test_one_channel_far_wider_in_the_values(kv, d):
     eps = (5 + 16 + 4 + 2 + 16 + 12 + 14) * F32
     tol = 2 * eps * (p @ vv[0].abs() / p.sum(-1, keepdim=True) + want.abs())
     assert ((out[0].double() - want).abs() <= tol).all(), ((out[0].double() - want).abs() / tol).max()
+
+
+# ------------------------------------------------------------------ a wait that runs out
+def stages_of(lens, hkv, warps, sel_blocks=None):
+    """(unit of every stage, stages of a run): the attention's row of stages, where it is not a short one."""
+    units = []
+    for s, n in enumerate(lens):
+        blocks = (n + BLOCK - 1) // BLOCK
+        st = ((blocks if sel_blocks is None else min(blocks, sel_blocks)) + 1) // 2
+        units += [(s, h) for h in range(hkv) for _ in range(st)]
+    ctas = min(160, torch.cuda.get_device_properties(0).multi_processor_count)
+    return units, (len(units) + ctas - 1) // ctas
+
+
+def lose(c, stage):
+    lib().compkv_internal_lose_stage(ctypes.c_void_p(c.ctx), stage)
+
+
+@pytest.mark.parametrize("kv", KV8)
+def test_a_copy_that_never_comes_is_reported(kv):
+    # long and short sequences in turn, several heads a run: behind the stage that never comes, its warp's ring still names
+    # blocks that the next, shorter sequence does not have.  The call ends, says so, and every unit that has nothing of that
+    # warp's stages is what it is anyway; so is everything in the next call.
+    hkv, warps, lens = 32, 8, [128, 1] * 32
+    c = make_cache([max(BLOCK, n) for n in lens], kv, hkv=hkv, g=1, d=128, budget=128)
+    fill(c, 1, lens)
+    q = randn(2, len(lens), hkv, 128)
+    sel = selection(3, c, lens, 8)
+    units, per = stages_of(lens, hkv, warps, 8)
+    assert per > 2 * warps  # (then every run has `per` stages)
+    run = next(r for r in range(len(units) // per) if units[r * per][0] % 2 == 0 and units[(r + 1) * per - 1][0] != units[r * per][0])
+    mine = [units[i] for i in range(run * per, (run + 1) * per, warps)]
+    assert len(mine) > 3 and mine[0][0] % 2 == 0 and mine[-1][0] == mine[0][0] + 1
+    want = c.attend(0, q, sel)
+    lose(c, run * per)
+    out = c.attend(0, q, sel)
+    lose(c, -1)
+    assert c.device_status() == 5 and "sequence %d, head %d, site 71" % mine[0] in C.compkv_last_error()
+    other = torch.ones(len(lens), hkv, dtype=torch.bool, device="cuda")
+    for s, h in mine:
+        other[s, h] = False
+    assert torch.equal(out[other], want[other])
+    assert torch.equal(c.attend(0, q, sel), want) and c.device_status() == 0
+
+
+@pytest.mark.parametrize("kv", KV8)
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_copy_that_never_comes_in_a_dense_call(kv, d):
+    # one unit over many CTAs: the parts of all of them are still joined and the counters end at zero
+    c = make_cache([4096, 64], kv, hkv=2, g=4, d=d)
+    fill(c, 1, [4000, 50])
+    q = randn(2, 2, 8, d)
+    want = c.attend_all(0, q)
+    lose(c, 40)
+    out = c.attend_all(0, q)
+    lose(c, -1)
+    assert c.device_status() == 5 and "sequence 0, head 0" in C.compkv_last_error()
+    assert torch.equal(out[0, 4:], want[0, 4:]) and torch.equal(out[1], want[1])
+    for _ in range(2):
+        assert torch.equal(c.attend_all(0, q), want)
+    assert c.device_status() == 0
