@@ -39,8 +39,8 @@
 // between their copy and the product.
 //
 // Bound by DRAM for long rows, with the instructions that widen the codes close
-// behind: 64 sequences of up to 64K tokens of 8 heads, d 128 (4.4 GB of codes), 628
-// us, 7.0 TB/s; one of 128K 49 us, of which 5 pass before the first stage is there
+// behind: 64 sequences of up to 64K tokens of 8 heads, d 128 (4.4 GB of codes), 624
+// us, 7.1 TB/s; one of 128K 49 us, of which 5 pass before the first stage is there
 // and 8 between the first and the last CTA's end (some multiprocessors get a tenth
 // less of the memory's rate) and in the join; 1025 tokens of 2 heads 7 us.  Twelve
 // warps of two stages: where these took 617 us on the 64 sequences, eight of three
@@ -129,7 +129,7 @@ __device__ __forceinline__ void split_f16(float x, float y, uint32_t& hi, uint32
 // Four codes as two pairs of fp16, in units of kCode: coordinates 0 and 1, then 2 and 3 (e4m3), or 0 and 2, then 1 and 3
 // (int8).  A byte on its own is a subnormal fp16 number, byte * 2^-24, so an int8 code is made unsigned, put in place, and
 // the 128 taken off again: exactly, before the products, whose sums would otherwise carry 128 times the queries or the
-// weights through every step (64 sequences of up to 64K tokens 628 us; with products that start from -128 times these sums
+// weights through every step (64 sequences of up to 64K tokens 624 us; with products that start from -128 times these sums
 // 612, and errors two to four times as large, more where a block has wide channels).  e4m3 has an instruction (16 x 64K: 196
 // us; its bits shifted into place, 263).
 template <int KV>

@@ -354,7 +354,9 @@ compkv_status compkv_attend_shared(compkv_ctx *ctx, int layer, const void *q, in
                                    void *stream);
 
 /* ---------------------------------------------------------------------------
- * K and V in 8 bits: half the memory of a token and half the bytes of a read.
+ * K and V in 8 bits: half the bytes of K and V, and of a read of them; the fp32
+ * summaries stay (d 128, r 4: 322 bytes a token and KV head for 577 in bf16), and
+ * the tail below takes 24 KB a sequence and KV head of d 128.
  * The CompKV page has no counterpart to these calls either.
  *
  * A row's K, and its V, are 16 x d codes c and one fp32 scale: the block's
@@ -385,7 +387,8 @@ compkv_status compkv_attend_shared(compkv_ctx *ctx, int layer, const void *q, in
  * compkv_decode_host, compkv_read and compkv_attend_all; compkv_prefill,
  * compkv_fork, compkv_compact, compkv_attend_shared and compkv_trace give
  * COMPKV_ERR_UNSUPPORTED_SHAPE, and compkv_profile_enable(2) times its calls
- * as 1 does.
+ * as 1 does.  compkv_decode_host reads the selection back from a page-locked
+ * sel_host, which the attention takes it from.
  * ------------------------------------------------------------------------- */
 typedef struct {
   int type;                     /* COMPKV_INT8 or COMPKV_E4M3                        */
