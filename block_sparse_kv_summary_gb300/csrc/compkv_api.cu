@@ -1237,8 +1237,8 @@ compkv_status compkv_internal_fail(compkv_status st, const char* what, const cha
   return fail(st, "%s: %s", what, detail);
 }
 
-// From the next call on, the attention of a cache in 8 bits leaves out the copies of one stage (two blocks, in the order
-// of the kernel's row of stages; -1: of none), so that the wait for them runs out: for tests of what follows then.
+// From the next call on, the attention of a cache in 8 bits waits in one stage (two blocks, in the order of the kernel's row
+// of stages; -1: in none) for more than its copies bring, so that the wait runs out: for tests of what follows then.
 extern "C" void compkv_internal_lose_stage(compkv_ctx* c, int stage) { c->lost_stage = stage; }
 
 // Decode step with a scratch buffer supplied by the caller of this function

@@ -168,7 +168,7 @@ struct Attend8Args {
   int q_bf16;
   int B, Hkv, G, d;
   int P;                       // CTAs
-  int lost;                    // a stage whose copies are announced and not made, for the tests of a wait that runs out (-1)
+  int lost;                    // a stage that announces more than its copies bring, for the tests of a wait that runs out (-1)
   int64_t layer_row0;          // first row of this layer in the whole cache (tensor-map coordinates)
   int64_t seq_row0[kMaxBatch];
   int cap_blocks[kMaxBatch];

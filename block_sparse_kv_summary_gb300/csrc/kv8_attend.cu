@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
         y_issue = (int)((a.layer_row0 + row_issue) * kBlock);
       }
       const int j = to_issue - unit_first;
-      const bool made = to_issue != a.lost;
+      const uint32_t missing = to_issue == a.lost ? 16 : 0;  // (tests: more is announced than comes)
       to_issue += W;
       if (j >= stages_issue) continue;  // behind a unit's last stage
       uint64_t* bar = &sm.full[warp][issue_slot];
@@ -617,23 +617,21 @@ __global__ void __launch_bounds__(Smem8<D, SPARSE>::kThreads, 1) attend8_kernel(
       }
       if (lane == 0) {
         if constexpr (SPARSE) {
-          mbar_arrive_expect_tx(bar, ((b0 >= 0) + (b1 >= 0)) * (2 * B8 + D * 4));
+          mbar_arrive_expect_tx(bar, ((b0 >= 0) + (b1 >= 0)) * (2 * B8 + D * 4) + missing);
 #pragma unroll
           for (int i = 0; i < kPair; ++i) {
             const int b = i ? b1 : b0;
             sm.block[warp][issue_slot][i] = b;
-            if (b < 0 || !made) continue;
+            if (b < 0) continue;
             tma_2d(dst + i * B8, a.k16, 0, y_issue + b * kBlock, bar, pol);
             tma_2d(dst + (kPair + i) * B8, a.v16, 0, y_issue + b * kBlock, bar, pol);
             bulk_g2s(sm.vbar[warp][issue_slot][i], a.vbar + (row_issue + b) * D, D * 4, bar);
           }
         } else {
           // (a pair's second block may be another unit's, or lie behind the cache, which reads as zero: it is masked)
-          mbar_arrive_expect_tx(bar, Smem::kStage);
-          if (made) {
-            tma_2d(dst, a.k32, 0, y_issue + b0 * kBlock, bar, pol);
-            tma_2d(dst + kPair * B8, a.v32, 0, y_issue + b0 * kBlock, bar, pol);
-          }
+          mbar_arrive_expect_tx(bar, Smem::kStage + missing);
+          tma_2d(dst, a.k32, 0, y_issue + b0 * kBlock, bar, pol);
+          tma_2d(dst + kPair * B8, a.v32, 0, y_issue + b0 * kBlock, bar, pol);
         }
       }
       ++flying;
